@@ -22,8 +22,9 @@ import torch
 __all__ = ["prefill", "prefill_varlen", "prefill_varlen_pool", "decode_step",
            "decode_placement", "decode_tokens", "decode_commit", "workspace_bytes",
            "prefill_fused", "prefill_varlen_fused", "decode_tokens_fused",
-           "fused_workspace_bytes", "backward", "backward_varlen", "version", "GdrError",
-           "lib_path",
+           "fused_workspace_bytes", "backward", "backward_varlen",
+           "cache_append", "attention_decode", "attention_workspace_bytes", "cache_evict",
+           "version", "GdrError", "lib_path",
            "FA", "SWA", "GDN", "KDA"]
 
 FA, SWA, GDN, KDA = 0, 1, 2, 3
@@ -99,6 +100,17 @@ def _load():
     lib.gdr_backward_chunked_varlen.restype = I
     lib.gdr_backward_chunked_varlen.argtypes = [I, I, I, I, I, I, I, I, F, P, P, P, P, P, P,
                                                 P, P, P, P, P, P, P, P, P, P, P, Z, P]
+    # include/gdr_cache.h
+    lib.gdr_cache_append.restype = I
+    lib.gdr_cache_append.argtypes = [I, I, I, I, I, I, P, P, P, P, P, P, I, I, I, P, P, P, P]
+    lib.gdr_attention_workspace_bytes.restype = Z
+    lib.gdr_attention_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
+    lib.gdr_attention_decode.restype = I
+    lib.gdr_attention_decode.argtypes = [I, I, I, I, I, I, F, I, P, P, P, P, P, I, I, I, P, P, P,
+                                         P, Z, P]
+    lib.gdr_cache_evict.restype = I
+    lib.gdr_cache_evict.argtypes = [I, I, I, I, I, I, I, P, P, P, P, P, I, P, P, I, I, I, P, P,
+                                    P, P]
     _lib = lib
     return lib
 
@@ -634,3 +646,8 @@ def backward_varlen(q, k, v, g, beta, do, cu_seqlens, h0=None, dht=None, scale: 
         _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(do), _ptr(dht), _ptr(dq), _ptr(dk),
         _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0), _ptr(workspace), nbytes, _stream(dev)))
     return dq, dk, dv, dg, dbeta, dh0
+
+
+# the paged key-value cache of the attention layers (include/gdr_cache.h)
+from .cache import (attention_decode, attention_workspace_bytes, cache_append,  # noqa: E402
+                    cache_evict)

@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdr.so")
-SOURCES = ["api.hip", "recurrent.hip", "chunked.hip", "chunked_chain.hip", "backward.hip"]
+SOURCES = ["api.hip", "recurrent.hip", "chunked.hip", "chunked_chain.hip", "backward.hip",
+           "cache_api.hip", "attention.hip", "cache.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",

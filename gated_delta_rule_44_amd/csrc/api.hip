@@ -10,11 +10,12 @@
 #include <mutex>
 
 #include "../../include/gdr.h"
+#include "api_util.h"
 #include "gdr_internal.h"
 
-namespace {
+namespace gdr {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 gdr_status fail(gdr_status code, const char *fmt, ...) {
     va_list ap;
@@ -24,7 +25,7 @@ gdr_status fail(gdr_status code, const char *fmt, ...) {
     return code;
 }
 
-bool debug_sync() {
+static bool debug_sync() {
     static const int on = [] {
         const char *e = getenv("GDR_DEBUG");
         return (e && e[0] && e[0] != '0') ? 1 : 0;
@@ -44,7 +45,23 @@ gdr_status finish(hipError_t launch, hipStream_t s, const char *what) {
     return GDR_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+gdr_status check_workspace(const char *what, const void *ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return GDR_OK;
+    if (!ws || ws_bytes < need)
+        return fail(GDR_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, need,
+                    ws ? ws_bytes : (size_t)0);
+    if (!aligned16(ws)) return fail(GDR_EINVAL, "%s: workspace is not 16-byte aligned", what);
+    return GDR_OK;
+}
+
+}  // namespace gdr
+
+namespace {
+
+using gdr::aligned16;
+using gdr::check_workspace;
+using gdr::fail;
+using gdr::finish;
 
 // (sequence, head) pairs of one prefill call: the prefill kernels launch up
 // to four workgroups per pair, rounded up to eight pairs, in a 31-bit grid
@@ -62,19 +79,6 @@ gdr_status check_common(int dt, int gk, int Dk, int Dv, const char *what) {
     return GDR_OK;
 }
 
-#define REQUIRE_PTR(p, name)                                                        \
-    do {                                                                            \
-        if (!(p)) return fail(GDR_EINVAL, "%s: %s is NULL", what, name);            \
-        if (!aligned16(p)) return fail(GDR_EINVAL, "%s: %s is not 16-byte aligned", \
-                                       what, name);                                 \
-    } while (0)
-#define REQUIRE_ALIGNED_OR_NULL(p, name)                                            \
-    do {                                                                            \
-        if ((p) && !aligned16(p)) return fail(GDR_EINVAL,                           \
-                                              "%s: %s is not 16-byte aligned",      \
-                                              what, name);                          \
-    } while (0)
-
 gdr_status check_prefill_ptrs(const char *what, const void *q, const void *k, const void *v,
                               const void *g, const void *beta, const float *h0,
                               const void *o, const float *ht, long long tokens) {
@@ -88,15 +92,6 @@ gdr_status check_prefill_ptrs(const char *what, const void *q, const void *k, co
     }
     REQUIRE_ALIGNED_OR_NULL(h0, "h0");
     REQUIRE_ALIGNED_OR_NULL(ht, "ht");
-    return GDR_OK;
-}
-
-gdr_status check_workspace(const char *what, const void *ws, size_t ws_bytes, size_t need) {
-    if (need == 0) return GDR_OK;
-    if (!ws || ws_bytes < need)
-        return fail(GDR_EINVAL, "%s: workspace of %zu bytes needed, %zu given", what, need,
-                    ws ? ws_bytes : (size_t)0);
-    if (!aligned16(ws)) return fail(GDR_EINVAL, "%s: workspace is not 16-byte aligned", what);
     return GDR_OK;
 }
 
@@ -155,7 +150,7 @@ gdr_status check_gate_scale(const char *what, float c) {
 
 extern "C" {
 
-const char *gdr_last_error(void) { return g_err; }
+const char *gdr_last_error(void) { return gdr::g_err; }
 
 const char *gdr_version(void) { return "gdr 0.1.0 (gfx950)"; }
 
