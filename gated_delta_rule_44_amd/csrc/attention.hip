@@ -641,16 +641,25 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
     }
 }
 
-// (m, l) of one row over a sequence's slots; `stride` parts between slots.
+// (m, l) of one row over a sequence's slots, `stride` parts apart, by one
+// wave: lanes take slots in turn.
 __device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, int count) {
+    const int lane = threadIdx.x & 63;
     float top = -INFINITY, l = 0.f;
-    for (int i = 0; i < count; ++i) top = fmaxf(top, ml[part + i * stride].x);
-    top = finite_top(top);
-    for (int i = 0; i < count; ++i) {
+    for (int i = lane; i < count; i += 64) {
         const float2 x = ml[part + i * stride];
-        l += x.y * exp2_(x.x - top);
+        const float mn = fmaxf(top, x.x), ms = finite_top(mn);
+        l = l * exp2_(top - ms) + x.y * exp2_(x.x - ms);
+        top = mn;
     }
-    return float2{top, l};
+    float all = top;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) all = fmaxf(all, __shfl_xor(all, m));
+    all = finite_top(all);
+    l *= exp2_(top - all);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m);
+    return float2{all, l};
 }
 
 // Joins the slots' parts, one workgroup per query row (the first `joins`
@@ -678,6 +687,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
         const float2 tot = join_ml(k.ml, part, stride, sc.y);
         const int d = 4 * (tid % kAcross), grp = tid / kAcross;
         f32x4 y{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int i = grp; i < sc.y; i += kGroups) {
             const float f = exp2_(k.ml[part + i * stride].x - tot.x);
             const f32x4 x = *reinterpret_cast<const f32x4 *>(k.po + (part + i * stride) * D + d);
@@ -698,6 +708,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
     }
     constexpr int kRows = 64, kTokens = 4 * kThreads;
     __shared__ float2 st[kRows];
+    const int w = tid >> 6;
     const long long per = (k.cap32 + kTokens - 1) / kTokens;
     const long long all = (long long)a.B * a.Hkv * per;
     for (long long blk = blockIdx.x - joins; blk < all; blk += score_blocks) {
@@ -710,19 +721,20 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
         const int j = base + 4 * tid;
         f32x4 sum{0.f, 0.f, 0.f, 0.f};
         for (int r0 = 0; r0 < rows; r0 += kRows) {
+            const int nr = rows - r0 < kRows ? rows - r0 : kRows;
             __syncthreads();
-            if (tid < kRows && r0 + tid < rows) {
-                const int row = r0 + tid;
+            for (int r = w; r < nr; r += kWaves) {
+                const int row = r0 + r;
                 const size_t part = (size_t)sc.x * stride +
                                     ((size_t)h * k.plan.row_blocks + row / (16 * R)) * 16 * R +
                                     row % (16 * R);
                 const float2 x = join_ml(k.ml, part, stride, sc.y);
-                st[tid] = float2{x.x, x.y == 0.f ? 0.f : 1.f / x.y};
+                if ((tid & 63) == 0) st[r] = float2{x.x, x.y == 0.f ? 0.f : 1.f / x.y};
             }
             __syncthreads();
-            const int nr = rows - r0 < kRows ? rows - r0 : kRows;
             if (j < len) {
                 const float *x = k.logits + (((size_t)b * a.Hkv + h) * rows + r0) * k.cap32 + j;
+#pragma unroll 4
                 for (int r = 0; r < nr; ++r) {
                     const Span sp = token_span(len, a.n, a.window, (r0 + r) / a.G);
                     const f32x4 v = *reinterpret_cast<const f32x4 *>(x + r * k.cap32);
