@@ -14,7 +14,7 @@
 // n G rows that read the same K and V: 16 R rows are one workgroup's, so
 // that a token is read from HBM once for all of them, as MFMA operands.
 // Bytes bound the kernel: 2 D elements a token against 4 D flops per row and
-// token is at most 16 R flops a byte, where the card turns at about 300.
+// token is at most 16 R flops a byte, where the card turns at about 250.
 #include "cache_internal.h"
 #include "gdr_internal.h"
 #include "device_util.h"
@@ -22,7 +22,7 @@
 namespace gdr {
 namespace {
 
-constexpr int kWaves = 4;                  // waves of a workgroup: each takes every fourth tile
+constexpr int kWaves = 4;                  // waves of a workgroup
 constexpr int kThreads = 64 * kWaves;
 
 // First and one past the last token that query token t of a sequence of len
@@ -62,11 +62,10 @@ Plan make_plan(int B, int n, int G, int Hkv, int R, long long capacity) {
     p.max_slots = (int)(by_len < bound ? (by_len < B ? B : by_len) : bound);
     return p;
 }
-// Rows of a workgroup's block, in tiles of 16: as many as there are, up to
-// four (two for fp32, whose operands take twice the registers).
-int row_tiles(bool bf16_io, long long rows) {
-    return rows <= 16 ? 1 : rows <= 32 || !bf16_io ? 2 : 4;
-}
+// Rows of a workgroup's block, in tiles of 16, one per wave: the four waves
+// are R tiles of rows x 4 / R shares of the tokens.  Waves of one share read
+// the same K and V, from HBM once and then from the CU's L1.
+int row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 // Workspace: {first slot, slots} of every sequence; (m, l) of every slot, unit
 // and row; o of the same, unnormalised; with scores, the logits x of every row and
@@ -370,21 +369,21 @@ template <int D> struct Tile<float, D> {
     }
 };
 
-// Workgroup = (slot, key-value head, row block); its four waves take the
-// slot's tiles in turn, each with m, l and o of its own, joined through LDS
-// at the end.  K and V go from HBM straight into the registers that MFMA
+// Workgroup = (slot, key-value head, row block).  Wave w has row tile w % R
+// and takes every 4 / R-th tile of tokens, with m, l and o of its own, joined
+// through LDS at the end.  K and V go from HBM straight into the registers that MFMA
 // reads: the next tile's K is requested as soon as this one's logits are
 // formed, its V after this one's product.
 template <typename T, int D, int R>
-__global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k) {
+__global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D>;
     constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = 16 * kBlocks;
-    constexpr int kPad = D + 4;
-    __shared__ float sm[kWaves][16 * R], sl[kWaves][16 * R];
+    constexpr int kPad = D + 4, kShares = kWaves / R;
+    __shared__ float sm[kWaves][16], sl[kWaves][16];
     __shared__ __align__(16) float so[kWaves][16][kPad];
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, lg = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), rt = w % R, share = w / R;
     // the row blocks of one (slot, head) follow each other on one XCD, which
     // holds their K and V in its L2 (workgroups go to the eight XCDs in turn)
     const int wg = blockIdx.x;
@@ -398,21 +397,16 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
     const Span seq = seq_span(len, a.n, a.window);
     if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
 
-    // this lane's query rows and what they attend to
-    const int rows = a.n * a.G, row0 = rb * 16 * R;
-    constexpr unsigned esz = sizeof(T);
-    Span sp[R];
-    typename TL::Q q[R];
+    // this lane's query row and what it attends to
+    const int rows = a.n * a.G, row0 = rb * 16 * R, row = row0 + 16 * rt + r16;
+    Span sp{0, 0};
+    typename TL::Q q;
     {
         const size_t qb = (size_t)b * a.n * a.Hq * D;
         const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + qb, 0xFFFFFFFFu);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = row0 + 16 * i + r16;
-            const int t = row < rows ? row / a.G : 0, g = row < rows ? row % a.G : 0;
-            sp[i] = row < rows ? token_span(len, a.n, a.window, t) : Span{0, 0};
-            TL::load_q(q[i], rq, (unsigned)(t * a.Hq + h * a.G + g) * (D * esz), lane);
-        }
+        const int t = row < rows ? row / a.G : 0, g = row < rows ? row % a.G : 0;
+        if (row < rows) sp = token_span(len, a.n, a.window, t);
+        TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + g) * (D * (unsigned)sizeof(T)), lane);
     }
     // the block's tokens: what its rows attend to, within the slot
     const int t_first = row0 / a.G;
@@ -424,25 +418,20 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
     const int k_lo = first.lo > c_lo ? first.lo : c_lo, k_hi = last.hi < c_hi ? last.hi : c_hi;
     // every row attends to the tokens of [all_lo, all_hi)
     const int all_lo = last.lo, all_hi = first.hi;
-    const int tile0 = k_lo / kTile + w;
-    const int tiles = k_hi > k_lo ? ((k_hi + kTile - 1) / kTile - tile0 + kWaves - 1) / kWaves : 0;
+    const int tile0 = k_lo / kTile + share;
+    const int tiles = k_hi > k_lo ? ((k_hi + kTile - 1) / kTile - tile0 + kShares - 1) / kShares : 0;
 
     const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
     const float c1 = a.scale * kLog2e;
-    float m[R], l[R];
-    f32x4 acc[R][PER];
+    float m = -INFINITY, l = 0.f;
+    f32x4 acc[PER];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int c = 0; c < PER; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // pages of this wave's next 64 tiles, one tile per lane
     int pg[kBlocks];
     auto load_pages = [&](int i0) {
-        const int j = (tile0 + kWaves * (i0 + lane)) * kTile;
+        const int j = (tile0 + kShares * (i0 + lane)) * kTile;
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
             pg[blk] = i0 + lane < tiles && j + 16 * blk < len ? page_of(a.map, b, j + 16 * blk) : -1;
@@ -453,7 +442,7 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
     struct Src { size_t at; unsigned bytes; };
     auto block_src = [&](int i, int blk) {
         const int page = __builtin_amdgcn_readlane(pg[blk], i & 63);
-        const int j = (tile0 + kWaves * i) * kTile + 16 * blk;
+        const int j = (tile0 + kShares * i) * kTile + 16 * blk;
         Src s;
         s.at = ((size_t)page * a.Hkv + h) * page_bytes + (size_t)slot_of(a.map, j) * TL::kRowBytes;
         const int valid = len - j < 16 ? len - j : 16;
@@ -477,12 +466,10 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
         TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
 
     for (int i = 0; i < tiles; ++i) {
-        const int j0 = (tile0 + kWaves * i) * kTile;
-        f32x4 x[R][kBlocks];
+        const int j0 = (tile0 + kShares * i) * kTile;
+        f32x4 x[kBlocks];
 #pragma unroll
-        for (int rt = 0; rt < R; ++rt)
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) x[rt][blk] = TL::logits(kf, blk, q[rt]);
+        for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
         const bool full = present && j0 >= all_lo && j0 + kTile <= all_hi;
         bool here[kBlocks];
 #pragma unroll
@@ -496,146 +483,125 @@ __global__ __launch_bounds__(kThreads, R == 1 ? 2 : 1) void attn_kernel(KArgs k)
             present &= src[blk].bytes != 0;
             TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
         }
-        typename TL::P p[R];
+        float top = -INFINITY;
 #pragma unroll
-        for (int rt = 0; rt < R; ++rt) {
-            float top = -INFINITY;
+        for (int blk = 0; blk < kBlocks; ++blk) {
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[rt][blk][e] *= c1;
-                if (k.logits) {
-                    const int row = row0 + 16 * rt + r16;
-                    if (row < rows)
-                        *reinterpret_cast<f32x4 *>(
-                            k.logits + (((size_t)b * a.Hkv + h) * rows + row) * k.cap32 + j0 +
-                            16 * blk + 4 * lg) = x[rt][blk];
-                }
-                if (!full) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + 16 * blk + 4 * lg + e;
-                        const bool in = here[blk] && j >= sp[rt].lo && j < sp[rt].hi;
-                        x[rt][blk][e] = in ? x[rt][blk][e] : -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, x[rt][blk][e]);
-            }
-            top = swap_max32(swap_max16(top));
-            const float mn = fmaxf(m[rt], top);
-            const float ms = finite_top(mn);
-            if (__builtin_amdgcn_ballot_w64(mn != m[rt])) {
-                const float al = exp2_(m[rt] - ms);
-                l[rt] *= al;
-#pragma unroll
-                for (int c = 0; c < PER; ++c) acc[rt][c] *= al;
-                m[rt] = mn;
-            }
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk)
+            for (int e = 0; e < 4; ++e) x[blk][e] *= c1;
+            if (k.logits && row < rows)
+                *reinterpret_cast<f32x4 *>(k.logits +
+                                           (((size_t)b * a.Hkv + h) * rows + row) * k.cap32 + j0 +
+                                           16 * blk + 4 * lg) = x[blk];
+            if (!full) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[rt][blk][e] = exp2_(x[rt][blk][e] - ms);
-                    l[rt] += x[rt][blk][e];
+                    const int j = j0 + 16 * blk + 4 * lg + e;
+                    x[blk][e] = here[blk] && j >= sp.lo && j < sp.hi ? x[blk][e] : -INFINITY;
                 }
-            p[rt] = TL::weights(x[rt]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, x[blk][e]);
         }
+        const float mn = fmaxf(m, swap_max32(swap_max16(top))), ms = finite_top(mn);
+        if (__builtin_amdgcn_ballot_w64(mn != m)) {
+            const float al = exp2_(m - ms);
+            l *= al;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) acc[c] *= al;
+            m = mn;
+        }
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[blk][e] = exp2_(x[blk][e] - ms);
+                l += x[blk][e];
+            }
+        const typename TL::P p = TL::weights(x);
         // Where a tile is attended to by some rows only, a weight of zero must
         // not meet an infinity or NaN.  Such values are taken out of V, and a
         // row that attends to one gets +inf, -inf or (both, or NaN) their
         // sum in that channel.
         if (!full && __builtin_amdgcn_ballot_w64(TL::odd(vf))) {
+            f32x4 in[kBlocks];
 #pragma unroll
-            for (int rt = 0; rt < R; ++rt) {
-                f32x4 in[kBlocks];
+            for (int blk = 0; blk < kBlocks; ++blk)
 #pragma unroll
-                for (int blk = 0; blk < kBlocks; ++blk)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + 16 * blk + 4 * lg + e;
-                        in[blk][e] = j >= sp[rt].lo && j < sp[rt].hi ? 1.f : 0.f;
-                    }
-                const typename TL::P ones = TL::weights(in);
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const f32x4 up = TL::count_odd(vf, c, TL::kMinusInf, ones);
-                    const f32x4 down = TL::count_odd(vf, c, TL::kPlusInf, ones);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[rt][c][e] += (up[e] > 0.f ? INFINITY : 0.f) +
-                                         (down[e] > 0.f ? -INFINITY : 0.f);
-                    __builtin_amdgcn_sched_barrier(0);   // a rare path: few registers
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + 16 * blk + 4 * lg + e;
+                    in[blk][e] = j >= sp.lo && j < sp.hi ? 1.f : 0.f;
                 }
+            const typename TL::P ones = TL::weights(in);
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const f32x4 up = TL::count_odd(vf, c, TL::kMinusInf, ones);
+                const f32x4 down = TL::count_odd(vf, c, TL::kPlusInf, ones);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[c][e] += (up[e] > 0.f ? INFINITY : 0.f) + (down[e] > 0.f ? -INFINITY : 0.f);
+                __builtin_amdgcn_sched_barrier(0);   // a rare path: few registers
             }
             TL::clear_odd(vf);
         }
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
-#pragma unroll
-            for (int rt = 0; rt < R; ++rt) acc[rt][c] = TL::pv(vf, c, p[rt], acc[rt][c]);
+        for (int c = 0; c < PER; ++c) acc[c] = TL::pv(vf, c, p, acc[c]);
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
             TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
     }
 
-    // join the waves: every wave's o in units of the common maximum, summed
-    // row by row
-#pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        const float lt = swap_sum32(swap_sum16(l[rt]));
-        if (lg == 0) {
-            sm[w][16 * rt + r16] = m[rt];
-            sl[w][16 * rt + r16] = lt;
-        }
+    // join the waves of a row tile: every wave's o in units of their common
+    // maximum, summed row by row
+    l = swap_sum32(swap_sum16(l));
+    if (lg == 0) {
+        sm[w][r16] = m;
+        sl[w][r16] = l;
     }
     __syncthreads();
+    float top = -INFINITY;
 #pragma unroll
-    for (int rt = 0; rt < R; ++rt) {
-        float top = -INFINITY;
+    for (int i = 0; i < kShares; ++i) top = fmaxf(top, sm[rt + R * i][r16]);
+    const float f = exp2_(m - finite_top(top));
+    // acc[c][e] is channel dim(c, 4 lg + e); four at a time
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sm[i][16 * rt + r16]);
-        const float f = exp2_(m[rt] - finite_top(top));
-        if (rt > 0) __syncthreads();
-        // acc[c][e] is channel dim(c, 4 lg + e); four at a time
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int c = 0; c < PER; c += 4)
+            *reinterpret_cast<f32x4 *>(&so[w][r16][TL::dim(c, 4 * lg + e)]) =
+                f32x4{acc[c][e] * f, acc[c + 1][e] * f, acc[c + 2][e] * f, acc[c + 3][e] * f};
+    __syncthreads();
+    // 16 threads per row, four channels at a time
 #pragma unroll
-            for (int c = 0; c < PER; c += 4)
-                *reinterpret_cast<f32x4 *>(&so[w][r16][TL::dim(c, 4 * lg + e)]) =
-                    f32x4{acc[rt][c][e] * f, acc[rt][c + 1][e] * f, acc[rt][c + 2][e] * f,
-                          acc[rt][c + 3][e] * f};
-        __syncthreads();
-        // 16 threads per row, four channels at a time
-        const int lr = tid >> 4, row = row0 + 16 * rt + lr;
-        if (row < rows) {
-            float rtop = -INFINITY, rl = 0.f;
+    for (int i = 0; i < R; ++i) {
+        const int lr = tid >> 4, orow = row0 + 16 * i + lr;
+        if (orow >= rows) break;
+        float rtop = -INFINITY, rl = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) rtop = fmaxf(rtop, sm[i][16 * rt + lr]);
+        for (int x = 0; x < kShares; ++x) rtop = fmaxf(rtop, sm[i + R * x][lr]);
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i)
-                rl += sl[i][16 * rt + lr] * exp2_(sm[i][16 * rt + lr] - finite_top(rtop));
-            const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * 16 * R +
-                                16 * rt + lr;
-            const bool alone = sl_.count == 1;
-            if ((!alone || k.logits) && (tid & 15) == 0) k.ml[part] = float2{rtop, rl};
-            const float inv = rl == 0.f ? 0.f : 1.f / rl;
-            const int t = row / a.G, g = row % a.G;
-            T *o = static_cast<T *>(a.o) + (((size_t)b * a.n + t) * a.Hq + h * a.G + g) * D;
+        for (int x = 0; x < kShares; ++x)
+            rl += sl[i + R * x][lr] * exp2_(sm[i + R * x][lr] - finite_top(rtop));
+        const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * 16 * R +
+                            16 * i + lr;
+        const bool alone = sl_.count == 1;
+        if ((!alone || k.logits) && (tid & 15) == 0) k.ml[part] = float2{rtop, rl};
+        const float inv = 1.f / rl;
+        const int t = orow / a.G, g = orow % a.G;
+        T *o = static_cast<T *>(a.o) + (((size_t)b * a.n + t) * a.Hq + h * a.G + g) * D;
 #pragma unroll
-            for (int u = 0; u < D / 64; ++u) {
-                const int d = 64 * u + 4 * (tid & 15);
-                f32x4 y = *reinterpret_cast<const f32x4 *>(&so[0][lr][d]);
+        for (int u = 0; u < D / 64; ++u) {
+            const int d = 64 * u + 4 * (tid & 15);
+            f32x4 y = *reinterpret_cast<const f32x4 *>(&so[i][lr][d]);
 #pragma unroll
-                for (int i = 1; i < kWaves; ++i) y += *reinterpret_cast<const f32x4 *>(&so[i][lr][d]);
-                if (!alone) {
-                    *reinterpret_cast<f32x4 *>(k.po + part * D + d) = y;
-                } else {
+            for (int x = 1; x < kShares; ++x)
+                y += *reinterpret_cast<const f32x4 *>(&so[i + R * x][lr][d]);
+            if (!alone) {
+                *reinterpret_cast<f32x4 *>(k.po + part * D + d) = y;
+            } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = rl == 0.f ? 0.f : y[e] * inv;
-                    if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(o + d) = cvt4(y);
-                    else                          *reinterpret_cast<f32x4 *>(o + d) = y;
-                }
+                for (int e = 0; e < 4; ++e) y[e] = rl == 0.f ? 0.f : y[e] * inv;
+                if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(o + d) = cvt4(y);
+                else                          *reinterpret_cast<f32x4 *>(o + d) = y;
             }
         }
     }
@@ -785,12 +751,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t launch_r(const AttnArgs &a, hipStream_t s) {
-    switch (row_tiles(sizeof(T) == 2, (long long)a.n * a.G)) {
+    switch (row_tiles((long long)a.n * a.G)) {
     case 1:  return launch<T, D, 1>(a, s);
     case 2:  return launch<T, D, 2>(a, s);
-    default:
-        if constexpr (sizeof(T) == 2) return launch<T, D, 4>(a, s);
-        else                          return launch<T, D, 2>(a, s);
+    default: return launch<T, D, 4>(a, s);
     }
 }
 
@@ -799,11 +763,7 @@ hipError_t launch_r(const AttnArgs &a, hipStream_t s) {
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
                            bool with_scores) {
     const int G = Hq / Hkv;
-    const long long rows = (long long)n * G;
-    // one size for both dtypes
-    const size_t x = ws_map(B, n, G, Hkv, D, row_tiles(true, rows), capacity, with_scores).total;
-    const size_t y = ws_map(B, n, G, Hkv, D, row_tiles(false, rows), capacity, with_scores).total;
-    return x > y ? x : y;
+    return ws_map(B, n, G, Hkv, D, row_tiles((long long)n * G), capacity, with_scores).total;
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
