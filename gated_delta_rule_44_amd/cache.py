@@ -14,30 +14,60 @@ import ctypes
 
 import torch
 
-from . import GdrError, _BF16, _F32, _check, _dense, _host_i32, _load, _need, _workspace
+from . import (GdrError, _BF16, _F32, _check, _dense, _host_i32, _load, _need,
+               _workspace)
+
+_Tensor, _INT32, _FLOAT32 = torch.Tensor, torch.int32, torch.float32
+_DTYPES = {torch.bfloat16: _BF16, torch.float32: _F32}
+# the current stream's handle, without a torch.cuda.Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _i32(name, t, shape, dev):
-    _dense(name, t, torch.int32, dev)
-    _need(t.shape == shape, "%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+# A decode step is microseconds of GPU work, so the checks cost as little as
+# they can: one test per tensor, and a message only for one that fails.
+def _gpu(name, t, dtype, dev):
+    if not (isinstance(t, _Tensor) and t.is_cuda and t.dtype == dtype and t.device == dev
+            and t.is_contiguous()):
+        _dense(name, t, dtype, dev)
 
 
-def _cache(k_cache, v_cache, scores, dtype=None):
-    """Checks of the caches and their scores; returns P, Hkv, page, D."""
-    _dense("k_cache", k_cache, dtype)
-    _need(k_cache.dim() == 4 and k_cache.shape[1] >= 1, "k_cache must be [P,Hkv,page,D]")
-    _dense("v_cache", v_cache, k_cache.dtype, k_cache.device)
-    _need(v_cache.shape == k_cache.shape, "k_cache, v_cache shapes differ")
+def _shape(name, t, shape):
+    if t.shape != shape:
+        raise GdrError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _cache(k_cache, v_cache, scores):
+    """Checks of the caches and their scores; returns their device, dtype
+    code and P, Hkv, page, D."""
+    if not isinstance(k_cache, _Tensor) or not k_cache.is_cuda:
+        _dense("k_cache", k_cache)
+    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise GdrError("the cache must be bfloat16 or float32, got %s" % dtype)
+    if len(shape) != 4 or shape[1] < 1:
+        raise GdrError("k_cache must be [P,Hkv,page,D], got %s" % list(shape))
+    _gpu("k_cache", k_cache, dtype, dev)
+    _gpu("v_cache", v_cache, dtype, dev)
+    _shape("v_cache", v_cache, shape)
     if scores is not None:
-        _dense("scores", scores, torch.float32, k_cache.device)
-        _need(scores.shape == k_cache.shape[:3], "scores must be [P,Hkv,page]")
-    return k_cache.shape
+        _gpu("scores", scores, _FLOAT32, dev)
+        _shape("scores", scores, shape[:3])
+    return dev, dt, shape
+
+
+def _int(name, x, lo):
+    """A C int (ctypes would keep the low 32 bits of a larger one)."""
+    if not lo <= x < 1 << 31:
+        raise GdrError("%s = %r is outside %d..2^31-1" % (name, x, lo))
 
 
 def _table(name, t, B, dev):
-    _dense(name, t, torch.int32, dev)
-    _need(t.dim() == 2 and t.shape[0] == B, "%s must be [B,max_pages]" % name)
-    return t.shape[1]
+    _gpu(name, t, _INT32, dev)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise GdrError("%s must be [B,max_pages] with B = %d, got %s" % (name, B, list(shape)))
+    return shape[1]
 
 
 def _host_table(name, x, shape):
@@ -47,14 +77,6 @@ def _host_table(name, x, shape):
     a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
     _need(a.shape == shape, "%s must be %s" % (name, list(shape)))
     return a
-
-
-def _dt(t):
-    if t.dtype == torch.bfloat16:
-        return _BF16
-    if t.dtype == torch.float32:
-        return _F32
-    raise GdrError("the cache must be bfloat16 or float32, got %s" % t.dtype)
 
 
 def _p(t):
@@ -67,12 +89,14 @@ def _hp(a):
 
 def _call(dev, fn, *args):
     """fn(*args, stream): the current stream of dev, with dev current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, stream))
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+            rc = fn(*args, _raw_stream(i))
+    if rc:
+        _check(rc)
 
 
 def cache_append(k, v, start, page_table, k_cache, v_cache, scores=None, cu_seqlens=None,
@@ -86,29 +110,30 @@ def cache_append(k, v, start, page_table, k_cache, v_cache, scores=None, cu_seql
     Positions outside the table or on an absent page are left out.  scores,
     when given, are set to 0 at every position written.
     """
-    P, Hkv, page, D = _cache(k_cache, v_cache, scores)
-    dev = k_cache.device
-    _dense("k", k, k_cache.dtype, dev)
-    _dense("v", v, k_cache.dtype, dev)
-    _need(k.shape == v.shape, "k, v shapes differ")
-    host = None
+    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("k", k, k_cache.dtype, dev)
+    _gpu("v", v, k_cache.dtype, dev)
+    shape, host = k.shape, None
+    _shape("v", v, shape)
     if cu_seqlens is None:
-        _need(k.dim() == 4 and k.shape[2:] == (Hkv, D), "k must be [B,n,Hkv,D]")
-        B, n = k.shape[:2]
+        _need(len(shape) == 4 and shape[2:] == (Hkv, D), "k must be [B,n,Hkv,D]")
+        B, n = shape[0], shape[1]
         T = B * n
         _need(cu_seqlens_host is None, "cu_seqlens_host given without cu_seqlens")
     else:
-        _need(k.dim() == 3 and k.shape[1:] == (Hkv, D), "k must be [T_tot,Hkv,D]")
-        _dense("cu_seqlens", cu_seqlens, torch.int32, dev)
+        _need(len(shape) == 3 and shape[1:] == (Hkv, D), "k must be [T_tot,Hkv,D]")
+        _gpu("cu_seqlens", cu_seqlens, _INT32, dev)
         _need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 1, "cu_seqlens must be [B+1]")
-        B, n, T = cu_seqlens.numel() - 1, 0, k.shape[0]
-        host = None if cu_seqlens_host is None else _host_i32(cu_seqlens_host, B + 1,
-                                                               "cu_seqlens_host")
-    _i32("start", start, (B,), dev)
+        B, n, T = cu_seqlens.numel() - 1, 0, shape[0]
+        if cu_seqlens_host is not None:
+            host = _host_i32(cu_seqlens_host, B + 1, "cu_seqlens_host")
+    _int("the number of tokens", T, 0)
+    _gpu("start", start, _INT32, dev)
+    _shape("start", start, (B,))
     M = _table("page_table", page_table, B, dev)
-    _call(dev, _load().gdr_cache_append, _dt(k_cache), B, n, T, Hkv, D, _p(k), _p(v),
-          _p(cu_seqlens), _hp(host), _p(start), _p(page_table), M, page, P, _p(k_cache),
-          _p(v_cache), _p(scores))
+    _call(dev, _load().gdr_cache_append, dt, B, n, T, Hkv, D, k.data_ptr(), v.data_ptr(),
+          _p(cu_seqlens), _hp(host), start.data_ptr(), page_table.data_ptr(), M, page, P,
+          k_cache.data_ptr(), v_cache.data_ptr(), _p(scores))
 
 
 def attention_workspace_bytes(batch: int, n_tok: int, heads: int, kv_heads: int, dim: int,
@@ -133,27 +158,33 @@ def attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, wind
     to one sequence; page_table_host, a host copy, makes the library validate
     that).  A row that attends to nothing gives zeros.  Returns o [B,n,Hq,D].
     """
-    P, Hkv, page, D = _cache(k_cache, v_cache, scores)
-    dev = k_cache.device
-    _dense("q", q, k_cache.dtype, dev)
-    _need(q.dim() == 4 and q.shape[3] == D, "q must be [B,n,Hq,D]")
-    B, n, Hq, _ = q.shape
-    _need(Hq >= 1 and Hq % Hkv == 0, "Hq (%d) must be a multiple of Hkv (%d)" % (Hq, Hkv))
-    _i32("seq_lens", seq_lens, (B,), dev)
+    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("q", q, k_cache.dtype, dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise GdrError("q must be [B,n,Hq,D] with D = %d, got %s" % (D, list(shape)))
+    B, n, Hq, _ = shape
+    if Hq < 1 or Hq % Hkv:
+        raise GdrError("Hq (%d) must be a multiple of Hkv (%d)" % (Hq, Hkv))
+    _gpu("seq_lens", seq_lens, _INT32, dev)
+    _shape("seq_lens", seq_lens, (B,))
     M = _table("page_table", page_table, B, dev)
     host = _host_table("page_table_host", page_table_host, (B, M))
     if o is None:
         o = torch.empty_like(q)
     else:
-        _dense("o", o, q.dtype, dev)
-        _need(o.shape == q.shape, "o must be [B,n,Hq,D]")
+        _gpu("o", o, k_cache.dtype, dev)
+        _shape("o", o, shape)
+    _int("window", window, 0)
     lib = _load()
-    nbytes = lib.gdr_attention_workspace_bytes(B, n, Hq, Hkv, D, M, page, int(scores is not None))
-    workspace = _workspace(workspace, nbytes, dev)
-    _call(dev, lib.gdr_attention_decode, _dt(k_cache), B, n, Hq, Hkv, D,
-          D ** -0.5 if scale is None else float(scale), int(window), _p(q), _p(k_cache),
-          _p(v_cache), _p(page_table), _hp(host), M, page, P, _p(seq_lens), _p(scores), _p(o),
-          _p(workspace), nbytes)
+    nbytes = lib.gdr_attention_workspace_bytes(B, n, Hq, Hkv, D, M, page, scores is not None)
+    workspace = _workspace(workspace, nbytes, dev) if workspace is None or not (
+        isinstance(workspace, _Tensor) and workspace.device == dev and workspace.is_contiguous()
+        and workspace.nbytes >= nbytes) else workspace
+    _call(dev, lib.gdr_attention_decode, dt, B, n, Hq, Hkv, D,
+          D ** -0.5 if scale is None else scale, window, q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), page_table.data_ptr(), _hp(host), M, page, P, seq_lens.data_ptr(),
+          _p(scores), o.data_ptr(), workspace.data_ptr(), nbytes)
     return o
 
 
@@ -172,12 +203,13 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     make the library validate them.
     """
     _need(scores is not None, "scores are required")
-    P, Hkv, page, D = _cache(k_cache, v_cache, scores)
-    dev = k_cache.device
-    _dense("seq_lens", seq_lens, torch.int32, dev)
+    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("seq_lens", seq_lens, _INT32, dev)
     _need(seq_lens.dim() == 1, "seq_lens must be [B]")
-    B, budget = seq_lens.shape[0], int(budget)
-    _need(budget >= 1, "budget must be at least 1")
+    B = seq_lens.shape[0]
+    _int("budget", budget, 1)
+    _int("recent", recent, 0)
+    _int("sink", sink, 0)
     M = _table("page_table", page_table, B, dev)
     host = _host_table("page_table_host", page_table_host, (B, M))
     M2, host2 = 0, None
@@ -189,12 +221,15 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
     else:
-        _i32("new_lens", new_lens, (B,), dev)
+        _gpu("new_lens", new_lens, _INT32, dev)
+        _shape("new_lens", new_lens, (B,))
     if kept is None:
-        kept = torch.empty((B, Hkv, budget), device=dev, dtype=torch.int32)
+        kept = torch.empty((B, Hkv, budget), device=dev, dtype=_INT32)
     else:
-        _i32("kept", kept, (B, Hkv, budget), dev)
-    _call(dev, _load().gdr_cache_evict, _dt(k_cache), B, Hkv, D, budget, int(recent), int(sink),
-          _p(k_cache), _p(v_cache), _p(scores), _p(page_table), _hp(host), M,
-          _p(new_page_table), _hp(host2), M2, page, P, _p(seq_lens), _p(new_lens), _p(kept))
+        _gpu("kept", kept, _INT32, dev)
+        _shape("kept", kept, (B, Hkv, budget))
+    _call(dev, _load().gdr_cache_evict, dt, B, Hkv, D, budget, recent, sink, k_cache.data_ptr(),
+          v_cache.data_ptr(), scores.data_ptr(), page_table.data_ptr(), _hp(host), M,
+          _p(new_page_table), _hp(host2), M2, page, P, seq_lens.data_ptr(), new_lens.data_ptr(),
+          kept.data_ptr())
     return new_lens, kept

@@ -128,6 +128,8 @@ struct Slot { int b, first, count, chunk; };      // sequence, its first slot, i
 // The sequence that slot s belongs to (b = -1: past the last slot).  Thread
 // i of the workgroup looks after sequences i per .. i per + per - 1.
 __device__ inline Slot find_slot(const KArgs &k, int s) {
+    // too short a table for a second slot: slot and sequence are one
+    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 30};
     __shared__ long long lds64[kWaves];
     __shared__ int lds32[kWaves], found[3];
     const AttnArgs &a = k.a;
@@ -428,13 +430,15 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // pages of this wave's next 64 tiles, one tile per lane
+    // pages of this wave's next 64 tiles, one tile per lane (of the table's
+    // entries past the length too, which block_src leaves out)
+    const int cap = a.map.max_pages << a.map.page_shift;
     int pg[kBlocks];
     auto load_pages = [&](int i0) {
         const int j = (tile0 + kShares * (i0 + lane)) * kTile;
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
-            pg[blk] = i0 + lane < tiles && j + 16 * blk < len ? page_of(a.map, b, j + 16 * blk) : -1;
+            pg[blk] = j + 16 * blk < cap ? page_of(a.map, b, j + 16 * blk) : -1;
     };
     // the cache rows of block blk of tile i (none past the length, on an
     // absent page or past the last tile: such loads give zeros)
@@ -446,8 +450,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         Src s;
         s.at = ((size_t)page * a.Hkv + h) * page_bytes + (size_t)slot_of(a.map, j) * TL::kRowBytes;
         const int valid = len - j < 16 ? len - j : 16;
-        s.bytes = page >= 0 && i < tiles ? (unsigned)(valid * TL::kRowBytes) : 0u;
-        if (page < 0) s.at = 0;
+        const bool some = page >= 0 && i < tiles && valid > 0;
+        s.bytes = some ? (unsigned)(valid * TL::kRowBytes) : 0u;
+        if (!some) s.at = 0;
         return s;
     };
     typename TL::K kf;

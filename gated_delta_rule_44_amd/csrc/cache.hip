@@ -49,40 +49,27 @@ __device__ inline unsigned key_of(float x) {
     const unsigned u = __builtin_bit_cast(unsigned, x == 0.f ? 0.f : x);
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
-__device__ inline unsigned key_at(const EvictArgs &a, int b, int h, int j) {
-    const int page = page_of(a.map, b, j);
-    return page < 0 ? 0u : key_of(a.scores[cache_row(a.map, a.Hkv, page, h, slot_of(a.map, j))]);
-}
 
-constexpr int kSelThreads = 1024;
+// Which tokens a (sequence, head) keeps: one workgroup per pair, which holds
+// the keys of up to kHeld tokens in registers, read once: four adjacent
+// tokens per thread and round.  The m-th largest key of the tokens between
+// sink and recent is found digit by digit: 8 bits a step, from the top, by a
+// histogram of the keys that share the digits found so far, which ends when
+// a digit's keys are all wanted.  The kept tokens' places then follow from
+// counts over the waves in the tokens' order.  (Longer sequences go through
+// the same steps with their keys read anew, kHeld at a time.)
+constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+constexpr int kRounds = 8, kPerRound = 4 * kSelThreads, kHeld = kRounds * kPerRound;
+// Neighbouring scores share their top bits, so that one histogram's counter
+// would be hit by most lanes of a wave at once: kCopies of it, in different
+// LDS banks, taken by the lanes in turn.
+constexpr int kCopies = 16, kCopyStride = 257;
 
-// Sum of x over the workgroup's threads before this one, and over all.
-__device__ inline int block_scan(int x, int &total, int *lds) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int incl = x;
-    for (int m = 1; m < 64; m <<= 1) {
-        const int y = __shfl_up(incl, m);
-        if (lane >= m) incl += y;
-    }
-    if (lane == 63) lds[w] = incl;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int i = 0; i < kSelThreads / 64; ++i) {
-        const int v = lds[i];
-        before += i < w ? v : 0;
-        total += v;
-    }
-    __syncthreads();
-    return before + incl - x;
-}
+typedef unsigned keys4 __attribute__((ext_vector_type(4)));
 
-// Which tokens a (sequence, head) keeps: one workgroup per pair.  The m-th
-// largest key of the tokens between sink and recent is found digit by digit
-// (8 bits, from the top, by histograms of the keys that share the digits
-// found so far); a last pass in the tokens' order writes the kept ones.
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
+    const int lane = tid & 63, w = tid >> 6;
     const int len = cached_len(a.seq_lens, b, a.map);
     int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
     if (len <= a.budget) {
@@ -90,90 +77,243 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         return;
     }
     const int lo = a.sink, hi = len - a.recent;
-    int want = a.budget - a.sink - a.recent;       // of hi - lo > want tokens
-    __shared__ int hist[256], found[2], scan[kSelThreads / 64];
+    __shared__ int hist[kCopies * kCopyStride], waves[4], found[3];
+    __shared__ int2 counts[kRounds][kSelWaves];
+
+    // keys of tokens j .. j + 3 (one page holds all four)
+    auto load4 = [&](int j) {
+        keys4 k{0, 0, 0, 0};
+        if (j < len) {
+            const int page = page_of(a.map, b, j);
+            if (page >= 0) {
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    a.scores + cache_row(a.map, a.Hkv, page, h, slot_of(a.map, j)));
+                k = keys4{key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w)};
+            }
+        }
+        return k;
+    };
+    keys4 key[kRounds];
+    auto load_held = [&](int base) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (base + r * kPerRound < len) key[r] = load4(base + r * kPerRound + 4 * tid);
+            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // addresses of four rounds at once
+        }
+    };
+    const bool once = len <= kHeld;
+    load_held(0);
+
+    int want = a.budget - a.sink - a.recent;       // of the hi - lo > want tokens between
     unsigned prefix = 0;                           // digits of the threshold found so far
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    const bool none = want == 0;
+    for (int shift = 24; shift >= 0 && !none; shift -= 8) {
+        for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
         __syncthreads();
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            const unsigned k = key_at(a, b, h, j);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(k >> shift) & 255], 1);
+        for (int base = 0; base < len; base += kHeld) {
+            if (!once) load_held(base);
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                if (base + r * kPerRound >= len) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = base + r * kPerRound + 4 * tid + e;
+                    const unsigned k = key[r][e];
+                    if (j >= lo && j < hi && (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0))
+                        atomicAdd(&hist[(lane & (kCopies - 1)) * kCopyStride + ((k >> shift) & 255)], 1);
+                }
+            }
         }
         __syncthreads();
-        if (tid == 0) {
-            int d = 255, left = want;
-            while (hist[d] < left) left -= hist[d--];
-            found[0] = d;
-            found[1] = left;
+        // thread t < 256 has digit 255 - t: how many keys have it, and how
+        // many have it or a larger one
+        int count = 0, incl = 0;
+        if (tid < 256) {
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) count += hist[c * kCopyStride + 255 - tid];
+            incl = count;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const int y = __shfl_up(incl, m);
+                if (lane >= m) incl += y;
+            }
+            if (lane == 63) waves[w] = incl;
+        }
+        __syncthreads();
+        if (tid < 256) {
+            for (int i = 0; i < w; ++i) incl += waves[i];
+            if (incl >= want && incl - count < want) {      // one thread: the threshold's digit
+                found[0] = 255 - tid;
+                found[1] = want - (incl - count);
+                found[2] = count;
+            }
         }
         __syncthreads();
         prefix |= (unsigned)found[0] << shift;
         want = found[1];                           // wanted among the keys with this prefix
-        __syncthreads();
+        if (want == found[2]) break;               // all of them: prefix 00.. is a threshold
     }
     // every key above prefix is kept, and the first `want` keys equal to it
-    const bool none = a.budget == a.sink + a.recent;
-    int above = 0, equal = 0;                      // kept, and equal keys, before this chunk
-    for (int base = 0; base < len; base += kSelThreads) {
-        const int j = base + tid;
-        int keep = 0, eq = 0;
-        if (j < len) {
-            if (j < lo || j >= hi) {
-                keep = 1;
-            } else if (!none) {
-                const unsigned k = key_at(a, b, h, j);
-                keep = k > prefix;
-                eq = k == prefix;
+    // (all keys that share its digits, where the search ended early)
+    int above = 0, equal = 0;                      // kept, and equal keys, before base
+    for (int base = 0; base < len; base += kHeld) {
+        if (!once) load_held(base);
+        auto flags = [&](int r, int e, bool &keep, bool &eq) {
+            const int j = base + r * kPerRound + 4 * tid + e;
+            const bool mid = j >= lo && j < hi;
+            keep = j < len && (!mid || (!none && key[r][e] > prefix));
+            eq = mid && !none && key[r][e] == prefix;
+        };
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (base + r * kPerRound >= len) break;
+            int2 c{0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bool keep, eq;
+                flags(r, e, keep, eq);
+                c.x += __popcll(__ballot(keep));
+                c.y += __popcll(__ballot(eq));
+            }
+            if (lane == 0) counts[r][w] = c;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (base + r * kPerRound >= len) break;
+            // lane i of the first kSelWaves: wave i's counts
+            int2 c = lane < kSelWaves ? counts[r][lane] : int2{0, 0}, t = c;
+#pragma unroll
+            for (int m = 1; m < kSelWaves; m <<= 1) {
+                const int x = __shfl_up(t.x, m), y = __shfl_up(t.y, m);
+                if (lane >= m) { t.x += x; t.y += y; }
+            }
+            int nk = above + __shfl(t.x - c.x, w), ne = equal + __shfl(t.y - c.y, w);
+            above += __shfl(t.x, kSelWaves - 1);
+            equal += __shfl(t.y, kSelWaves - 1);
+            // before this lane's four tokens
+            bool keep[4], eq[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                flags(r, e, keep[e], eq[e]);
+                const unsigned long long bk = __ballot(keep[e]), be = __ballot(eq[e]);
+                const unsigned long long below = (1ull << lane) - 1;
+                nk += __popcll(bk & below);
+                ne += __popcll(be & below);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (keep[e] || (eq[e] && ne < want))
+                    kept[nk + (ne < want ? ne : want)] = base + r * kPerRound + 4 * tid + e;
+                nk += keep[e];
+                ne += eq[e];
             }
         }
-        int tot_k, tot_e;
-        const int bk = block_scan(keep, tot_k, scan), be = block_scan(eq, tot_e, scan);
-        const int e = equal + be;
-        if (keep || (eq && e < want)) kept[above + bk + (e < want ? e : want)] = j;
-        above += tot_k;
-        equal += tot_e;
     }
 }
 
-// Rows kept[b, h, i] -> i, one workgroup per (sequence, head) and 16 bytes
-// of the rows.  In place, a tile of rows is read, then written: kept[i] >= i
-// and kept ascends, so a tile's writes lie below everything the later tiles
-// read.
-__global__ __launch_bounds__(256) void move_kernel(EvictArgs a, int lpr_shift) {
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, c = blockIdx.y, tid = threadIdx.x;
+// The places of row i of the new order and of the row it comes from, as rows
+// of the caches; false where it is not moved.
+__device__ inline bool row_move(const EvictArgs &a, int b, int h, int i, int j, size_t &src,
+                                size_t &dst) {
+    const int from = page_of(a.map, b, j), to = page_of(a.to, b, i);
+    src = cache_row(a.map, a.Hkv, from, h, slot_of(a.map, j));
+    dst = cache_row(a.to, a.Hkv, to, h, slot_of(a.to, i));
+    return from >= 0 && to >= 0;
+}
+constexpr int kMoveRows = 4;       // rows of a thread, their loads in flight together
+
+// Rows kept[b, h, i] -> i into other pages: 16 bytes of K and of V per
+// thread and row, every row on its own.
+__global__ __launch_bounds__(256) void copy_rows_kernel(EvictArgs a, int lpr_shift) {
+    const int pair = blockIdx.x, b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x;
     const int len = cached_len(a.seq_lens, b, a.map);
     const int m = len < a.budget ? len : a.budget;
-    const int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
+    if (blockIdx.y == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
+    const int c = tid & ((1 << lpr_shift) - 1), rows = 256 >> lpr_shift;
+    const int32_t *kept = a.kept + (size_t)pair * a.budget;
     u32x4 *kc = static_cast<u32x4 *>(a.k_cache), *vc = static_cast<u32x4 *>(a.v_cache);
-    for (int base = 0; base < m; base += 256) {
-        const int i = base + tid;
-        u32x4 x, y;
-        float sc = 0.f;
-        size_t dst = 0;
-        bool move = false;
-        if (i < m) {
-            const int j = kept[i];
-            const int from = page_of(a.map, b, j), to = page_of(a.to, b, i);
-            move = from >= 0 && to >= 0 && !(a.in_place && i == j);
-            if (move) {
-                const size_t src = cache_row(a.map, a.Hkv, from, h, slot_of(a.map, j));
-                dst = cache_row(a.to, a.Hkv, to, h, slot_of(a.to, i));
-                x = kc[(src << lpr_shift) + c];
-                y = vc[(src << lpr_shift) + c];
-                if (c == 0) sc = a.scores[src];
+    for (int base = blockIdx.y * rows * kMoveRows; base < m; base += gridDim.y * rows * kMoveRows) {
+        size_t src[kMoveRows], dst[kMoveRows];
+        bool move[kMoveRows];
+        u32x4 x[kMoveRows], y[kMoveRows];
+        float sc[kMoveRows];
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u) {
+            const int i = base + rows * u + (tid >> lpr_shift);
+            move[u] = i < m && row_move(a, b, h, i, kept[i < m ? i : 0], src[u], dst[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u)
+            if (move[u]) {
+                x[u] = kc[(src[u] << lpr_shift) + c];
+                y[u] = vc[(src[u] << lpr_shift) + c];
+                if (c == 0) sc[u] = a.scores[src[u]];
             }
-        }
-        __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): the tile is read ...
-        __syncthreads();                      // ... by every wave before any writes
-        if (move) {
-            kc[(dst << lpr_shift) + c] = x;
-            vc[(dst << lpr_shift) + c] = y;
-            if (c == 0) a.scores[dst] = sc;
-        }
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u)
+            if (move[u]) {
+                kc[(dst[u] << lpr_shift) + c] = x[u];
+                vc[(dst[u] << lpr_shift) + c] = y[u];
+                if (c == 0) a.scores[dst[u]] = sc[u];
+            }
     }
-    if (h == 0 && c == 0 && tid == 0) a.new_lens[b] = m;
+}
+
+// The same in place: a workgroup has 64 bytes of the rows of one (sequence,
+// head), of K (even blockIdx.y) or V, and goes through the rows in order, a
+// tile of them read, then written.  kept[i] >= i and kept ascends, so that a
+// tile's writes lie at or below its own reads and below all later ones, and
+// the next tile can be read before this one is written.
+__global__ __launch_bounds__(256) void close_up_kernel(EvictArgs a, int lpr_shift) {
+    constexpr int kRows = 64 * kMoveRows;
+    const int pair = blockIdx.x, b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x;
+    const int slice = blockIdx.y >> 1, c = 4 * slice + (tid & 3);
+    const int len = cached_len(a.seq_lens, b, a.map);
+    const int m = len < a.budget ? len : a.budget;
+    // (new_lens may be seq_lens: what another workgroup has written gives the
+    // same m)
+    if (blockIdx.y == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
+    const int32_t *kept = a.kept + (size_t)pair * a.budget;
+    u32x4 *cache = static_cast<u32x4 *>(blockIdx.y & 1 ? a.v_cache : a.k_cache);
+    const bool scores = blockIdx.y == 0 && (tid & 3) == 0;
+    struct Tile {
+        size_t dst[kMoveRows];
+        bool move[kMoveRows];
+        u32x4 x[kMoveRows];
+        float sc[kMoveRows];
+    };
+    auto load = [&](int base, Tile &t) {
+        size_t src[kMoveRows];
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u) {
+            const int i = base + 64 * u + (tid >> 2), j = i < m ? kept[i] : i;
+            t.move[u] = i != j && row_move(a, b, h, i, j, src[u], t.dst[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u)
+            if (t.move[u]) {
+                t.x[u] = cache[(src[u] << lpr_shift) + c];
+                if (scores) t.sc[u] = a.scores[src[u]];
+            }
+    };
+    Tile t;
+    load(0, t);
+    for (int base = 0; base < m; base += kRows) {
+        // the tile is read (vmcnt(0)) by every wave before any of it is written
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        __syncthreads();
+        Tile next;
+        load(base + kRows, next);
+#pragma unroll
+        for (int u = 0; u < kMoveRows; ++u)
+            if (t.move[u]) {
+                cache[(t.dst[u] << lpr_shift) + c] = t.x[u];
+                if (scores) a.scores[t.dst[u]] = t.sc[u];
+            }
+        t = next;
+    }
 }
 
 int lpr_shift_of(int row_bytes) { return row_bytes == 128 ? 3 : row_bytes == 256 ? 4 : 5; }
@@ -189,8 +329,19 @@ hipError_t launch_cache_append(int row_bytes, const AppendArgs &a, hipStream_t s
 
 hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s) {
     const int sh = lpr_shift_of(row_bytes);
-    select_kernel<<<a.B * a.Hkv, kSelThreads, 0, s>>>(a);
-    move_kernel<<<dim3(a.B * a.Hkv, 1 << sh), 256, 0, s>>>(a, sh);
+    const int pairs = a.B * a.Hkv;
+    select_kernel<<<pairs, kSelThreads, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.in_place) {
+        close_up_kernel<<<dim3(pairs, 2 << (sh - 2)), 256, 0, s>>>(a, sh);
+    } else {
+        const int cap = a.map.max_pages << a.map.page_shift;
+        const int most = a.budget < cap ? a.budget : cap, tile = (256 >> sh) * kMoveRows;
+        int tiles = (most + tile - 1) / tile;
+        tiles = tiles < 1 ? 1 : (tiles > 16384 ? 16384 : tiles);
+        copy_rows_kernel<<<dim3(pairs, tiles), 256, 0, s>>>(a, sh);
+    }
     return hipGetLastError();
 }
 
