@@ -51,15 +51,16 @@ __device__ inline unsigned key_of(float x) {
 }
 
 // Which tokens a (sequence, head) keeps: one workgroup per pair, which holds
-// the keys of up to kHeld tokens in registers, read once: four adjacent
-// tokens per thread and round.  The m-th largest key of the tokens between
+// the keys of up to kHeld tokens, read once: four adjacent tokens per thread
+// and round, the first eight rounds in registers, the others in LDS.  The m-th largest key of the tokens between
 // sink and recent is found digit by digit: 8 bits a step, from the top, by a
 // histogram of the keys that share the digits found so far, which ends when
 // a digit's keys are all wanted.  The kept tokens' places then follow from
 // counts over the waves in the tokens' order.  (Longer sequences go through
 // the same steps with their keys read anew, kHeld at a time.)
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kRounds = 8, kPerRound = 4 * kSelThreads, kHeld = kRounds * kPerRound;
+constexpr int kRegRounds = 8, kRounds = 16;
+constexpr int kPerRound = 4 * kSelThreads, kHeld = kRounds * kPerRound;
 // Neighbouring scores share their top bits, so that one histogram's counter
 // would be hit by most lanes of a wave at once: kCopies of it, in different
 // LDS banks, taken by the lanes in turn.
@@ -69,7 +70,7 @@ typedef unsigned keys4 __attribute__((ext_vector_type(4)));
 
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
-    const int lane = tid & 63, w = tid >> 6;
+    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int len = cached_len(a.seq_lens, b, a.map);
     int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
     if (len <= a.budget) {
@@ -80,48 +81,66 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     __shared__ int hist[kCopies * kCopyStride], waves[4], found[3];
     __shared__ int2 counts[kRounds][kSelWaves];
 
-    // keys of tokens j .. j + 3 (one page holds all four)
-    auto load4 = [&](int j) {
-        keys4 k{0, 0, 0, 0};
-        if (j < len) {
-            const int page = page_of(a.map, b, j);
-            if (page >= 0) {
-                const float4 x = *reinterpret_cast<const float4 *>(
-                    a.scores + cache_row(a.map, a.Hkv, page, h, slot_of(a.map, j)));
-                k = keys4{key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w)};
-            }
-        }
-        return k;
+    __shared__ keys4 lds_keys[(kRounds - kRegRounds) * kSelThreads];
+    keys4 reg_keys[kRegRounds];
+    auto keys = [&](int r) {
+        return r < kRegRounds ? reg_keys[r] : lds_keys[(r - kRegRounds) * kSelThreads + tid];
     };
-    keys4 key[kRounds];
+    // eight rounds at a time: their pages, then their scores
     auto load_held = [&](int base) {
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            if (base + r * kPerRound < len) key[r] = load4(base + r * kPerRound + 4 * tid);
-            if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // addresses of four rounds at once
+        for (int r0 = 0; r0 < kRounds; r0 += 8) {
+            if (base + r0 * kPerRound >= len) break;
+            int page[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = base + (r0 + i) * kPerRound + 4 * tid;
+                page[i] = j < len ? page_of(a.map, b, j) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // tokens j .. j + 3: one page holds all four
+                const int j = base + (r0 + i) * kPerRound + 4 * tid;
+                keys4 k{0, 0, 0, 0};
+                if (page[i] >= 0) {
+                    const float4 x = *reinterpret_cast<const float4 *>(
+                        a.scores + cache_row(a.map, a.Hkv, page[i], h, slot_of(a.map, j)));
+                    k = keys4{key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w)};
+                    if (j < lo || j + 4 > hi)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) k[e] = j + e >= lo && j + e < hi ? k[e] : 0u;
+                }
+                if (r0 + i < kRegRounds) reg_keys[r0 + i] = k;
+                else lds_keys[(r0 + i - kRegRounds) * kSelThreads + tid] = k;
+            }
+            __builtin_amdgcn_sched_barrier(0);   // the addresses of eight rounds at once
         }
     };
     const bool once = len <= kHeld;
     load_held(0);
 
+    // (Tokens outside lo .. hi have key 0 as well: they add to the count of
+    // the digits 00.. only, which comes last and is not compared with.)
     int want = a.budget - a.sink - a.recent;       // of the hi - lo > want tokens between
     unsigned prefix = 0;                           // digits of the threshold found so far
     const bool none = want == 0;
+    if (none) prefix = 0xFFFFFFFFu;                // above every key
+    bool ties = false;                             // more keys equal the threshold than wanted
     for (int shift = 24; shift >= 0 && !none; shift -= 8) {
         for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
         __syncthreads();
+        int *mine = hist + (lane & (kCopies - 1)) * kCopyStride;
+        // keys prefix .. prefix + span share the digits found
+        const unsigned span = shift == 24 ? 0xFFFFFFFFu : (1u << (shift + 8)) - 1;
         for (int base = 0; base < len; base += kHeld) {
             if (!once) load_held(base);
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) {
                 if (base + r * kPerRound >= len) break;
+                const keys4 k4 = keys(r);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = base + r * kPerRound + 4 * tid + e;
-                    const unsigned k = key[r][e];
-                    if (j >= lo && j < hi && (shift == 24 || ((k ^ prefix) >> (shift + 8)) == 0))
-                        atomicAdd(&hist[(lane & (kCopies - 1)) * kCopyStride + ((k >> shift) & 255)], 1);
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (k4[e] - prefix <= span) atomicAdd(&mine[(k4[e] >> shift) & 255], 1);
             }
         }
         __syncthreads();
@@ -151,30 +170,44 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         __syncthreads();
         prefix |= (unsigned)found[0] << shift;
         want = found[1];                           // wanted among the keys with this prefix
-        if (want == found[2]) break;               // all of them: prefix 00.. is a threshold
+        ties = want != found[2];
+        if (!ties) break;                          // all of them: prefix 00.. is a threshold
     }
-    // every key above prefix is kept, and the first `want` keys equal to it
-    // (all keys that share its digits, where the search ended early)
+    // Kept are sink and recent, every key above the threshold, and of the
+    // keys equal to it the first `want` (without ties: all).
     int above = 0, equal = 0;                      // kept, and equal keys, before base
+    auto count_below = [&](unsigned long long x) {
+        return (int)__builtin_amdgcn_mbcnt_hi((unsigned)(x >> 32),
+                                              __builtin_amdgcn_mbcnt_lo((unsigned)x, 0));
+    };
     for (int base = 0; base < len; base += kHeld) {
         if (!once) load_held(base);
-        auto flags = [&](int r, int e, bool &keep, bool &eq) {
-            const int j = base + r * kPerRound + 4 * tid + e;
-            const bool mid = j >= lo && j < hi;
-            keep = j < len && (!mid || (!none && key[r][e] > prefix));
-            eq = mid && !none && key[r][e] == prefix;
+        auto flags = [&](int r, keys4 k, bool (&keep)[4], bool (&eq)[4]) {
+            const int j0 = base + r * kPerRound;
+            if (j0 >= lo && j0 + kPerRound <= hi && !ties) {      // the usual round
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { keep[e] = k[e] >= prefix; eq[e] = false; }
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + 4 * tid + e;
+                const bool mid = j >= lo && j < hi;
+                keep[e] = j < len && (!mid || (ties ? k[e] > prefix : k[e] >= prefix));
+                eq[e] = ties && mid && k[e] == prefix;
+            }
         };
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             if (base + r * kPerRound >= len) break;
+            bool keep[4], eq[4];
+            flags(r, keys(r), keep, eq);
             int2 c{0, 0};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                bool keep, eq;
-                flags(r, e, keep, eq);
-                c.x += __popcll(__ballot(keep));
-                c.y += __popcll(__ballot(eq));
+                c.x += __popcll(__ballot(keep[e]));
+                if (ties) c.y += __popcll(__ballot(eq[e]));
             }
             if (lane == 0) counts[r][w] = c;
         }
@@ -189,18 +222,17 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 const int x = __shfl_up(t.x, m), y = __shfl_up(t.y, m);
                 if (lane >= m) { t.x += x; t.y += y; }
             }
-            int nk = above + __shfl(t.x - c.x, w), ne = equal + __shfl(t.y - c.y, w);
-            above += __shfl(t.x, kSelWaves - 1);
-            equal += __shfl(t.y, kSelWaves - 1);
+            int nk = above + __builtin_amdgcn_readlane(t.x - c.x, w);
+            int ne = equal + __builtin_amdgcn_readlane(t.y - c.y, w);
+            above += __builtin_amdgcn_readlane(t.x, kSelWaves - 1);
+            equal += __builtin_amdgcn_readlane(t.y, kSelWaves - 1);
             // before this lane's four tokens
             bool keep[4], eq[4];
+            flags(r, keys(r), keep, eq);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                flags(r, e, keep[e], eq[e]);
-                const unsigned long long bk = __ballot(keep[e]), be = __ballot(eq[e]);
-                const unsigned long long below = (1ull << lane) - 1;
-                nk += __popcll(bk & below);
-                ne += __popcll(be & below);
+                nk += count_below(__ballot(keep[e]));
+                if (ties) ne += count_below(__ballot(eq[e]));
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
