@@ -79,33 +79,40 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     }
     const int lo = a.sink, hi = len - a.recent;
     __shared__ int hist[kCopies * kCopyStride], waves[4], found[3];
-    __shared__ int2 counts[kRounds][kSelWaves];
+    __shared__ int2 counts[kRounds][kSelWaves], wave_counts[4];
 
     __shared__ keys4 lds_keys[(kRounds - kRegRounds) * kSelThreads];
     keys4 reg_keys[kRegRounds];
     auto keys = [&](int r) {
         return r < kRegRounds ? reg_keys[r] : lds_keys[(r - kRegRounds) * kSelThreads + tid];
     };
-    // eight rounds at a time: their pages, then their scores
+    // the pages of all rounds, then their scores, eight rounds at a time
     auto load_held = [&](int base) {
+        int page[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int j = base + r * kPerRound + 4 * tid;
+            page[r] = j < len ? page_of(a.map, b, j) : -1;
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r0 = 0; r0 < kRounds; r0 += 8) {
             if (base + r0 * kPerRound >= len) break;
-            int page[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = base + (r0 + i) * kPerRound + 4 * tid;
-                page[i] = j < len ? page_of(a.map, b, j) : -1;
-            }
+            float4 x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 // tokens j .. j + 3: one page holds all four
                 const int j = base + (r0 + i) * kPerRound + 4 * tid;
+                if (page[r0 + i] >= 0)
+                    x[i] = *reinterpret_cast<const float4 *>(
+                        a.scores + cache_row(a.map, a.Hkv, page[r0 + i], h, slot_of(a.map, j)));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = base + (r0 + i) * kPerRound + 4 * tid;
                 keys4 k{0, 0, 0, 0};
-                if (page[i] >= 0) {
-                    const float4 x = *reinterpret_cast<const float4 *>(
-                        a.scores + cache_row(a.map, a.Hkv, page[i], h, slot_of(a.map, j)));
-                    k = keys4{key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w)};
+                if (page[r0 + i] >= 0) {
+                    k = keys4{key_of(x[i].x), key_of(x[i].y), key_of(x[i].z), key_of(x[i].w)};
                     if (j < lo || j + 4 > hi)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) k[e] = j + e >= lo && j + e < hi ? k[e] : 0u;
@@ -113,7 +120,6 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 if (r0 + i < kRegRounds) reg_keys[r0 + i] = k;
                 else lds_keys[(r0 + i - kRegRounds) * kSelThreads + tid] = k;
             }
-            __builtin_amdgcn_sched_barrier(0);   // the addresses of eight rounds at once
         }
     };
     const bool once = len <= kHeld;
@@ -212,20 +218,32 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             if (lane == 0) counts[r][w] = c;
         }
         __syncthreads();
+        // counts before each round and wave: thread t scans entry t, in order
+        static_assert(kRounds * kSelWaves == 256, "four waves scan the counts");
+        int2 c{0, 0}, t{0, 0};
+        if (tid < 256) {
+            if (base + (tid / kSelWaves) * kPerRound < len) c = counts[tid / kSelWaves][tid % kSelWaves];
+            t = c;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            if (base + r * kPerRound >= len) break;
-            // lane i of the first kSelWaves: wave i's counts
-            int2 c = lane < kSelWaves ? counts[r][lane] : int2{0, 0}, t = c;
-#pragma unroll
-            for (int m = 1; m < kSelWaves; m <<= 1) {
+            for (int m = 1; m < 64; m <<= 1) {
                 const int x = __shfl_up(t.x, m), y = __shfl_up(t.y, m);
                 if (lane >= m) { t.x += x; t.y += y; }
             }
-            int nk = above + __builtin_amdgcn_readlane(t.x - c.x, w);
-            int ne = equal + __builtin_amdgcn_readlane(t.y - c.y, w);
-            above += __builtin_amdgcn_readlane(t.x, kSelWaves - 1);
-            equal += __builtin_amdgcn_readlane(t.y, kSelWaves - 1);
+            if (lane == 63) wave_counts[w] = t;
+        }
+        __syncthreads();
+        if (tid < 256) {
+            int2 x{above + t.x - c.x, equal + t.y - c.y};
+            for (int i = 0; i < w; ++i) { x.x += wave_counts[i].x; x.y += wave_counts[i].y; }
+            counts[tid / kSelWaves][tid % kSelWaves] = x;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { above += wave_counts[i].x; equal += wave_counts[i].y; }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (base + r * kPerRound >= len) break;
+            int nk = counts[r][w].x, ne = counts[r][w].y;
             // before this lane's four tokens
             bool keep[4], eq[4];
             flags(r, keys(r), keep, eq);

@@ -465,6 +465,17 @@ def test_evict_long_and_large_budget(pages):
             run_evict(kc, vc, s, table, lens, budget, 100, 10, new_table, kind)
 
 
+@pytest.mark.parametrize("kind", ["weights", "ties"])
+def test_evict_longer_than_a_workgroup_holds(kind):
+    """Past 65,536 tokens, and just at that length."""
+    announce("evict very long %s" % kind)
+    lens = [70001, 65536, 131]
+    kc, vc, sc, table = make_cache(lens, 1, 64, 256, torch.bfloat16, seed=90)
+    s = odd_scores(sc, kind, 91)
+    run_evict(kc, vc, s, table, lens, 30000, 1000, 10, None, kind)
+    run_evict(kc, vc, s, table, lens, 100, 0, 0, None, kind)
+
+
 def test_evict_absent_pages():
     """Tokens on absent pages go first and are not moved; absent new pages
     take nothing."""
