@@ -183,6 +183,13 @@ __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 // over and the weights keep).
 __device__ inline float finite_top(float m) { return m == -INFINITY ? 0.f : m; }
 
+// K and V are read once by one wave (R = 1): loads that pass through the
+// caches without staying there (64 contexts, 680 MB: 142 -> 129 us).
+constexpr int kStream = 2;
+__device__ inline u32x4 stream16(rsrc_t r, unsigned off) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStream);
+}
+
 // A tile's operands, per dtype.  With lane = 16 lg + r:
 //   S^T = K Q^T: lane supplies key r of a block of 16 (A) and query row r (B),
 //     and gets the logits of query row r with keys 4 lg .. 4 lg + 3;
@@ -191,7 +198,16 @@ __device__ inline float finite_top(float m) { return m == -INFINITY ? 0.f : m; }
 //     and V^T's is read from rows 4 lg + e of V, PER = D / 16 channels per
 //     lane, so that V needs no transposition through LDS: acc[c][e] is
 //     channel dim(c, 4 lg + e) of query row r.
+// Several waves that read one tile (R > 1) take it from LDS, where it lies row
+// by row, the 16-byte chunks of a row exchanged by its number (chunk c at
+// c ^ swap(row)), so that the sixteen rows of a K operand are in different
+// banks.
 template <typename T, int D> struct Tile;
+template <int ROW_BYTES>
+__device__ inline int chunk_at(int row, int c) {
+    const int swap = ROW_BYTES >= 256 ? row & 15 : (row >> 1) & 7;
+    return row * ROW_BYTES + ((c ^ swap) << 4);
+}
 
 template <int D> struct Tile<bf16, D> {
     static constexpr int kBlocks = 2;              // blocks of 16 tokens: 32 k slots
@@ -208,20 +224,43 @@ template <int D> struct Tile<bf16, D> {
     __device__ static inline void load_k(K &k, int blk, rsrc_t r, int lane) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-            k.f[blk][i] = bload16(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4));
+            k.f[blk][i] = __builtin_bit_cast(
+                bf16x8, stream16(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4)));
     }
     __device__ static inline void load_v(V &v, int blk, rsrc_t r, int lane) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const unsigned off = (4 * (lane >> 4) + e) * kRowBytes + (lane & 15) * PER * 2;
             if constexpr (PER == 8) {
-                const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+                const u32x4 x = stream16(r, off);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v.w[blk][e][i] = x[i];
             } else {
-                const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+                const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kStream);
                 v.w[blk][e][0] = x[0];
                 v.w[blk][e][1] = x[1];
+            }
+        }
+    }
+    __device__ static inline void lds_k(K &k, int blk, const char *t, int lane) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            k.f[blk][i] = *reinterpret_cast<const bf16x8 *>(
+                t + chunk_at<kRowBytes>(16 * blk + (lane & 15), 4 * i + (lane >> 4)));
+    }
+    __device__ static inline void lds_v(V &v, int blk, const char *t, int lane) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 16 * blk + 4 * (lane >> 4) + e, r = lane & 15;
+            if constexpr (PER == 8) {
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(t + chunk_at<kRowBytes>(row, r));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v.w[blk][e][i] = x[i];
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(
+                    t + chunk_at<kRowBytes>(row, r >> 1) + 8 * (r & 1));
+                v.w[blk][e][0] = x.x;
+                v.w[blk][e][1] = x.y;
             }
         }
     }
@@ -309,15 +348,31 @@ template <int D> struct Tile<float, D> {
     __device__ static inline void load_k(K &k, int, rsrc_t r, int lane) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-            k.f[0][i] = bload16f(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4));
+            k.f[0][i] = __builtin_bit_cast(
+                f32x4, stream16(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4)));
     }
     __device__ static inline void load_v(V &v, int, rsrc_t r, int lane) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int i = 0; i < PER / 4; ++i)
-                v.f[e][i] = bload16f(r, (4 * (lane >> 4) + e) * kRowBytes + 256 * i +
-                                            16 * (lane & 15));
+                v.f[e][i] = __builtin_bit_cast(
+                    f32x4, stream16(r, (4 * (lane >> 4) + e) * kRowBytes + 256 * i +
+                                           16 * (lane & 15)));
+    }
+    __device__ static inline void lds_k(K &k, int, const char *t, int lane) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            k.f[0][i] = *reinterpret_cast<const f32x4 *>(
+                t + chunk_at<kRowBytes>(lane & 15, 4 * i + (lane >> 4)));
+    }
+    __device__ static inline void lds_v(V &v, int, const char *t, int lane) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < PER / 4; ++i)
+                v.f[e][i] = *reinterpret_cast<const f32x4 *>(
+                    t + chunk_at<kRowBytes>(4 * (lane >> 4) + e, 16 * i + (lane & 15)));
     }
     __device__ static inline f32x4 logits(const K &k, int, const Q &q) {
         f32x4 s{0.f, 0.f, 0.f, 0.f};
@@ -373,16 +428,26 @@ template <int D> struct Tile<float, D> {
 
 // Workgroup = (slot, key-value head, row block).  Wave w has row tile w % R
 // and takes every 4 / R-th tile of tokens, with m, l and o of its own, joined
-// through LDS at the end.  K and V go from HBM straight into the registers that MFMA
-// reads: the next tile's K is requested as soon as this one's logits are
-// formed, its V after this one's product.
+// through LDS at the end.
+//
+// R = 1: K and V go from HBM straight into the registers that MFMA reads: the
+// next tile's K is requested as soon as this one's logits are formed, its V
+// after this one's product.
+// R > 1: the waves of a share read the same tiles, which all threads bring
+// into LDS together, a stage (one tile per share) at a time: one stage is
+// worked on, the next is written beside it, and two more are on the way in
+// registers.
 template <typename T, int D, int R>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D>;
     constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = 16 * kBlocks;
     constexpr int kPad = D + 4, kShares = kWaves / R;
+    constexpr int kTileBytes = kTile * TL::kRowBytes, kStage = kShares * 2 * kTileBytes;
+    constexpr int kOBytes = kWaves * 16 * kPad * (int)sizeof(float);
     __shared__ float sm[kWaves][16], sl[kWaves][16];
-    __shared__ __align__(16) float so[kWaves][16][kPad];
+    // the stages, and at the end every wave's o
+    __shared__ __align__(16) char lds[R > 1 && 2 * kStage > kOBytes ? 2 * kStage : kOBytes];
+    float(*so)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(lds);
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6), rt = w % R, share = w / R;
@@ -420,8 +485,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const int k_lo = first.lo > c_lo ? first.lo : c_lo, k_hi = last.hi < c_hi ? last.hi : c_hi;
     // every row attends to the tokens of [all_lo, all_hi)
     const int all_lo = last.lo, all_hi = first.hi;
-    const int tile0 = k_lo / kTile + share;
-    const int tiles = k_hi > k_lo ? ((k_hi + kTile - 1) / kTile - tile0 + kShares - 1) / kShares : 0;
+    const int tile0 = k_lo / kTile;
+    const int tiles = k_hi > k_lo ? (k_hi + kTile - 1) / kTile - tile0 : 0;
 
     const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
     const float c1 = a.scale * kLog2e;
@@ -430,70 +495,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
     for (int c = 0; c < PER; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // pages of this wave's next 64 tiles, one tile per lane (of the table's
-    // entries past the length too, which block_src leaves out)
-    const int cap = a.map.max_pages << a.map.page_shift;
-    int pg[kBlocks];
-    auto load_pages = [&](int i0) {
-        const int j = (tile0 + kShares * (i0 + lane)) * kTile;
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk)
-            pg[blk] = j + 16 * blk < cap ? page_of(a.map, b, j + 16 * blk) : -1;
-    };
-    // the cache rows of block blk of tile i (none past the length, on an
-    // absent page or past the last tile: such loads give zeros)
-    const size_t page_bytes = (size_t)TL::kRowBytes << a.map.page_shift;
-    struct Src { size_t at; unsigned bytes; };
-    auto block_src = [&](int i, int blk) {
-        const int page = __builtin_amdgcn_readlane(pg[blk], i & 63);
-        const int j = (tile0 + kShares * i) * kTile + 16 * blk;
-        Src s;
-        s.at = ((size_t)page * a.Hkv + h) * page_bytes + (size_t)slot_of(a.map, j) * TL::kRowBytes;
-        const int valid = len - j < 16 ? len - j : 16;
-        const bool some = page >= 0 && i < tiles && valid > 0;
-        s.bytes = some ? (unsigned)(valid * TL::kRowBytes) : 0u;
-        if (!some) s.at = 0;
-        return s;
-    };
-    typename TL::K kf;
-    typename TL::V vf;
-    load_pages(0);
-    bool present = true;                        // both blocks of the tile at hand
-    Src src[kBlocks];
-#pragma unroll
-    for (int blk = 0; blk < kBlocks; ++blk) {
-        src[blk] = block_src(0, blk);
-        present &= src[blk].bytes != 0;
-        TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
-    }
-#pragma unroll
-    for (int blk = 0; blk < kBlocks; ++blk)
-        TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
-
-    for (int i = 0; i < tiles; ++i) {
-        const int j0 = (tile0 + kShares * i) * kTile;
-        f32x4 x[kBlocks];
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
-        const bool full = present && j0 >= all_lo && j0 + kTile <= all_hi;
-        bool here[kBlocks];
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) here[blk] = src[blk].bytes != 0;
-        // the next tile's K
-        if (((i + 1) & 63) == 0) load_pages(i + 1);
-        present = true;
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) {
-            src[blk] = block_src(i + 1, blk);
-            present &= src[blk].bytes != 0;
-            TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
-        }
+    // One tile's logits (before scaling) and values into m, l and o.  full:
+    // every row attends to all of it; here: which of its blocks are there.
+    auto absorb = [&](int j0, f32x4 (&x)[kBlocks], typename TL::V &vf, bool full,
+                      const bool (&here)[kBlocks]) {
         float top = -INFINITY;
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[blk][e] *= c1;
-            if (k.logits && row < rows)
+            if (k.logits && row < rows && here[blk])
                 *reinterpret_cast<f32x4 *>(k.logits +
                                            (((size_t)b * a.Hkv + h) * rows + row) * k.cap32 + j0 +
                                            16 * blk + 4 * lg) = x[blk];
@@ -550,9 +561,164 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         }
 #pragma unroll
         for (int c = 0; c < PER; ++c) acc[c] = TL::pv(vf, c, p, acc[c]);
+    };
+
+    // Pages of the next 64 tiles from tile i0 on, `step` apart, one per lane
+    // (of the table's entries past the length too, which block_src leaves out).
+    constexpr int step = R == 1 ? kShares : 1;
+    const int cap = a.map.max_pages << a.map.page_shift;
+    int pg[kBlocks];
+    auto load_pages = [&](int i0) {
+        const int j = (tile0 + i0 + step * lane) * kTile;
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk)
+            pg[blk] = j + 16 * blk < cap ? page_of(a.map, b, j + 16 * blk) : -1;
+    };
+    // the cache rows of block blk of tile i, whose pages lane `at` holds (none
+    // past the length, on an absent page or past the last tile: such loads
+    // give zeros)
+    const size_t page_bytes = (size_t)TL::kRowBytes << a.map.page_shift;
+    struct Src { size_t at; unsigned bytes; };
+    auto block_src = [&](int i, int at, int blk) {
+        const int page = __builtin_amdgcn_readlane(pg[blk], at);
+        const int j = (tile0 + i) * kTile + 16 * blk;
+        Src s;
+        s.at = ((size_t)page * a.Hkv + h) * page_bytes + (size_t)slot_of(a.map, j) * TL::kRowBytes;
+        const int valid = len - j < 16 ? len - j : 16;
+        const bool some = page >= 0 && i < tiles && valid > 0;
+        s.bytes = some ? (unsigned)(valid * TL::kRowBytes) : 0u;
+        if (!some) s.at = 0;
+        return s;
+    };
+    typename TL::K kf;
+    typename TL::V vf;
+    if constexpr (R == 1) {
+        load_pages(share);
+        bool present = true;                    // all blocks of the tile at hand
+        Src src[kBlocks];
+#pragma unroll
+        for (int blk = 0; blk < kBlocks; ++blk) {
+            src[blk] = block_src(share, 0, blk);
+            present &= src[blk].bytes != 0;
+            TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
+        }
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
             TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
+
+        for (int i = share, at = 1; i < tiles; i += kShares, ++at) {
+            const int j0 = (tile0 + i) * kTile;
+            f32x4 x[kBlocks];
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
+            const bool full = present && j0 >= all_lo && j0 + kTile <= all_hi;
+            bool here[kBlocks];
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) here[blk] = src[blk].bytes != 0;
+            // the next tile's K
+            if ((at & 63) == 0) load_pages(i + kShares);
+            present = true;
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) {
+                src[blk] = block_src(i + kShares, at & 63, blk);
+                present &= src[blk].bytes != 0;
+                TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
+            }
+            absorb(j0, x, vf, full, here);
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk)
+                TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
+        }
+    } else {
+        constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTileBytes / 16 / kThreads;
+        static_assert(kUnits * kThreads * 16 == kTileBytes && 64 / kChunks <= 16,
+                      "threads cover a tile, a wave's rows lie in one block");
+        // a stage on its way: 16 bytes of K and of V per thread, unit and
+        // share, and which blocks of this wave's own tile are there
+        struct Stage {
+            u32x4 kv[kShares][kUnits][2];
+            bool here[kBlocks];
+        };
+        int paged = 0;                          // the tile that lane 0 of pg stands for
+        load_pages(0);
+        auto load = [&](int it, Stage &s) {
+#pragma unroll
+            for (int x = 0; x < kShares; ++x) {
+                const int i = it * kShares + x;
+                if (i >= paged + 64) {
+                    paged = i;
+                    load_pages(i);
+                }
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int unit = tid + kThreads * u, r = unit / kChunks;
+                    const int blk = __builtin_amdgcn_readfirstlane(r >> 4);
+                    const Src src = kBlocks == 1 || blk == 0 ? block_src(i, i - paged, 0)
+                                                             : block_src(i, i - paged, kBlocks - 1);
+                    const unsigned off = (r & 15) * TL::kRowBytes + unit % kChunks * 16;
+                    s.kv[x][u][0] = __builtin_amdgcn_raw_buffer_load_b128(
+                        make_rsrc(kc + src.at, src.bytes), off, 0, 0);
+                    s.kv[x][u][1] = __builtin_amdgcn_raw_buffer_load_b128(
+                        make_rsrc(vc + src.at, src.bytes), off, 0, 0);
+                }
+                if (x == share)
+#pragma unroll
+                    for (int blk = 0; blk < kBlocks; ++blk)
+                        s.here[blk] = block_src(i, i - paged, blk).bytes != 0;
+            }
+        };
+        auto store = [&](char *to, const Stage &s) {
+#pragma unroll
+            for (int x = 0; x < kShares; ++x)
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int unit = tid + kThreads * u;
+                    const int at = 2 * x * kTileBytes +
+                                   chunk_at<TL::kRowBytes>(unit / kChunks, unit % kChunks);
+                    *reinterpret_cast<u32x4 *>(to + at) = s.kv[x][u][0];
+                    *reinterpret_cast<u32x4 *>(to + at + kTileBytes) = s.kv[x][u][1];
+                }
+        };
+        auto work = [&](int it, const char *from, const bool (&here)[kBlocks]) {
+            const int j0 = (tile0 + it * kShares + share) * kTile;
+            const char *t = from + 2 * share * kTileBytes;
+            f32x4 x[kBlocks];
+            bool full = j0 >= all_lo && j0 + kTile <= all_hi;
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) {
+                TL::lds_k(kf, blk, t, lane);
+                TL::lds_v(vf, blk, t + kTileBytes, lane);
+                full &= here[blk];
+            }
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
+            absorb(j0, x, vf, full, here);
+        };
+        const int its = (tiles + kShares - 1) / kShares;
+        Stage s0, s1;
+        bool here0[kBlocks], here1[kBlocks];
+        auto put = [&](char *to, const Stage &s, bool (&here)[kBlocks]) {
+            store(to, s);
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) here[blk] = s.here[blk];
+        };
+        load(0, s0);
+        load(1, s1);
+        put(lds, s0, here0);
+        load(2, s0);
+        __syncthreads();
+        for (int it = 0; it < its; it += 2) {
+            work(it, lds, here0);
+            put(lds + kStage, s1, here1);
+            load(it + 3, s1);
+            __syncthreads();
+            if (it + 1 >= its) break;
+            work(it + 1, lds + kStage, here1);
+            put(lds, s0, here0);
+            load(it + 4, s0);
+            __syncthreads();
+        }
+        __syncthreads();                        // the stages make room for o
     }
 
     // join the waves of a row tile: every wave's o in units of their common
