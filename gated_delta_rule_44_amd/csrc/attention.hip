@@ -431,8 +431,8 @@ template <int D> struct Tile<float, D> {
 // through LDS at the end.
 //
 // R = 1: K and V go from HBM straight into the registers that MFMA reads: the
-// next tile's K is requested as soon as this one's logits are formed, its V
-// after this one's product.
+// next tile to come is requested into a tile's registers as they fall free, K
+// after its logits are formed, V after its product.
 // R > 1: the waves of a share read the same tiles, which all threads bring
 // into LDS together, a stage (one tile per share) at a time: one stage is
 // worked on, the next is written beside it, and two more are on the way in
@@ -590,44 +590,58 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         if (!some) s.at = 0;
         return s;
     };
-    typename TL::K kf;
-    typename TL::V vf;
     if constexpr (R == 1) {
-        load_pages(share);
-        bool present = true;                    // all blocks of the tile at hand
-        Src src[kBlocks];
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) {
-            src[blk] = block_src(share, 0, blk);
-            present &= src[blk].bytes != 0;
-            TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
-        }
-#pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk)
-            TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
-
-        for (int i = share, at = 1; i < tiles; i += kShares, ++at) {
-            const int j0 = (tile0 + i) * kTile;
-            f32x4 x[kBlocks];
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
-            const bool full = present && j0 >= all_lo && j0 + kTile <= all_hi;
-            bool here[kBlocks];
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) here[blk] = src[blk].bytes != 0;
-            // the next tile's K
-            if ((at & 63) == 0) load_pages(i + kShares);
-            present = true;
+        // D = 64: two tiles on their way, in two sets of registers.  D = 128:
+        // one, as a second set's 64 registers would spill (64 contexts 125 ->
+        // 136 us with it; D = 64 in fp32, 8 contexts: 35 -> 31 us).
+        constexpr bool kTwo = D == 64;
+        struct Ahead {
+            typename TL::K kf;
+            typename TL::V vf;
+            Src src[kBlocks];
+        } s0, s1;
+        int at = 0;                             // tiles whose loads have been issued
+        auto load_k = [&](Ahead &s) {
+            if ((at & 63) == 0) load_pages(share + kShares * at);
 #pragma unroll
             for (int blk = 0; blk < kBlocks; ++blk) {
-                src[blk] = block_src(i + kShares, at & 63, blk);
-                present &= src[blk].bytes != 0;
-                TL::load_k(kf, blk, make_rsrc(kc + src[blk].at, src[blk].bytes), lane);
+                s.src[blk] = block_src(share + kShares * at, at & 63, blk);
+                TL::load_k(s.kf, blk, make_rsrc(kc + s.src[blk].at, s.src[blk].bytes), lane);
             }
-            absorb(j0, x, vf, full, here);
+            ++at;
+        };
+        auto load_v = [&](Ahead &s) {
 #pragma unroll
             for (int blk = 0; blk < kBlocks; ++blk)
-                TL::load_v(vf, blk, make_rsrc(vc + src[blk].at, src[blk].bytes), lane);
+                TL::load_v(s.vf, blk, make_rsrc(vc + s.src[blk].at, s.src[blk].bytes), lane);
+        };
+        auto work = [&](int i, Ahead &s) {
+            const int j0 = (tile0 + i) * kTile;
+            f32x4 x[kBlocks];
+            bool here[kBlocks], full = j0 >= all_lo && j0 + kTile <= all_hi;
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) {
+                x[blk] = TL::logits(s.kf, blk, q);
+                here[blk] = s.src[blk].bytes != 0;
+                full &= here[blk];
+            }
+            load_k(s);
+            absorb(j0, x, s.vf, full, here);
+            load_v(s);
+        };
+        load_k(s0);
+        load_v(s0);
+        if constexpr (kTwo) {
+            load_k(s1);
+            load_v(s1);
+        }
+        for (int i = share; i < tiles; i += kShares) {
+            work(i, s0);
+            if constexpr (kTwo) {
+                i += kShares;
+                if (i >= tiles) break;
+                work(i, s1);
+            }
         }
     } else {
         constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTileBytes / 16 / kThreads;
@@ -679,6 +693,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
                     *reinterpret_cast<u32x4 *>(to + at + kTileBytes) = s.kv[x][u][1];
                 }
         };
+        typename TL::K kf;
+        typename TL::V vf;
         auto work = [&](int it, const char *from, const bool (&here)[kBlocks]) {
             const int j0 = (tile0 + it * kShares + share) * kTile;
             const char *t = from + 2 * share * kTileBytes;
