@@ -11,10 +11,11 @@
 // the same rule.
 //
 // The G = Hq / Hkv query heads of a key-value head and the n new tokens make
-// n G rows that read the same K and V: 16 R rows are one workgroup's, so
-// that a token is read from HBM once for all of them, as MFMA operands.
-// Bytes bound the kernel: 2 D elements a token against 4 D flops per row and
-// token is at most 16 R flops a byte, where the card turns at about 250.
+// n G rows that read the same K and V: a workgroup has up to 32 of them (16 in
+// fp32), so that a token is read from HBM once for all of them, as MFMA
+// operands.  Bytes bound the kernel: 2 D elements a token against 4 D flops
+// per row and token is at most 32 flops a byte, where the card turns at
+// about 250.
 #include "cache_internal.h"
 #include "gdr_internal.h"
 #include "device_util.h"
@@ -48,13 +49,13 @@ constexpr int kTargetWgs = 1024;
 constexpr int kMinChunk = 512;
 struct Plan {
     int units;            // workgroups of one slot: key-value heads x row blocks
-    int row_blocks;       // blocks of 16 R rows
+    int row_blocks;       // blocks of RW rows
     int want_slots;       // slots aimed at
     int max_slots;        // bound on the slots there can be: sum ceil(len / C) <= want + B
 };
-Plan make_plan(int B, int n, int G, int Hkv, int R, long long capacity) {
+Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
     Plan p;
-    p.row_blocks = (n * G + 16 * R - 1) / (16 * R);
+    p.row_blocks = (n * G + rw - 1) / rw;
     p.units = Hkv * p.row_blocks;
     p.want_slots = p.units >= kTargetWgs ? 1 : kTargetWgs / p.units;
     const long long by_len = (capacity + kMinChunk - 1) / kMinChunk * B;
@@ -62,10 +63,10 @@ Plan make_plan(int B, int n, int G, int Hkv, int R, long long capacity) {
     p.max_slots = (int)(by_len < bound ? (by_len < B ? B : by_len) : bound);
     return p;
 }
-// Rows of a workgroup's block, in tiles of 16, one per wave: the four waves
-// are R tiles of rows x 4 / R shares of the tokens.  Waves of one share read
-// the same K and V, from HBM once and then from the CU's L1.
-int row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Rows of a workgroup's block (RW), those of one MFMA tile.  More rows are
+// several blocks, which read K and V from L2 after the first.  In fp32 a block
+// of 32 would need twice the registers there are.
+int block_rows(bool bf16_io, long long rows) { return bf16_io && rows > 16 ? 32 : 16; }
 
 // Workspace: {first slot, slots} of every sequence; (m, l) of every slot, unit
 // and row; o of the same, unnormalised; with scores, the logits x of every row and
@@ -73,10 +74,10 @@ int row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 struct WsMap {
     size_t sched, ml, o, logits, total;
 };
-WsMap ws_map(int B, int n, int G, int Hkv, int D, int R, long long capacity, bool with_scores) {
+WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bool with_scores) {
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
-    const Plan p = make_plan(B, n, G, Hkv, R, capacity);
-    const size_t rows = (size_t)p.max_slots * p.units * 16 * R;
+    const Plan p = make_plan(B, n, G, Hkv, rw, capacity);
+    const size_t rows = (size_t)p.max_slots * p.units * rw;
     const bool parts = p.max_slots > B;
     WsMap w{};
     w.sched = 0;
@@ -124,14 +125,14 @@ __device__ inline N group_scan(N x, N &total, N *lds) {
     return before + incl - x;
 }
 
-struct Slot { int b, first, count, chunk; };      // sequence, its first slot, its slots, C
+struct Slot { int b, first, count, chunk; };      // sequence, its first slot, its slots, tokens of one
 // The sequence that slot s belongs to (b = -1: past the last slot).  Thread
 // i of the workgroup looks after sequences i per .. i per + per - 1.
 __device__ inline Slot find_slot(const KArgs &k, int s) {
     // too short a table for a second slot: slot and sequence are one
-    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 30};
+    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 29};
     __shared__ long long lds64[kWaves];
-    __shared__ int lds32[kWaves], found[3];
+    __shared__ int lds32[kWaves], found[4];
     const AttnArgs &a = k.a;
     const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
     long long sum = 0, total;
@@ -158,13 +159,15 @@ __device__ inline Slot find_slot(const KArgs &k, int s) {
             ns = ns > 1 ? ns : 1;
             if (s < at + ns) {
                 found[0] = b; found[1] = at; found[2] = ns;
+                // the sequence's slots alike, in multiples of 128 tokens
+                found[3] = ((sp.hi - sp.lo + ns - 1) / ns + 127) & ~127;
                 break;
             }
             at += ns;
         }
     }
     __syncthreads();
-    return Slot{found[0], found[1], found[2], chunk};
+    return Slot{found[0], found[1], found[2], found[3]};
 }
 
 __device__ inline float swap_max16(float x) {
@@ -183,212 +186,255 @@ __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 // over and the weights keep).
 __device__ inline float finite_top(float m) { return m == -INFINITY ? 0.f : m; }
 
-// K and V are read once by one wave (R = 1): loads that pass through the
-// caches without staying there (64 contexts, 680 MB: 142 -> 129 us).
-constexpr int kStream = 2;
-__device__ inline u32x4 stream16(rsrc_t r, unsigned off) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStream);
+// K and V that one workgroup reads once pass through the caches without
+// staying there (64 contexts, 680 MB: 142 -> 129 us); what several row blocks
+// read is kept.
+template <bool STREAM>
+__device__ inline u32x4 load16(rsrc_t r, unsigned off) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, STREAM ? 2 : 0);
 }
 
-// A tile's operands, per dtype.  With lane = 16 lg + r:
-//   S^T = K Q^T: lane supplies key r of a block of 16 (A) and query row r (B),
-//     and gets the logits of query row r with keys 4 lg .. 4 lg + 3;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// A block of 16 tokens of one head in a cache: its first byte, and how many
+// bytes of it may be read (0: none of its tokens are there).
+struct Src { size_t at; unsigned bytes; };
+
+// A tile of tokens as MFMA operands, per dtype and rows of a block.  With RW
+// rows, lane = RW g + r is row r:
+//   S^T = K Q^T: the lane supplies key r (A) and query row r (B), and gets
+//     logits of query row r: value i is that of the tile's token key(i, g);
 //   O^T = V^T P^T: P^T's operand is those logits' weights as they lie (the
 //     sum over k runs over the keys in whatever order both operands use),
-//     and V^T's is read from rows 4 lg + e of V, PER = D / 16 channels per
-//     lane, so that V needs no transposition through LDS: acc[c][e] is
-//     channel dim(c, 4 lg + e) of query row r.
-// Several waves that read one tile (R > 1) take it from LDS, where it lies row
-// by row, the 16-byte chunks of a row exchanged by its number (chunk c at
-// c ^ swap(row)), so that the sixteen rows of a K operand are in different
-// banks.
-template <typename T, int D> struct Tile;
-template <int ROW_BYTES>
-__device__ inline int chunk_at(int row, int c) {
-    const int swap = ROW_BYTES >= 256 ? row & 15 : (row >> 1) & 7;
-    return row * ROW_BYTES + ((c ^ swap) << 4);
+//     and V^T's is read from the rows of V that hold the same keys, PER = D / RW
+//     channels per lane, so that V needs no transposition through LDS:
+//     acc[c][i] is channel dim(c, m(i, g)) of query row r.
+template <typename T, int D, int RW> struct Tile;
+
+// two keys' values of one channel pair -> channel c of both
+__device__ inline unsigned pick2(unsigned k0, unsigned k1, int c) {
+    return __builtin_amdgcn_perm(k1, k0, c & 1 ? 0x07060302u : 0x05040100u);
+}
+// bits 15 and 31: whether the word's bf16 values are infinities or NaN (an
+// exponent of all ones carries)
+__device__ inline unsigned odd2(unsigned x) { return (x & 0x7F807F80u) + 0x00800080u; }
+__device__ inline unsigned clear2(unsigned x) {
+    return ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) |
+           ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+}
+// 1 where a value is an infinity or NaN other than `but`
+__device__ inline unsigned mark2(unsigned x, unsigned but) {
+    const unsigned lo = x & 0xFFFFu, hi = x >> 16;
+    return ((lo & 0x7F80u) == 0x7F80u && lo != but ? 0x3F80u : 0u) |
+           ((hi & 0x7F80u) == 0x7F80u && hi != but ? 0x3F800000u : 0u);
 }
 
-template <int D> struct Tile<bf16, D> {
-    static constexpr int kBlocks = 2;              // blocks of 16 tokens: 32 k slots
-    static constexpr int PER = D / 16;
+template <int D, int RW> struct Tile<bf16, D, RW> {
+    static constexpr int kBlocks = 2, kTile = 32;  // blocks of 16 tokens
+    static constexpr int kGroups = 64 / RW;        // lanes of a row
+    static constexpr int kVals = kTile / kGroups;  // logits of a lane
+    static constexpr int PER = D / RW;             // channels of a lane's V rows, blocks of acc
     static constexpr int kRowBytes = D * 2;
-    struct Q { bf16x8 f[D / 32]; };
-    struct K { bf16x8 f[2][D / 32]; };
-    struct V { unsigned w[2][4][PER / 2]; };
-    __device__ static inline int dim(int c, int m) { return PER * m + c; }
+    static constexpr int kSteps = D / (8 * kGroups);     // MFMAs of a block of keys
+    static constexpr int kKeyBlocks = kTile / RW;        // S^T tiles: 2 (RW = 16) or 1
+    typedef std::conditional_t<RW == 16, f32x4, f32x16> Acc;
+    static constexpr int kAcc = sizeof(Acc) / 4;
+    struct Q { bf16x8 f[kSteps]; };
+    struct K { bf16x8 f[kKeyBlocks][kSteps]; };
+    struct V { unsigned w[kVals][PER / 2]; };      // row of V: key(i, g)
+    // RW = 16: blocks of 16 keys, 4 g + e each; RW = 32: 8 (e / 4) + 4 g + e % 4
+    __device__ static inline int key(int i, int g) {
+        return RW == 16 ? 16 * (i >> 2) + 4 * g + (i & 3) : 8 * (i >> 2) + 4 * g + (i & 3);
+    }
+    __device__ static inline int dim(int c, int i, int g) {
+        return PER * (RW == 16 ? 4 * g + i : 8 * (i >> 2) + 4 * g + (i & 3)) + c;
+    }
+    static constexpr int block(int i) { return RW == 16 ? i >> 2 : i >> 3; }   // key's block of 16
+    __device__ static inline Acc mfma(bf16x8 a, bf16x8 b, Acc c) {
+        if constexpr (RW == 16) return mfma32(a, b, c);
+        else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
     __device__ static inline void load_q(Q &q, rsrc_t r, unsigned off, int lane) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) q.f[i] = bload16(r, off + 64 * i + 16 * (lane >> 4));
+        for (int i = 0; i < kSteps; ++i) q.f[i] = bload16(r, off + 16 * kGroups * i + 16 * (lane / RW));
     }
-    __device__ static inline void load_k(K &k, int blk, rsrc_t r, int lane) {
+    // kc + src[b].at: the rows of block b of 16 tokens
+    template <bool STREAM>
+    __device__ static inline void load_k(K &k, const char *kc, const Src (&src)[2], bool one_page,
+                                         int lane) {
+        const int g = lane / RW, r = lane % RW;
+        if constexpr (RW == 16) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            k.f[blk][i] = __builtin_bit_cast(
-                bf16x8, stream16(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4)));
+            for (int b = 0; b < 2; ++b) {
+                const rsrc_t rs = make_rsrc(kc + src[b].at, src[b].bytes);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+                    k.f[b][i] = __builtin_bit_cast(
+                        bf16x8, load16<STREAM>(rs, r * kRowBytes + 16 * kGroups * i + 16 * g));
+            }
+        } else if (one_page) {
+            // both blocks, one after the other
+            const rsrc_t whole = make_rsrc(kc + src[0].at, src[0].bytes + src[1].bytes);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+                k.f[0][i] = __builtin_bit_cast(
+                    bf16x8, load16<STREAM>(whole, r * kRowBytes + 16 * kGroups * i + 16 * g));
+        } else if (src[0].bytes + src[1].bytes) {
+            // pages of 16: an address per lane.  Rows of an absent block are
+            // read from the other one, and rows past the length as they lie
+            // in their page: their logits are masked.
+            const bool second = r < 16 ? src[0].bytes == 0 : src[1].bytes != 0;
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(
+                kc + (second ? src[1].at : src[0].at) + (r & 15) * kRowBytes + 16 * g);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+                k.f[0][i] = __builtin_bit_cast(bf16x8, STREAM ? __builtin_nontemporal_load(p + kGroups * i)
+                                                              : p[kGroups * i]);
+        }
     }
-    __device__ static inline void load_v(V &v, int blk, rsrc_t r, int lane) {
+    template <bool STREAM>
+    __device__ static inline void load_v(V &v, const rsrc_t (&rsrc)[2], int lane) {
+        const int g = lane / RW, r = lane % RW;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const unsigned off = (4 * (lane >> 4) + e) * kRowBytes + (lane & 15) * PER * 2;
+        for (int i = 0; i < kVals; ++i) {
+            const unsigned off = (key(i, g) & 15) * kRowBytes + r * PER * 2;
             if constexpr (PER == 8) {
-                const u32x4 x = stream16(r, off);
+                const u32x4 x = load16<STREAM>(rsrc[block(i)], off);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v.w[blk][e][i] = x[i];
+                for (int j = 0; j < 4; ++j) v.w[i][j] = x[j];
+            } else if constexpr (PER == 4) {
+                const auto x = __builtin_amdgcn_raw_buffer_load_b64(rsrc[block(i)], off, 0, STREAM ? 2 : 0);
+                v.w[i][0] = x[0];
+                v.w[i][1] = x[1];
             } else {
-                const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kStream);
-                v.w[blk][e][0] = x[0];
-                v.w[blk][e][1] = x[1];
+                v.w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc[block(i)], off, 0, STREAM ? 2 : 0);
             }
         }
     }
-    __device__ static inline void lds_k(K &k, int blk, const char *t, int lane) {
+    __device__ static inline void logits(float (&x)[kVals], const K &k, const Q &q) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            k.f[blk][i] = *reinterpret_cast<const bf16x8 *>(
-                t + chunk_at<kRowBytes>(16 * blk + (lane & 15), 4 * i + (lane >> 4)));
-    }
-    __device__ static inline void lds_v(V &v, int blk, const char *t, int lane) {
+        for (int b = 0; b < kKeyBlocks; ++b) {
+            Acc s;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = 16 * blk + 4 * (lane >> 4) + e, r = lane & 15;
-            if constexpr (PER == 8) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(t + chunk_at<kRowBytes>(row, r));
+            for (int e = 0; e < kAcc; ++e) s[e] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v.w[blk][e][i] = x[i];
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(
-                    t + chunk_at<kRowBytes>(row, r >> 1) + 8 * (r & 1));
-                v.w[blk][e][0] = x.x;
-                v.w[blk][e][1] = x.y;
-            }
+            for (int i = 0; i < kSteps; ++i) s = mfma(k.f[b][i], q.f[i], s);
+#pragma unroll
+            for (int e = 0; e < kAcc; ++e) x[kAcc * b + e] = s[e];
         }
-    }
-    __device__ static inline f32x4 logits(const K &k, int blk, const Q &q) {
-        f32x4 s{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) s = mfma32(k.f[blk][i], q.f[i], s);
-        return s;
     }
     // weights rounded to bf16, as the product's operand must be: each is off
     // by at most 2^-8 of itself, and the signs of these errors average out
     // over a row's tokens; o itself is rounded to bf16 at the end
-    struct P { bf16x8 f; };
-    __device__ static inline P weights(const f32x4 *p) { return P{acc_pair(p[0], p[1])}; }
-    __device__ static inline bf16x8 v_frag(const V &v, int c) {
-        const unsigned sel = c & 1 ? 0x07060302u : 0x05040100u;
+    struct P { bf16x8 f[kVals / 8]; };
+    __device__ static inline P weights(const float (&x)[kVals]) {
+        P p;
+#pragma unroll
+        for (int h = 0; h < kVals / 8; ++h) p.f[h] = cvt8(x + 8 * h);
+        return p;
+    }
+    __device__ static inline u32x4 v_frag(const V &v, int c, int h) {
         u32x4 x;
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                x[2 * blk + u] = __builtin_amdgcn_perm(v.w[blk][2 * u + 1][c >> 1],
-                                                       v.w[blk][2 * u][c >> 1], sel);
-        return __builtin_bit_cast(bf16x8, x);
+        for (int u = 0; u < 4; ++u)
+            x[u] = pick2(v.w[8 * h + 2 * u][c >> 1], v.w[8 * h + 2 * u + 1][c >> 1], c);
+        return x;
     }
-    __device__ static inline f32x4 pv(const V &v, int c, const P &p, f32x4 acc) {
-        return mfma32(v_frag(v, c), p.f, acc);
+    __device__ static inline Acc pv(const V &v, int c, const P &p, Acc acc) {
+#pragma unroll
+        for (int h = 0; h < kVals / 8; ++h)
+            acc = mfma(__builtin_bit_cast(bf16x8, v_frag(v, c, h)), p.f[h], acc);
+        return acc;
     }
     // an infinity or NaN among this lane's values
     __device__ static inline bool odd(const V &v) {
-        bool y = false;
+        unsigned y = 0;
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
+        for (int i = 0; i < kVals; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < PER / 2; ++i)
-                    y |= (v.w[blk][e][i] & 0x7F80u) == 0x7F80u ||
-                         (v.w[blk][e][i] & 0x7F800000u) == 0x7F800000u;
-        return y;
+            for (int j = 0; j < PER / 2; ++j) y |= odd2(v.w[i][j]);
+        return (y & 0x80008000u) != 0;
     }
-    // 1 where a value is an infinity or NaN other than `but` (an infinity's
-    // bits), times the 0 or 1 of ones, summed over the tile's tokens
-    __device__ static inline f32x4 count_odd(const V &v, int c, unsigned but, const P &ones) {
-        u32x4 x = __builtin_bit_cast(u32x4, v_frag(v, c));
+    // how many infinities and NaN other than `but` (an infinity's bits) each
+    // row meets where ones is 1
+    __device__ static inline Acc count_odd(const V &v, int c, unsigned but, const P &ones) {
+        Acc s;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const unsigned lo = x[i] & 0xFFFFu, hi = x[i] >> 16;
-            x[i] = ((lo & 0x7F80u) == 0x7F80u && lo != but ? 0x3F80u : 0u) |
-                   ((hi & 0x7F80u) == 0x7F80u && hi != but ? 0x3F800000u : 0u);
+        for (int e = 0; e < kAcc; ++e) s[e] = 0.f;
+#pragma unroll
+        for (int h = 0; h < kVals / 8; ++h) {
+            u32x4 x = v_frag(v, c, h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = mark2(x[i], but);
+            s = mfma(__builtin_bit_cast(bf16x8, x), ones.f[h], s);
         }
-        return mfma32z(__builtin_bit_cast(bf16x8, x), ones.f);
+        return s;
     }
     static constexpr unsigned kPlusInf = 0x7F80u, kMinusInf = 0xFF80u;
     __device__ static inline void clear_odd(V &v) {
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
+        for (int i = 0; i < kVals; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int i = 0; i < PER / 2; ++i) {
-                    const unsigned x = v.w[blk][e][i];
-                    v.w[blk][e][i] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) |
-                                     ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
-                }
+            for (int j = 0; j < PER / 2; ++j) v.w[i][j] = clear2(v.w[i][j]);
     }
 };
 
-template <int D> struct Tile<float, D> {
-    static constexpr int kBlocks = 1;
-    static constexpr int PER = D / 16;
-    static constexpr int kRowBytes = D * 4;
+template <int D> struct Tile<float, D, 16> {
+    static constexpr int kBlocks = 1, kTile = 16;
+    static constexpr int kGroups = 4, kVals = 4, PER = D / 16, kRowBytes = D * 4;
+    typedef f32x4 Acc;
+    static constexpr int kAcc = 4;
     struct Q { f32x4 f[D / 16]; };
-    struct K { f32x4 f[1][D / 16]; };
+    struct K { f32x4 f[D / 16]; };
     struct V { f32x4 f[4][PER / 4]; };
+    __device__ static inline int key(int i, int g) { return 4 * g + i; }
+    static constexpr int block(int) { return 0; }
+    // channels 64 (c / 4) + 4 m + c % 4: a load covers 256 bytes of a row
+    __device__ static inline int dim(int c, int i, int g) {
+        return 64 * (c >> 2) + 4 * (4 * g + i) + (c & 3);
+    }
     // a value parameter: the bit cast of a vector's element in place takes
     // the vector's first element
     __device__ static inline unsigned bits(float x) { return __builtin_bit_cast(unsigned, x); }
-    // channels 64 (c / 4) + 4 m + c % 4: a load covers 256 bytes of a row
-    __device__ static inline int dim(int c, int m) { return 64 * (c >> 2) + 4 * m + (c & 3); }
+    __device__ static inline f32x4 mfma(float a, float b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+    }
     __device__ static inline void load_q(Q &q, rsrc_t r, unsigned off, int lane) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) q.f[i] = bload16f(r, off + 64 * i + 16 * (lane >> 4));
     }
-    __device__ static inline void load_k(K &k, int, rsrc_t r, int lane) {
+    template <bool STREAM>
+    __device__ static inline void load_k(K &k, const char *kc, const Src (&src)[1], bool, int lane) {
+        const rsrc_t rs = make_rsrc(kc + src[0].at, src[0].bytes);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-            k.f[0][i] = __builtin_bit_cast(
-                f32x4, stream16(r, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4)));
+            k.f[i] = __builtin_bit_cast(
+                f32x4, load16<STREAM>(rs, (lane & 15) * kRowBytes + 64 * i + 16 * (lane >> 4)));
     }
-    __device__ static inline void load_v(V &v, int, rsrc_t r, int lane) {
+    template <bool STREAM>
+    __device__ static inline void load_v(V &v, const rsrc_t (&rsrc)[1], int lane) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int i = 0; i < PER / 4; ++i)
                 v.f[e][i] = __builtin_bit_cast(
-                    f32x4, stream16(r, (4 * (lane >> 4) + e) * kRowBytes + 256 * i +
-                                           16 * (lane & 15)));
+                    f32x4, load16<STREAM>(rsrc[0], (4 * (lane >> 4) + e) * kRowBytes + 256 * i +
+                                                       16 * (lane & 15)));
     }
-    __device__ static inline void lds_k(K &k, int, const char *t, int lane) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            k.f[0][i] = *reinterpret_cast<const f32x4 *>(
-                t + chunk_at<kRowBytes>(lane & 15, 4 * i + (lane >> 4)));
-    }
-    __device__ static inline void lds_v(V &v, int, const char *t, int lane) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < PER / 4; ++i)
-                v.f[e][i] = *reinterpret_cast<const f32x4 *>(
-                    t + chunk_at<kRowBytes>(4 * (lane >> 4) + e, 16 * i + (lane & 15)));
-    }
-    __device__ static inline f32x4 logits(const K &k, int, const Q &q) {
+    __device__ static inline void logits(float (&x)[4], const K &k, const Q &q) {
         f32x4 s{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s = __builtin_amdgcn_mfma_f32_16x16x4f32(k.f[0][i][e], q.f[i][e], s, 0, 0, 0);
-        return s;
+            for (int e = 0; e < 4; ++e) s = mfma(k.f[i][e], q.f[i][e], s);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = s[e];
     }
-    struct P { f32x4 f; };
-    __device__ static inline P weights(const f32x4 *p) { return P{p[0]}; }
+    struct P { float f[4]; };
+    __device__ static inline P weights(const float (&x)[4]) { return P{{x[0], x[1], x[2], x[3]}}; }
     __device__ static inline f32x4 pv(const V &v, int c, const P &p, f32x4 acc) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.f[e][c >> 2][c & 3], p.f[e], acc, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) acc = mfma(v.f[e][c >> 2][c & 3], p.f[e], acc);
         return acc;
     }
     __device__ static inline bool odd(const V &v) {
@@ -396,10 +442,8 @@ template <int D> struct Tile<float, D> {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < PER / 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    y |= (bits(v.f[e][i][j]) & 0x7F800000u) == 0x7F800000u;
+            for (int c = 0; c < PER; ++c)
+                y |= (bits(v.f[e][c >> 2][c & 3]) & 0x7F800000u) == 0x7F800000u;
         return y;
     }
     __device__ static inline f32x4 count_odd(const V &v, int c, unsigned but, const P &ones) {
@@ -407,8 +451,7 @@ template <int D> struct Tile<float, D> {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const unsigned u = bits(v.f[e][c >> 2][c & 3]);
-            const float x = (u & 0x7F800000u) == 0x7F800000u && u != but ? 1.f : 0.f;
-            s = __builtin_amdgcn_mfma_f32_16x16x4f32(x, ones.f[e], s, 0, 0, 0);
+            s = mfma((u & 0x7F800000u) == 0x7F800000u && u != but ? 1.f : 0.f, ones.f[e], s);
         }
         return s;
     }
@@ -417,40 +460,29 @@ template <int D> struct Tile<float, D> {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < PER / 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const unsigned u = bits(v.f[e][i][j]);
-                    v.f[e][i][j] = (u & 0x7F800000u) == 0x7F800000u ? 0.f : v.f[e][i][j];
-                }
+            for (int c = 0; c < PER; ++c) {
+                const unsigned u = bits(v.f[e][c >> 2][c & 3]);
+                v.f[e][c >> 2][c & 3] = (u & 0x7F800000u) == 0x7F800000u ? 0.f : v.f[e][c >> 2][c & 3];
+            }
     }
 };
 
-// Workgroup = (slot, key-value head, row block).  Wave w has row tile w % R
-// and takes every 4 / R-th tile of tokens, with m, l and o of its own, joined
-// through LDS at the end.
-//
-// R = 1: K and V go from HBM straight into the registers that MFMA reads: the
-// next tile to come is requested into a tile's registers as they fall free, K
-// after its logits are formed, V after its product.
-// R > 1: the waves of a share read the same tiles, which all threads bring
-// into LDS together, a stage (one tile per share) at a time: one stage is
-// worked on, the next is written beside it, and two more are on the way in
-// registers.
-template <typename T, int D, int R>
+// Workgroup = (slot, key-value head, row block of RW rows).  Its four waves
+// take the slot's tiles of tokens in turn, each with m, l and o of its own,
+// joined through LDS at the end.  K and V go from HBM straight into the
+// registers that MFMA reads: the next tile to come is requested into a tile's
+// registers as they fall free, K after its logits are formed, V after its
+// product.
+template <typename T, int D, int RW, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
-    using TL = Tile<T, D>;
-    constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = 16 * kBlocks;
-    constexpr int kPad = D + 4, kShares = kWaves / R;
-    constexpr int kTileBytes = kTile * TL::kRowBytes, kStage = kShares * 2 * kTileBytes;
-    constexpr int kOBytes = kWaves * 16 * kPad * (int)sizeof(float);
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
-    // the stages, and at the end every wave's o
-    __shared__ __align__(16) char lds[R > 1 && 2 * kStage > kOBytes ? 2 * kStage : kOBytes];
-    float(*so)[16][kPad] = reinterpret_cast<float(*)[16][kPad]>(lds);
+    using TL = Tile<T, D, RW>;
+    constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = TL::kTile, kVals = TL::kVals;
+    constexpr int kPad = D + 4;
+    __shared__ float sm[kWaves][RW], sl[kWaves][RW];
+    __shared__ __align__(16) float so[kWaves][RW][kPad];
     const AttnArgs &a = k.a;
-    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, lg = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), rt = w % R, share = w / R;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane % RW, g = lane / RW;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the row blocks of one (slot, head) follow each other on one XCD, which
     // holds their K and V in its L2 (workgroups go to the eight XCDs in turn)
     const int wg = blockIdx.x;
@@ -465,21 +497,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
 
     // this lane's query row and what it attends to
-    const int rows = a.n * a.G, row0 = rb * 16 * R, row = row0 + 16 * rt + r16;
+    const int rows = a.n * a.G, row0 = rb * RW, row = row0 + r;
     Span sp{0, 0};
     typename TL::Q q;
     {
         const size_t qb = (size_t)b * a.n * a.Hq * D;
         const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + qb, 0xFFFFFFFFu);
-        const int t = row < rows ? row / a.G : 0, g = row < rows ? row % a.G : 0;
+        const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0;
         if (row < rows) sp = token_span(len, a.n, a.window, t);
-        TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + g) * (D * (unsigned)sizeof(T)), lane);
+        TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + hg) * (D * (unsigned)sizeof(T)), lane);
     }
     // the block's tokens: what its rows attend to, within the slot
-    const int t_first = row0 / a.G;
-    const int t_last = ((row0 + 16 * R < rows ? row0 + 16 * R : rows) - 1) / a.G;
-    const Span first = token_span(len, a.n, a.window, t_first);
-    const Span last = token_span(len, a.n, a.window, t_last);
+    const Span first = token_span(len, a.n, a.window, row0 / a.G);
+    const Span last = token_span(len, a.n, a.window,
+                                 ((row0 + RW < rows ? row0 + RW : rows) - 1) / a.G);
     const int c_lo = seq.lo + (slot - sl_.first) * sl_.chunk;
     const int c_hi = c_lo + sl_.chunk < len ? c_lo + sl_.chunk : len;
     const int k_lo = first.lo > c_lo ? first.lo : c_lo, k_hi = last.hi < c_hi ? last.hi : c_hi;
@@ -491,34 +522,42 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
     const float c1 = a.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
-    f32x4 acc[PER];
+    typename TL::Acc acc[PER];
 #pragma unroll
-    for (int c = 0; c < PER; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < PER; ++c)
+#pragma unroll
+        for (int e = 0; e < TL::kAcc; ++e) acc[c][e] = 0.f;
+
+    // the largest of a value over a row's lanes, and the sum
+    auto row_max = [](float x) { return swap_max32(RW == 16 ? swap_max16(x) : x); };
+    auto row_sum = [](float x) { return swap_sum32(RW == 16 ? swap_sum16(x) : x); };
 
     // One tile's logits (before scaling) and values into m, l and o.  full:
     // every row attends to all of it; here: which of its blocks are there.
-    auto absorb = [&](int j0, f32x4 (&x)[kBlocks], typename TL::V &vf, bool full,
+    // (Past the length and on absent pages V is zeros.)
+    auto absorb = [&](int j0, float (&x)[kVals], typename TL::V &vf, bool full,
                       const bool (&here)[kBlocks]) {
         float top = -INFINITY;
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) {
+        for (int i = 0; i < kVals; ++i) x[i] *= c1;
+        if (k.logits && row < rows) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[blk][e] *= c1;
-            if (k.logits && row < rows && here[blk])
-                *reinterpret_cast<f32x4 *>(k.logits +
-                                           (((size_t)b * a.Hkv + h) * rows + row) * k.cap32 + j0 +
-                                           16 * blk + 4 * lg) = x[blk];
-            if (!full) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + 16 * blk + 4 * lg + e;
-                    x[blk][e] = here[blk] && j >= sp.lo && j < sp.hi ? x[blk][e] : -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, x[blk][e]);
+            for (int i = 0; i < kVals; i += 4)
+                if (here[TL::block(i)])
+                    *reinterpret_cast<f32x4 *>(k.logits +
+                                               (((size_t)b * a.Hkv + h) * rows + row) * k.cap32 + j0 +
+                                               TL::key(i, g)) = f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
         }
-        const float mn = fmaxf(m, swap_max32(swap_max16(top))), ms = finite_top(mn);
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < kVals; ++i) {
+                const int j = j0 + TL::key(i, g);
+                x[i] = here[TL::block(i)] && j >= sp.lo && j < sp.hi ? x[i] : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) top = fmaxf(top, x[i]);
+        const float mn = fmaxf(m, row_max(top)), ms = finite_top(mn);
         if (__builtin_amdgcn_ballot_w64(mn != m)) {
             const float al = exp2_(m - ms);
             l *= al;
@@ -527,35 +566,34 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
             m = mn;
         }
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[blk][e] = exp2_(x[blk][e] - ms);
-                l += x[blk][e];
-            }
+        for (int i = 0; i < kVals; ++i) {
+            x[i] = exp2_(x[i] - ms);
+            l += x[i];
+        }
         const typename TL::P p = TL::weights(x);
-        // Where a tile is attended to by some rows only, a weight of zero must
-        // not meet an infinity or NaN.  Such values are taken out of V, and a
+        // Where some row does not attend to a token that is there, its weight of
+        // zero must not meet an infinity or NaN.  Such values are taken out of V, and a
         // row that attends to one gets +inf, -inf or (both, or NaN) their
         // sum in that channel.
-        if (!full && __builtin_amdgcn_ballot_w64(TL::odd(vf))) {
-            f32x4 in[kBlocks];
+        const int j1 = j0 + kTile < len ? j0 + kTile : len;
+        if ((j0 < all_lo || j1 > all_hi) && __builtin_amdgcn_ballot_w64(TL::odd(vf))) {
+            float in[kVals];
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + 16 * blk + 4 * lg + e;
-                    in[blk][e] = j >= sp.lo && j < sp.hi ? 1.f : 0.f;
-                }
+            for (int i = 0; i < kVals; ++i) {
+                const int j = j0 + TL::key(i, g);
+                in[i] = j >= sp.lo && j < sp.hi ? 1.f : 0.f;
+            }
             const typename TL::P ones = TL::weights(in);
 #pragma unroll
             for (int c = 0; c < PER; ++c) {
-                const f32x4 up = TL::count_odd(vf, c, TL::kMinusInf, ones);
-                const f32x4 down = TL::count_odd(vf, c, TL::kPlusInf, ones);
+                const typename TL::Acc up = TL::count_odd(vf, c, TL::kMinusInf, ones);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[c][e] += (up[e] > 0.f ? INFINITY : 0.f) + (down[e] > 0.f ? -INFINITY : 0.f);
+                for (int e = 0; e < TL::kAcc; ++e) acc[c][e] += up[e] > 0.f ? INFINITY : 0.f;
                 __builtin_amdgcn_sched_barrier(0);   // a rare path: few registers
+                const typename TL::Acc down = TL::count_odd(vf, c, TL::kPlusInf, ones);
+#pragma unroll
+                for (int e = 0; e < TL::kAcc; ++e) acc[c][e] += down[e] > 0.f ? -INFINITY : 0.f;
+                __builtin_amdgcn_sched_barrier(0);
             }
             TL::clear_odd(vf);
         }
@@ -563,13 +601,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         for (int c = 0; c < PER; ++c) acc[c] = TL::pv(vf, c, p, acc[c]);
     };
 
-    // Pages of the next 64 tiles from tile i0 on, `step` apart, one per lane
-    // (of the table's entries past the length too, which block_src leaves out).
-    constexpr int step = R == 1 ? kShares : 1;
+    // Pages of this wave's next 64 tiles, one per lane (of the table's
+    // entries past the length too, which block_src leaves out).
     const int cap = a.map.max_pages << a.map.page_shift;
     int pg[kBlocks];
     auto load_pages = [&](int i0) {
-        const int j = (tile0 + i0 + step * lane) * kTile;
+        const int j = (tile0 + i0 + kWaves * lane) * kTile;
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
             pg[blk] = j + 16 * blk < cap ? page_of(a.map, b, j + 16 * blk) : -1;
@@ -578,7 +615,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     // past the length, on an absent page or past the last tile: such loads
     // give zeros)
     const size_t page_bytes = (size_t)TL::kRowBytes << a.map.page_shift;
-    struct Src { size_t at; unsigned bytes; };
     auto block_src = [&](int i, int at, int blk) {
         const int page = __builtin_amdgcn_readlane(pg[blk], at);
         const int j = (tile0 + i) * kTile + 16 * blk;
@@ -590,198 +626,106 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         if (!some) s.at = 0;
         return s;
     };
-    if constexpr (R == 1) {
-        // D = 64: two tiles on their way, in two sets of registers.  D = 128:
-        // one, as a second set's 64 registers would spill (64 contexts 125 ->
-        // 136 us with it; D = 64 in fp32, 8 contexts: 35 -> 31 us).
-        constexpr bool kTwo = D == 64;
-        struct Ahead {
-            typename TL::K kf;
-            typename TL::V vf;
-            Src src[kBlocks];
-        } s0, s1;
-        int at = 0;                             // tiles whose loads have been issued
-        auto load_k = [&](Ahead &s) {
-            if ((at & 63) == 0) load_pages(share + kShares * at);
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) {
-                s.src[blk] = block_src(share + kShares * at, at & 63, blk);
-                TL::load_k(s.kf, blk, make_rsrc(kc + s.src[blk].at, s.src[blk].bytes), lane);
-            }
-            ++at;
-        };
-        auto load_v = [&](Ahead &s) {
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk)
-                TL::load_v(s.vf, blk, make_rsrc(vc + s.src[blk].at, s.src[blk].bytes), lane);
-        };
-        auto work = [&](int i, Ahead &s) {
-            const int j0 = (tile0 + i) * kTile;
-            f32x4 x[kBlocks];
-            bool here[kBlocks], full = j0 >= all_lo && j0 + kTile <= all_hi;
-#pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) {
-                x[blk] = TL::logits(s.kf, blk, q);
-                here[blk] = s.src[blk].bytes != 0;
-                full &= here[blk];
-            }
-            load_k(s);
-            absorb(j0, x, s.vf, full, here);
-            load_v(s);
-        };
-        load_k(s0);
-        load_v(s0);
-        if constexpr (kTwo) {
-            load_k(s1);
-            load_v(s1);
-        }
-        for (int i = share; i < tiles; i += kShares) {
-            work(i, s0);
-            if constexpr (kTwo) {
-                i += kShares;
-                if (i >= tiles) break;
-                work(i, s1);
-            }
-        }
-    } else {
-        constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTileBytes / 16 / kThreads;
-        static_assert(kUnits * kThreads * 16 == kTileBytes && 64 / kChunks <= 16,
-                      "threads cover a tile, a wave's rows lie in one block");
-        // a stage on its way: 16 bytes of K and of V per thread, unit and
-        // share, and which blocks of this wave's own tile are there
-        struct Stage {
-            u32x4 kv[kShares][kUnits][2];
-            bool here[kBlocks];
-        };
-        int paged = 0;                          // the tile that lane 0 of pg stands for
-        load_pages(0);
-        auto load = [&](int it, Stage &s) {
-#pragma unroll
-            for (int x = 0; x < kShares; ++x) {
-                const int i = it * kShares + x;
-                if (i >= paged + 64) {
-                    paged = i;
-                    load_pages(i);
-                }
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const int unit = tid + kThreads * u, r = unit / kChunks;
-                    const int blk = __builtin_amdgcn_readfirstlane(r >> 4);
-                    const Src src = kBlocks == 1 || blk == 0 ? block_src(i, i - paged, 0)
-                                                             : block_src(i, i - paged, kBlocks - 1);
-                    const unsigned off = (r & 15) * TL::kRowBytes + unit % kChunks * 16;
-                    s.kv[x][u][0] = __builtin_amdgcn_raw_buffer_load_b128(
-                        make_rsrc(kc + src.at, src.bytes), off, 0, 0);
-                    s.kv[x][u][1] = __builtin_amdgcn_raw_buffer_load_b128(
-                        make_rsrc(vc + src.at, src.bytes), off, 0, 0);
-                }
-                if (x == share)
-#pragma unroll
-                    for (int blk = 0; blk < kBlocks; ++blk)
-                        s.here[blk] = block_src(i, i - paged, blk).bytes != 0;
-            }
-        };
-        auto store = [&](char *to, const Stage &s) {
-#pragma unroll
-            for (int x = 0; x < kShares; ++x)
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const int unit = tid + kThreads * u;
-                    const int at = 2 * x * kTileBytes +
-                                   chunk_at<TL::kRowBytes>(unit / kChunks, unit % kChunks);
-                    *reinterpret_cast<u32x4 *>(to + at) = s.kv[x][u][0];
-                    *reinterpret_cast<u32x4 *>(to + at + kTileBytes) = s.kv[x][u][1];
-                }
-        };
+    // D = 64: two tiles on their way, in two sets of registers.  D = 128: one,
+    // as a second set's 64 registers would spill (64 contexts 125 -> 136 us
+    // with it; D = 64 in fp32, 8 contexts: 35 -> 31 us).
+    constexpr bool kTwo = D == 64;
+    struct Ahead {
         typename TL::K kf;
         typename TL::V vf;
-        auto work = [&](int it, const char *from, const bool (&here)[kBlocks]) {
-            const int j0 = (tile0 + it * kShares + share) * kTile;
-            const char *t = from + 2 * share * kTileBytes;
-            f32x4 x[kBlocks];
-            bool full = j0 >= all_lo && j0 + kTile <= all_hi;
+        Src src[kBlocks];
+    } s0, s1;
+    int at = 0;                                 // tiles whose loads have been issued
+    auto load_k = [&](Ahead &s) {
+        if ((at & 63) == 0) load_pages(w + kWaves * at);
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) {
-                TL::lds_k(kf, blk, t, lane);
-                TL::lds_v(vf, blk, t + kTileBytes, lane);
-                full &= here[blk];
-            }
+        for (int blk = 0; blk < kBlocks; ++blk)
+            s.src[blk] = block_src(w + kWaves * at, at & 63, blk);
+        TL::template load_k<STREAM>(s.kf, kc, s.src, a.map.page_shift > 4, lane);
+        ++at;
+    };
+    auto load_v = [&](Ahead &s) {
+        rsrc_t rs[kBlocks];
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) x[blk] = TL::logits(kf, blk, q);
-            absorb(j0, x, vf, full, here);
-        };
-        const int its = (tiles + kShares - 1) / kShares;
-        Stage s0, s1;
-        bool here0[kBlocks], here1[kBlocks];
-        auto put = [&](char *to, const Stage &s, bool (&here)[kBlocks]) {
-            store(to, s);
+        for (int blk = 0; blk < kBlocks; ++blk) rs[blk] = make_rsrc(vc + s.src[blk].at, s.src[blk].bytes);
+        TL::template load_v<STREAM>(s.vf, rs, lane);
+    };
+    auto work = [&](int i, Ahead &s) {
+        const int j0 = (tile0 + i) * kTile;
+        float x[kVals];
+        bool here[kBlocks], full = j0 >= all_lo && j0 + kTile <= all_hi;
+        TL::logits(x, s.kf, q);
 #pragma unroll
-            for (int blk = 0; blk < kBlocks; ++blk) here[blk] = s.here[blk];
-        };
-        load(0, s0);
-        load(1, s1);
-        put(lds, s0, here0);
-        load(2, s0);
-        __syncthreads();
-        for (int it = 0; it < its; it += 2) {
-            work(it, lds, here0);
-            put(lds + kStage, s1, here1);
-            load(it + 3, s1);
-            __syncthreads();
-            if (it + 1 >= its) break;
-            work(it + 1, lds + kStage, here1);
-            put(lds, s0, here0);
-            load(it + 4, s0);
-            __syncthreads();
+        for (int blk = 0; blk < kBlocks; ++blk) {
+            here[blk] = s.src[blk].bytes != 0;
+            full &= here[blk];
         }
-        __syncthreads();                        // the stages make room for o
+        load_k(s);
+        absorb(j0, x, s.vf, full, here);
+        load_v(s);
+    };
+    load_k(s0);
+    load_v(s0);
+    if constexpr (kTwo) {
+        load_k(s1);
+        load_v(s1);
+    }
+    for (int i = w; i < tiles; i += kWaves) {
+        work(i, s0);
+        if constexpr (kTwo) {
+            i += kWaves;
+            if (i >= tiles) break;
+            work(i, s1);
+        }
     }
 
-    // join the waves of a row tile: every wave's o in units of their common
-    // maximum, summed row by row
-    l = swap_sum32(swap_sum16(l));
-    if (lg == 0) {
-        sm[w][r16] = m;
-        sl[w][r16] = l;
+    // join the waves: every wave's o in units of their common maximum, summed
+    // row by row
+    l = row_sum(l);
+    if (g == 0) {
+        sm[w][r] = m;
+        sl[w][r] = l;
     }
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kShares; ++i) top = fmaxf(top, sm[rt + R * i][r16]);
+    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sm[i][r]);
     const float f = exp2_(m - finite_top(top));
-    // acc[c][e] is channel dim(c, 4 lg + e); four at a time
+    // acc[c][e] is channel dim(c, e, g); those of adjacent c lie together
+    constexpr int kRun = PER < 4 ? PER : 4;
+    typedef float run_t __attribute__((ext_vector_type(kRun)));
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < TL::kAcc; ++e)
 #pragma unroll
-        for (int c = 0; c < PER; c += 4)
-            *reinterpret_cast<f32x4 *>(&so[w][r16][TL::dim(c, 4 * lg + e)]) =
-                f32x4{acc[c][e] * f, acc[c + 1][e] * f, acc[c + 2][e] * f, acc[c + 3][e] * f};
+        for (int c = 0; c < PER; c += kRun) {
+            run_t y;
+#pragma unroll
+            for (int u = 0; u < kRun; ++u) y[u] = acc[c + u][e] * f;
+            *reinterpret_cast<run_t *>(&so[w][r][TL::dim(c, e, g)]) = y;
+        }
     __syncthreads();
     // 16 threads per row, four channels at a time
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int lr = tid >> 4, orow = row0 + 16 * i + lr;
+    for (int i = 0; i < RW / 16; ++i) {
+        const int lr = 16 * i + (tid >> 4), orow = row0 + lr;
         if (orow >= rows) break;
         float rtop = -INFINITY, rl = 0.f;
 #pragma unroll
-        for (int x = 0; x < kShares; ++x) rtop = fmaxf(rtop, sm[i + R * x][lr]);
+        for (int x = 0; x < kWaves; ++x) rtop = fmaxf(rtop, sm[x][lr]);
 #pragma unroll
-        for (int x = 0; x < kShares; ++x)
-            rl += sl[i + R * x][lr] * exp2_(sm[i + R * x][lr] - finite_top(rtop));
-        const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * 16 * R +
-                            16 * i + lr;
+        for (int x = 0; x < kWaves; ++x) rl += sl[x][lr] * exp2_(sm[x][lr] - finite_top(rtop));
+        const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * RW + lr;
         const bool alone = sl_.count == 1;
         if ((!alone || k.logits) && (tid & 15) == 0) k.ml[part] = float2{rtop, rl};
         const float inv = 1.f / rl;
-        const int t = orow / a.G, g = orow % a.G;
-        T *o = static_cast<T *>(a.o) + (((size_t)b * a.n + t) * a.Hq + h * a.G + g) * D;
+        const int t = orow / a.G, hg = orow % a.G;
+        T *o = static_cast<T *>(a.o) + (((size_t)b * a.n + t) * a.Hq + h * a.G + hg) * D;
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
             const int d = 64 * u + 4 * (tid & 15);
-            f32x4 y = *reinterpret_cast<const f32x4 *>(&so[i][lr][d]);
+            f32x4 y = *reinterpret_cast<const f32x4 *>(&so[0][lr][d]);
 #pragma unroll
-            for (int x = 1; x < kShares; ++x)
-                y += *reinterpret_cast<const f32x4 *>(&so[i + R * x][lr][d]);
+            for (int x = 1; x < kWaves; ++x) y += *reinterpret_cast<const f32x4 *>(&so[x][lr][d]);
             if (!alone) {
                 *reinterpret_cast<f32x4 *>(k.po + part * D + d) = y;
             } else {
@@ -820,13 +764,13 @@ __device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, i
 // scores, further workgroups each add the weights of 1,024 tokens of a
 // (sequence, head): a thread sums 2^{x - m} / l over the rows, in their order,
 // for four tokens.
-template <typename T, int D, int R>
+template <typename T, int D, int RW>
 __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins,
                                                         long long score_blocks) {
     constexpr int kAcross = D / 4, kGroups = kThreads / kAcross;
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, rows = a.n * a.G;
-    const size_t stride = (size_t)k.plan.units * 16 * R;
+    const size_t stride = (size_t)k.plan.units * RW;
     if (blockIdx.x < joins) {
         __shared__ __align__(16) float so[kGroups][D];
         const long long q = blockIdx.x;
@@ -834,9 +778,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
         const int2 sc = k.sched[b];
         if (sc.y == 1) return;
         const int h = hq / a.G, row = t * a.G + hq % a.G;
-        const int rb = row / (16 * R);
-        const size_t part = (size_t)sc.x * stride + ((size_t)h * k.plan.row_blocks + rb) * 16 * R +
-                            row % (16 * R);
+        const int rb = row / RW;
+        const size_t part = (size_t)sc.x * stride + ((size_t)h * k.plan.row_blocks + rb) * RW +
+                            row % RW;
         const float2 tot = join_ml(k.ml, part, stride, sc.y);
         const int d = 4 * (tid % kAcross), grp = tid / kAcross;
         f32x4 y{0.f, 0.f, 0.f, 0.f};
@@ -879,8 +823,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
             for (int r = w; r < nr; r += kWaves) {
                 const int row = r0 + r;
                 const size_t part = (size_t)sc.x * stride +
-                                    ((size_t)h * k.plan.row_blocks + row / (16 * R)) * 16 * R +
-                                    row % (16 * R);
+                                    ((size_t)h * k.plan.row_blocks + row / RW) * RW +
+                                    row % RW;
                 const float2 x = join_ml(k.ml, part, stride, sc.y);
                 if ((tid & 63) == 0) st[r] = float2{x.x, x.y == 0.f ? 0.f : 1.f / x.y};
             }
@@ -910,14 +854,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins
     }
 }
 
-template <typename T, int D, int R>
+template <typename T, int D, int RW>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
-    const WsMap w = ws_map(a.B, a.n, a.G, a.Hkv, D, R, cap, a.scores != nullptr);
+    const WsMap w = ws_map(a.B, a.n, a.G, a.Hkv, D, RW, cap, a.scores != nullptr);
     char *ws = static_cast<char *>(a.ws);
     KArgs k{};
     k.a = a;
-    k.plan = make_plan(a.B, a.n, a.G, a.Hkv, R, cap);
+    k.plan = make_plan(a.B, a.n, a.G, a.Hkv, RW, cap);
     k.sched = reinterpret_cast<int2 *>(ws + w.sched);
     k.ml = reinterpret_cast<float2 *>(ws + w.ml);
     k.po = reinterpret_cast<float *>(ws + w.o);
@@ -925,24 +869,24 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     k.cap32 = (cap + 31) / 32 * 32;
     k.parts = k.plan.max_slots > a.B;
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
-    attn_kernel<T, D, R><<<(unsigned)(pairs * k.plan.row_blocks), kThreads, 0, s>>>(k);
+    const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
+    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, true><<<grid, kThreads, 0, s>>>(k);
+    else                        attn_kernel<T, D, RW, false><<<grid, kThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long long joins = k.parts ? (long long)a.B * a.n * a.Hq : 0;
     long long score_blocks = a.scores ? (long long)a.B * a.Hkv * ((k.cap32 + 1023) / 1024) : 0;
     if (score_blocks > (1 << 20)) score_blocks = 1 << 20;
     if (joins + score_blocks == 0) return hipSuccess;
-    join_kernel<T, D, R><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(k, joins, score_blocks);
+    join_kernel<T, D, RW><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(k, joins, score_blocks);
     return hipGetLastError();
 }
 
-template <typename T, int D>
-hipError_t launch_r(const AttnArgs &a, hipStream_t s) {
-    switch (row_tiles((long long)a.n * a.G)) {
-    case 1:  return launch<T, D, 1>(a, s);
-    case 2:  return launch<T, D, 2>(a, s);
-    default: return launch<T, D, 4>(a, s);
-    }
+template <int D>
+hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
+    if (!bf16_io) return launch<float, D, 16>(a, s);
+    return block_rows(true, (long long)a.n * a.G) == 32 ? launch<bf16, D, 32>(a, s)
+                                                        : launch<bf16, D, 16>(a, s);
 }
 
 }  // namespace
@@ -950,12 +894,14 @@ hipError_t launch_r(const AttnArgs &a, hipStream_t s) {
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
                            bool with_scores) {
     const int G = Hq / Hkv;
-    return ws_map(B, n, G, Hkv, D, row_tiles((long long)n * G), capacity, with_scores).total;
+    // one size for both dtypes
+    const size_t x = ws_map(B, n, G, Hkv, D, block_rows(true, (long long)n * G), capacity, with_scores).total;
+    const size_t y = ws_map(B, n, G, Hkv, D, block_rows(false, (long long)n * G), capacity, with_scores).total;
+    return x > y ? x : y;
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
-    if (bf16_io) return D == 128 ? launch_r<bf16, 128>(a, s) : launch_r<bf16, 64>(a, s);
-    return D == 128 ? launch_r<float, 128>(a, s) : launch_r<float, 64>(a, s);
+    return D == 128 ? launch_d<128>(bf16_io, a, s) : launch_d<64>(bf16_io, a, s);
 }
 
 }  // namespace gdr
