@@ -759,48 +759,79 @@ __device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, i
     return float2{all, l};
 }
 
-// Joins the slots' parts, one workgroup per query row (the first `joins`
-// workgroups): D / 4 threads across a row, the others across slots.  With
-// scores, further workgroups each add the weights of 1,024 tokens of a
-// (sequence, head): a thread sums 2^{x - m} / l over the rows, in their order,
-// for four tokens.
+// m, l and four channels of o of some slots.
+struct Joined {
+    float m, l;
+    f32x4 y;
+    __device__ inline void add(float mo, float lo, f32x4 yo) {
+        const float mn = fmaxf(m, mo), ms = finite_top(mn);
+        const float f = exp2_(m - ms), fo = exp2_(mo - ms);
+        l = l * f + lo * fo;
+        y = y * f + yo * fo;
+        m = mn;
+    }
+};
+
+// Joins the slots' parts, `join_wgs` workgroups per sequence taking its rows
+// in turn: D / 4 lanes across a row, the others across slots, a row per wave
+// or (many slots) per workgroup.  With scores, further workgroups each add
+// the weights of 1,024 tokens of a (sequence, head): a thread sums
+// 2^{x - m} / l over the rows, in their order, for four tokens.
 template <typename T, int D, int RW>
-__global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, long long joins,
+__global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, long long joins,
                                                         long long score_blocks) {
-    constexpr int kAcross = D / 4, kGroups = kThreads / kAcross;
+    constexpr int kAcross = D / 4, kGroups = 64 / kAcross;
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, rows = a.n * a.G;
     const size_t stride = (size_t)k.plan.units * RW;
     if (blockIdx.x < joins) {
-        __shared__ __align__(16) float so[kGroups][D];
-        const long long q = blockIdx.x;
-        const int hq = (int)(q % a.Hq), t = (int)(q / a.Hq % a.n), b = (int)(q / a.Hq / a.n);
+        __shared__ __align__(16) Joined other[kWaves][kAcross];
+        const int b = (int)(blockIdx.x / join_wgs), part_of = (int)(blockIdx.x % join_wgs);
         const int2 sc = k.sched[b];
         if (sc.y == 1) return;
-        const int h = hq / a.G, row = t * a.G + hq % a.G;
-        const int rb = row / RW;
-        const size_t part = (size_t)sc.x * stride + ((size_t)h * k.plan.row_blocks + rb) * RW +
-                            row % RW;
-        const float2 tot = join_ml(k.ml, part, stride, sc.y);
-        const int d = 4 * (tid % kAcross), grp = tid / kAcross;
-        f32x4 y{0.f, 0.f, 0.f, 0.f};
+        const int lane = tid & 63, w = tid >> 6, d = 4 * (lane % kAcross), grp = lane / kAcross;
+        const bool together = sc.y > 16;       // four waves to a row
+        const int each = together ? kWaves : 1, per = together ? 1 : kWaves;
+        for (int q0 = part_of * per; q0 < a.n * a.Hq; q0 += join_wgs * per) {
+            const int q = q0 + (together ? 0 : w);
+            Joined x{-INFINITY, 0.f, f32x4{0.f, 0.f, 0.f, 0.f}};
+            if (q < a.n * a.Hq) {
+                const int hq = q % a.Hq, h = hq / a.G, row = q / a.Hq * a.G + hq % a.G;
+                const size_t part = (size_t)sc.x * stride +
+                                    ((size_t)h * k.plan.row_blocks + row / RW) * RW + row % RW;
 #pragma unroll 4
-        for (int i = grp; i < sc.y; i += kGroups) {
-            const float f = exp2_(k.ml[part + i * stride].x - tot.x);
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(k.po + (part + i * stride) * D + d);
-            y += x * f;
+                for (int i = (together ? w : 0) * kGroups + grp; i < sc.y; i += kGroups * each) {
+                    const size_t at = part + i * stride;
+                    const float2 ml = k.ml[at];
+                    x.add(ml.x, ml.y, *reinterpret_cast<const f32x4 *>(k.po + at * D + d));
+                }
+            }
+#pragma unroll
+            for (int m = kAcross; m < 64; m <<= 1)
+                x.add(__shfl_xor(x.m, m), __shfl_xor(x.l, m),
+                      f32x4{__shfl_xor(x.y.x, m), __shfl_xor(x.y.y, m), __shfl_xor(x.y.z, m),
+                            __shfl_xor(x.y.w, m)});
+            if (together) {
+                __syncthreads();               // the last row's have been read
+                if (grp == 0) other[w][lane] = x;
+                __syncthreads();
+                if (w > 0) continue;
+#pragma unroll
+                for (int i = 1; i < kWaves; ++i) {
+                    const Joined o = other[i][lane % kAcross];
+                    x.add(o.m, o.l, o.y);
+                }
+            }
+            if (q < a.n * a.Hq && grp == 0) {
+                const float inv = 1.f / x.l;
+                f32x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = x.l == 0.f ? 0.f : x.y[e] * inv;
+                T *o = static_cast<T *>(a.o) + ((size_t)b * a.n * a.Hq + q) * D + d;
+                if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(o) = cvt4(y);
+                else                          *reinterpret_cast<f32x4 *>(o) = y;
+            }
         }
-        *reinterpret_cast<f32x4 *>(&so[grp][d]) = y;
-        __syncthreads();
-        if (grp > 0) return;
-#pragma unroll
-        for (int i = 1; i < kGroups; ++i) y += *reinterpret_cast<const f32x4 *>(&so[i][d]);
-        const float inv = 1.f / tot.y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = tot.y == 0.f ? 0.f : y[e] * inv;
-        T *o = static_cast<T *>(a.o) + q * D + d;
-        if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4 *>(o) = cvt4(y);
-        else                          *reinterpret_cast<f32x4 *>(o) = y;
         return;
     }
     constexpr int kRows = 64, kTokens = 4 * kThreads;
@@ -874,11 +905,17 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     else                        attn_kernel<T, D, RW, false><<<grid, kThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const long long joins = k.parts ? (long long)a.B * a.n * a.Hq : 0;
+    // about 4,096 workgroups join, and at most one per row: sequences in one
+    // slot, often most of them, are left at once
+    int join_wgs = a.n * a.Hq;
+    const int spread = a.B < 4096 ? 4096 / a.B : 1;
+    if (join_wgs > spread) join_wgs = spread;
+    const long long joins = k.parts ? (long long)a.B * join_wgs : 0;
     long long score_blocks = a.scores ? (long long)a.B * a.Hkv * ((k.cap32 + 1023) / 1024) : 0;
     if (score_blocks > (1 << 20)) score_blocks = 1 << 20;
     if (joins + score_blocks == 0) return hipSuccess;
-    join_kernel<T, D, RW><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(k, joins, score_blocks);
+    join_kernel<T, D, RW><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(k, join_wgs, joins,
+                                                                              score_blocks);
     return hipGetLastError();
 }
 
