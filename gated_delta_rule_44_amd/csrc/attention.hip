@@ -40,24 +40,33 @@ __device__ inline Span seq_span(int len, int n, int window) {
 }
 
 // How the cached tokens are shared out.  Every sequence's span is cut into
-// chunks of C tokens, the same C for all, so that a long sequence among short
-// ones is spread over as many workgroups as its length asks for; C follows
-// from the lengths on the device, such that about kTargetWgs workgroups
-// have work.  Chunks are numbered over the sequences ("slots"); a sequence
-// without tokens has one, which writes its zeros.
-constexpr int kTargetWgs = 1024;
+// chunks of about C tokens, the same C for all, so that a long sequence among
+// short ones is spread over as many workgroups as its length asks for; C
+// follows from the lengths on the device.  Chunks are numbered over the
+// sequences ("slots"); a sequence without tokens has one, which writes its
+// zeros.
+//   The card holds kResident workgroups at once, and workgroups of a like
+// size end together: with sum ceil(len / C) <= total / C + B slots, C is taken
+// such that they fill the card once, or twice or four times where B
+// sequences' last chunks would leave over a quarter of it idle (64 rows a
+// head, 16 contexts: 77 us with C for 1,024 workgroups, XX us so; 130,001
+// tokens: 57 and XX us).  With more sequences than that, C is for 1,024.
+constexpr int kResident = 512;
 constexpr int kMinChunk = 512;
 struct Plan {
     int units;            // workgroups of one slot: key-value heads x row blocks
     int row_blocks;       // blocks of RW rows
-    int want_slots;       // slots aimed at
+    int want_slots;       // total / C
     int max_slots;        // bound on the slots there can be: sum ceil(len / C) <= want + B
 };
 Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
     Plan p;
     p.row_blocks = (n * G + rw - 1) / rw;
     p.units = Hkv * p.row_blocks;
-    p.want_slots = p.units >= kTargetWgs ? 1 : kTargetWgs / p.units;
+    p.want_slots = 2 * kResident / p.units;
+    for (int k = 4; k >= 1; k >>= 1)
+        if (4LL * B * p.units <= k * kResident) p.want_slots = k * kResident / p.units - B;
+    if (p.want_slots < 1) p.want_slots = 1;
     const long long by_len = (capacity + kMinChunk - 1) / kMinChunk * B;
     const long long bound = (long long)p.want_slots + B;
     p.max_slots = (int)(by_len < bound ? (by_len < B ? B : by_len) : bound);
@@ -125,14 +134,20 @@ __device__ inline N group_scan(N x, N &total, N *lds) {
     return before + incl - x;
 }
 
-struct Slot { int b, first, count, chunk; };      // sequence, its first slot, its slots, tokens of one
+// A value that is the same in all lanes, for a scalar register.
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+struct Slot { int b, len, first, count, chunk; };  // sequence, its first slot, its slots, tokens of one
 // The sequence that slot s belongs to (b = -1: past the last slot).  Thread
 // i of the workgroup looks after sequences i per .. i per + per - 1.
 __device__ inline Slot find_slot(const KArgs &k, int s) {
     // too short a table for a second slot: slot and sequence are one
-    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 29};
+    if (!k.parts) {
+        if (s >= k.a.B) return Slot{-1, 0, 0, 0, 0};
+        return Slot{s, uniform(cached_len(k.a.seq_lens, s, k.a.map)), s, 1, 1 << 29};
+    }
     __shared__ long long lds64[kWaves];
-    __shared__ int lds32[kWaves], found[4];
+    __shared__ int lds32[kWaves], found[5];
     const AttnArgs &a = k.a;
     const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
     long long sum = 0, total;
@@ -154,11 +169,12 @@ __device__ inline Slot find_slot(const KArgs &k, int s) {
     int at = group_scan<int>(mine, slots, lds32);
     if (s >= at && s < at + mine) {
         for (int b = b0; b < b0 + per && b < a.B; ++b) {
-            const Span sp = seq_span(cached_len(a.seq_lens, b, a.map), a.n, a.window);
+            const int len = cached_len(a.seq_lens, b, a.map);
+            const Span sp = seq_span(len, a.n, a.window);
             int ns = (sp.hi - sp.lo + chunk - 1) / chunk;
             ns = ns > 1 ? ns : 1;
             if (s < at + ns) {
-                found[0] = b; found[1] = at; found[2] = ns;
+                found[0] = b; found[1] = at; found[2] = ns; found[4] = len;
                 // the sequence's slots alike, in multiples of 128 tokens
                 found[3] = ((sp.hi - sp.lo + ns - 1) / ns + 127) & ~127;
                 break;
@@ -167,7 +183,8 @@ __device__ inline Slot find_slot(const KArgs &k, int s) {
         }
     }
     __syncthreads();
-    return Slot{found[0], found[1], found[2], found[3]};
+    return Slot{uniform(found[0]), uniform(found[4]), uniform(found[1]), uniform(found[2]),
+                uniform(found[3])};
 }
 
 __device__ inline float swap_max16(float x) {
@@ -492,7 +509,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const Slot sl_ = find_slot(k, slot);
     const int b = sl_.b;
     if (b < 0) return;
-    const int len = cached_len(a.seq_lens, b, a.map);
+    const int len = sl_.len;
     const Span seq = seq_span(len, a.n, a.window);
     if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
 
