@@ -24,6 +24,7 @@ __all__ = ["prefill", "prefill_varlen", "prefill_varlen_pool", "decode_step",
            "prefill_fused", "prefill_varlen_fused", "decode_tokens_fused",
            "fused_workspace_bytes", "backward", "backward_varlen",
            "cache_append", "attention_decode", "attention_workspace_bytes", "cache_evict",
+           "evict_workspace_bytes",
            "version", "GdrError", "lib_path",
            "FA", "SWA", "GDN", "KDA"]
 
@@ -109,8 +110,10 @@ def _load():
     lib.gdr_attention_decode.argtypes = [I, I, I, I, I, I, F, I, P, P, P, P, P, I, I, I, P, P, P,
                                          P, Z, P]
     lib.gdr_cache_evict.restype = I
+    lib.gdr_cache_evict_workspace_bytes.restype = Z
+    lib.gdr_cache_evict_workspace_bytes.argtypes = [I, I, I, I]
     lib.gdr_cache_evict.argtypes = [I, I, I, I, I, I, I, P, P, P, P, P, I, P, P, I, I, I, P, P,
-                                    P, P]
+                                    P, P, Z, P]
     _lib = lib
     return lib
 
@@ -650,4 +653,4 @@ def backward_varlen(q, k, v, g, beta, do, cu_seqlens, h0=None, dht=None, scale: 
 
 # the paged key-value cache of the attention layers (include/gdr_cache.h)
 from .cache import (attention_decode, attention_workspace_bytes, cache_append,  # noqa: E402
-                    cache_evict)
+                    cache_evict, evict_workspace_bytes)

@@ -26,7 +26,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 # A decode step is microseconds of GPU work, so the checks cost as little as
 # they can: one test per tensor, and a message only for one that fails.
 def _gpu(name, t, dtype, dev):
-    if not (isinstance(t, _Tensor) and t.is_cuda and t.dtype == dtype and t.device == dev
+    if not (isinstance(t, _Tensor) and t.dtype == dtype and t.device == dev
             and t.is_contiguous()):
         _dense(name, t, dtype, dev)
 
@@ -77,6 +77,14 @@ def _host_table(name, x, shape):
     a = np.ascontiguousarray(np.asarray(x, dtype=np.int32))
     _need(a.shape == shape, "%s must be %s" % (name, list(shape)))
     return a
+
+
+def _scratch(workspace, nbytes, dev):
+    """The caller's workspace if it will do, a new one if there is none."""
+    if not (isinstance(workspace, _Tensor) and workspace.device == dev
+            and workspace.is_contiguous() and workspace.nbytes >= nbytes):
+        workspace = _workspace(workspace, nbytes, dev)
+    return workspace
 
 
 def _p(t):
@@ -178,9 +186,7 @@ def attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, wind
     _int("window", window, 0)
     lib = _load()
     nbytes = lib.gdr_attention_workspace_bytes(B, n, Hq, Hkv, D, M, page, scores is not None)
-    workspace = _workspace(workspace, nbytes, dev) if workspace is None or not (
-        isinstance(workspace, _Tensor) and workspace.device == dev and workspace.is_contiguous()
-        and workspace.nbytes >= nbytes) else workspace
+    workspace = _scratch(workspace, nbytes, dev)
     _call(dev, lib.gdr_attention_decode, dt, B, n, Hq, Hkv, D,
           D ** -0.5 if scale is None else scale, window, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), page_table.data_ptr(), _hp(host), M, page, P, seq_lens.data_ptr(),
@@ -188,9 +194,16 @@ def attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, wind
     return o
 
 
+def evict_workspace_bytes(batch: int, kv_heads: int, max_pages: int, page_size: int) -> int:
+    """Bytes of device workspace cache_evict needs for these sizes: 0 for
+    most (include/gdr_cache.h, gdr_cache_evict_workspace_bytes)."""
+    return int(_load().gdr_cache_evict_workspace_bytes(int(batch), int(kv_heads), int(max_pages),
+                                                       int(page_size)))
+
+
 def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, recent: int = 0,
                 sink: int = 0, new_page_table=None, new_lens=None, kept=None,
-                page_table_host=None, new_page_table_host=None):
+                page_table_host=None, new_page_table_host=None, workspace=None):
     """Trim every sequence to at most `budget` tokens by accumulated weight.
 
     Each key-value head of a longer sequence keeps the first `sink` tokens,
@@ -200,7 +213,8 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     sequence uses yet).  Returns (new_lens int32 [B], kept int32
     [B,Hkv,budget]: the old index of each kept token, -1 past the new
     length).  new_lens may be seq_lens itself.  The host copies of the tables
-    make the library validate them.
+    make the library validate them.  workspace (a device buffer of
+    evict_workspace_bytes(...) bytes) is allocated when needed and not given.
     """
     _need(scores is not None, "scores are required")
     dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
@@ -228,8 +242,12 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     else:
         _gpu("kept", kept, _INT32, dev)
         _shape("kept", kept, (B, Hkv, budget))
-    _call(dev, _load().gdr_cache_evict, dt, B, Hkv, D, budget, recent, sink, k_cache.data_ptr(),
+    lib = _load()
+    nbytes = lib.gdr_cache_evict_workspace_bytes(B, Hkv, M, page)
+    if nbytes:
+        workspace = _scratch(workspace, nbytes, dev)
+    _call(dev, lib.gdr_cache_evict, dt, B, Hkv, D, budget, recent, sink, k_cache.data_ptr(),
           v_cache.data_ptr(), scores.data_ptr(), page_table.data_ptr(), _hp(host), M,
           _p(new_page_table), _hp(host2), M2, page, P, seq_lens.data_ptr(), new_lens.data_ptr(),
-          kept.data_ptr())
+          kept.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes)
     return new_lens, kept

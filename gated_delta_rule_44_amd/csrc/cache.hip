@@ -95,6 +95,45 @@ constexpr int kCopies = 16, kCopyStride = 257;
 
 typedef unsigned keys4 __attribute__((ext_vector_type(4)));
 
+// The digit of the `want`-th largest key: thread t < 256 brings how many keys
+// have digit 255 - t.
+struct Digit {
+    int digit, want, count;                        // wanted of its `count` keys
+};
+__device__ inline Digit find_digit(int count, int want) {
+    __shared__ int waves[4], found[3];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    int incl = count;                              // keys with this digit or a larger one
+    if (tid < 256) {
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int y = __shfl_up(incl, m);
+            if (lane >= m) incl += y;
+        }
+        if (lane == 63) waves[w] = incl;
+    }
+    __syncthreads();
+    if (tid < 256) {
+        for (int i = 0; i < w; ++i) incl += waves[i];
+        if (incl >= want && incl - count < want) { // one thread
+            found[0] = 255 - tid;
+            found[1] = want - (incl - count);
+            found[2] = count;
+        }
+    }
+    __syncthreads();
+    return Digit{found[0], found[1], found[2]};
+}
+// Keys that share the digits of `prefix` above `shift` + 8 lie in prefix ..
+// prefix + this.
+__device__ inline unsigned digit_span(int shift) {
+    return shift == 24 ? 0xFFFFFFFFu : (1u << (shift + 8)) - 1;
+}
+__device__ inline int lanes_below(unsigned long long x) {
+    return (int)__builtin_amdgcn_mbcnt_hi((unsigned)(x >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((unsigned)x, 0));
+}
+
 __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
     const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -105,7 +144,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         return;
     }
     const int lo = a.sink, hi = len - a.recent;
-    __shared__ int hist[kCopies * kCopyStride], waves[4], found[3];
+    __shared__ int hist[kCopies * kCopyStride];
     __shared__ int2 counts[kRounds][kSelWaves], wave_counts[4];
 
     __shared__ keys4 lds_keys[(kRounds - kRegRounds) * kSelThreads];
@@ -163,8 +202,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
         __syncthreads();
         int *mine = hist + (lane & (kCopies - 1)) * kCopyStride;
-        // keys prefix .. prefix + span share the digits found
-        const unsigned span = shift == 24 ? 0xFFFFFFFFu : (1u << (shift + 8)) - 1;
+        const unsigned span = digit_span(shift);
         for (int base = 0; base < len; base += kHeld) {
             if (!once) load_held(base);
 #pragma unroll
@@ -177,42 +215,19 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             }
         }
         __syncthreads();
-        // thread t < 256 has digit 255 - t: how many keys have it, and how
-        // many have it or a larger one
-        int count = 0, incl = 0;
-        if (tid < 256) {
+        int count = 0;
+        if (tid < 256)
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) count += hist[c * kCopyStride + 255 - tid];
-            incl = count;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const int y = __shfl_up(incl, m);
-                if (lane >= m) incl += y;
-            }
-            if (lane == 63) waves[w] = incl;
-        }
-        __syncthreads();
-        if (tid < 256) {
-            for (int i = 0; i < w; ++i) incl += waves[i];
-            if (incl >= want && incl - count < want) {      // one thread: the threshold's digit
-                found[0] = 255 - tid;
-                found[1] = want - (incl - count);
-                found[2] = count;
-            }
-        }
-        __syncthreads();
-        prefix |= (unsigned)found[0] << shift;
-        want = found[1];                           // wanted among the keys with this prefix
-        ties = want != found[2];
+        const Digit f = find_digit(count, want);
+        prefix |= (unsigned)f.digit << shift;
+        want = f.want;                             // wanted among the keys with this prefix
+        ties = want != f.count;
         if (!ties) break;                          // all of them: prefix 00.. is a threshold
     }
     // Kept are sink and recent, every key above the threshold, and of the
     // keys equal to it the first `want` (without ties: all).
     int above = 0, equal = 0;                      // kept, and equal keys, before base
-    auto count_below = [&](unsigned long long x) {
-        return (int)__builtin_amdgcn_mbcnt_hi((unsigned)(x >> 32),
-                                              __builtin_amdgcn_mbcnt_lo((unsigned)x, 0));
-    };
     for (int base = 0; base < len; base += kHeld) {
         if (!once) load_held(base);
         auto flags = [&](int r, keys4 k, bool (&keep)[4], bool (&eq)[4]) {
@@ -276,8 +291,8 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
             flags(r, keys(r), keep, eq);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                nk += count_below(__ballot(keep[e]));
-                if (ties) ne += count_below(__ballot(eq[e]));
+                nk += lanes_below(__ballot(keep[e]));
+                if (ties) ne += lanes_below(__ballot(eq[e]));
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -286,6 +301,181 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 nk += keep[e];
                 ne += eq[e];
             }
+        }
+    }
+}
+
+// The same for few (sequence, head) pairs with long sequences: one workgroup
+// reads a pair's scores at some 20 GB/s, so each pair is given `chunks`
+// workgroups of `chunk` tokens.  A launch per digit: every workgroup finds the
+// last digit from all chunks' histograms (each writes its own), adds up which of
+// its keys that puts above the threshold, and makes its histogram of the next
+// digit; the last launch places the chunk's kept tokens behind those of the
+// chunks before it.  (65,001 tokens, 8 heads: 53 us by one workgroup, XX us so.)
+constexpr int kSpreadPairs = 64;       // at most so many pairs ...
+constexpr int kSpreadTokens = 8192;    // ... and tables longer than this
+constexpr int kSpreadChunks = 64;
+struct Spread {
+    int chunks, chunk;         // chunk: a multiple of kPerRound
+    int *hist;                 // [4 digits][pairs][chunks][256]
+    int *above;                // [pairs][chunks]: keys above the threshold's digits so far
+    int4 *state;               // [5][pairs]: prefix, want, done, ties before each launch
+};
+struct SpreadLayout {
+    int chunks, chunk;
+    size_t above, state, total;
+};
+SpreadLayout spread_layout(int pairs, long long capacity) {
+    SpreadLayout l{};
+    if (pairs > kSpreadPairs || capacity <= kSpreadTokens) return l;
+    const long long c = (capacity + kSpreadChunks - 1) / kSpreadChunks;
+    l.chunk = (int)((c + kPerRound - 1) / kPerRound * kPerRound);
+    l.chunks = (int)((capacity + l.chunk - 1) / l.chunk);
+    const size_t cells = (size_t)pairs * l.chunks;
+    l.above = cells * 4 * 256 * sizeof(int);
+    l.state = l.above + (cells * sizeof(int) + 255) / 256 * 256;
+    l.total = l.state + (size_t)pairs * 5 * sizeof(int4);
+    return l;
+}
+
+__global__ __launch_bounds__(kSelThreads) void spread_kernel(EvictArgs a, Spread s, int level) {
+    const int pairs = a.B * a.Hkv, pair = blockIdx.x / s.chunks, me = blockIdx.x % s.chunks;
+    const int b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int len = cached_len(a.seq_lens, b, a.map);
+    int32_t *kept = a.kept + (size_t)pair * a.budget;
+    if (len <= a.budget) {
+        if (level == 4)
+            for (int i = me * kSelThreads + tid; i < a.budget; i += s.chunks * kSelThreads)
+                kept[i] = i < len ? i : -1;
+        return;
+    }
+    const int lo = a.sink, hi = len - a.recent, t0 = me * s.chunk;
+    if (t0 >= len) return;
+    const int t1 = t0 + s.chunk < len ? t0 + s.chunk : len;
+    const int used = (len + s.chunk - 1) / s.chunk;      // chunks with tokens
+    auto cell = [&](int digit, int c) {
+        return s.hist + (((size_t)digit * pairs + pair) * s.chunks + c) * 256;
+    };
+    __shared__ int hist[kCopies * kCopyStride], sums[3];
+    __shared__ int2 counts[kSelWaves];
+    // the threshold so far: its digits, the keys wanted among those that share
+    // them, whether it is found, and whether more keys equal it than wanted
+    unsigned prefix = 0;
+    int want = a.budget - a.sink - a.recent;
+    bool done = want == 0, ties = false;
+    if (done) prefix = 0xFFFFFFFFu;                      // above every key
+    // keys above it, and equal to it, in the chunks before this one (level 4)
+    int above = 0, equal = 0;
+    if (level > 0) {
+        const int4 st = s.state[(size_t)(level - 1) * pairs + pair];
+        prefix = (unsigned)st.x; want = st.y; done = st.z != 0; ties = st.w != 0;
+        if (tid < 3) sums[tid] = 0;
+        __syncthreads();
+        if (level == 4 && tid < me) atomicAdd(&sums[0], s.above[(size_t)pair * s.chunks + tid]);
+        if (!done) {
+            int count = 0;
+            if (tid < 256)
+                for (int c = 0; c < used; ++c) count += cell(level - 1, c)[255 - tid];
+            const Digit f = find_digit(count, want);
+            prefix |= (unsigned)f.digit << (32 - 8 * level);
+            want = f.want;
+            ties = want != f.count;
+            done = !ties || level == 4;
+            // own keys (level 4: those of the chunks before) above the digit, and with it
+            if (tid < 256 && 255 - tid >= f.digit) {
+                int n = 0;
+                if (level < 4) n = cell(level - 1, me)[255 - tid];
+                else for (int c = 0; c < me; ++c) n += cell(3, c)[255 - tid];
+                if (n) atomicAdd(&sums[255 - tid == f.digit ? 2 : 1], n);
+            }
+        }
+        __syncthreads();
+        if (level == 4) {
+            above = sums[0] + sums[1] + (ties ? 0 : sums[2]);
+            equal = ties ? sums[2] : 0;
+        } else if (tid == 0) {
+            int *x = s.above + (size_t)pair * s.chunks + me;
+            const int old = level == 1 ? 0 : *x;
+            *x = old + sums[1] + (done ? sums[2] : 0);   // without ties the equal ones are kept
+        }
+    }
+    if (me == 0 && tid == 0 && level < 4)
+        s.state[(size_t)level * pairs + pair] = int4{(int)prefix, want, done, ties};
+    if (level < 4 && done) return;
+
+    auto load4 = [&](int j) {
+        keys4 k{0, 0, 0, 0};
+        const int page = j < len ? page_of(a.map, b, j) : -1;
+        if (page >= 0) {
+            const float4 x = *reinterpret_cast<const float4 *>(
+                a.scores + cache_row(a.map, a.Hkv, page, h, slot_of(a.map, j)));
+            k = keys4{key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w)};
+            if (j < lo || j + 4 > hi)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) k[e] = j + e >= lo && j + e < hi ? k[e] : 0u;
+        }
+        return k;
+    };
+    if (level < 4) {
+        const int shift = 24 - 8 * level;
+        const unsigned span = digit_span(shift);
+        for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
+        __syncthreads();
+        int *mine = hist + (lane & (kCopies - 1)) * kCopyStride;
+        for (int base = t0; base < t1; base += kPerRound) {
+            const int j = base + 4 * tid;
+            const bool inside = j >= lo && j + 4 <= hi;
+            const keys4 k = load4(j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k[e] - prefix <= span && (inside || (j + e >= lo && j + e < hi)))
+                    atomicAdd(&mine[(k[e] >> shift) & 255], 1);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            int count = 0;
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) count += hist[c * kCopyStride + 255 - tid];
+            cell(level, me)[255 - tid] = count;
+        }
+        return;
+    }
+    // sink and recent tokens before this chunk
+    above += (t0 < lo ? t0 : lo) + (t0 > hi ? t0 - hi : 0);
+    for (int base = t0; base < t1; base += kPerRound) {
+        const keys4 k = load4(base + 4 * tid);
+        bool keep[4], eq[4];
+        int2 c{0, 0}, before{0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = base + 4 * tid + e;
+            const bool mid = j >= lo && j < hi;
+            keep[e] = j < len && (!mid || (ties ? k[e] > prefix : k[e] >= prefix));
+            eq[e] = ties && mid && k[e] == prefix;
+            const unsigned long long bk = __ballot(keep[e]), be = __ballot(eq[e]);
+            before.x += lanes_below(bk);
+            before.y += lanes_below(be);
+            c.x += __popcll(bk);
+            c.y += __popcll(be);
+        }
+        __syncthreads();
+        if (lane == 0) counts[w] = c;
+        __syncthreads();
+        int nk = above + before.x, ne = equal + before.y;
+#pragma unroll
+        for (int i = 0; i < kSelWaves; ++i) {
+            const int2 x = counts[i];
+            nk += i < w ? x.x : 0;
+            ne += i < w ? x.y : 0;
+            above += x.x;
+            equal += x.y;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (keep[e] || (eq[e] && ne < want)) kept[nk + (ne < want ? ne : want)] = base + 4 * tid + e;
+            nk += keep[e];
+            ne += eq[e];
         }
     }
 }
@@ -404,17 +594,34 @@ hipError_t launch_cache_append(int row_bytes, const AppendArgs &a, hipStream_t s
     return hipGetLastError();
 }
 
+size_t evict_workspace(int pairs, long long capacity) {
+    return spread_layout(pairs, capacity).total;
+}
+
 hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s) {
     const int sh = lpr_shift_of(row_bytes);
     const int pairs = a.B * a.Hkv;
-    select_kernel<<<pairs, kSelThreads, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    const long long capacity = (long long)a.map.max_pages << a.map.page_shift;
+    const SpreadLayout l = spread_layout(pairs, capacity);
+    if (l.chunks) {
+        char *ws = static_cast<char *>(a.ws);
+        const Spread sp{l.chunks, l.chunk, reinterpret_cast<int *>(ws),
+                        reinterpret_cast<int *>(ws + l.above), reinterpret_cast<int4 *>(ws + l.state)};
+        for (int level = 0; level <= 4; ++level) {
+            spread_kernel<<<pairs * l.chunks, kSelThreads, 0, s>>>(a, sp, level);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    } else {
+        select_kernel<<<pairs, kSelThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (a.in_place) {
         close_up_kernel<<<dim3(pairs, 2 << (sh - 2)), 256, 0, s>>>(a, sh);
     } else {
-        const int cap = a.map.max_pages << a.map.page_shift;
-        const int most = a.budget < cap ? a.budget : cap, tile = (256 >> sh) * kMoveRows;
+        const int most = a.budget < capacity ? a.budget : (int)capacity;
+        const int tile = (256 >> sh) * kMoveRows;
         int tiles = (most + tile - 1) / tile;
         tiles = tiles < 1 ? 1 : (tiles > 16384 ? 16384 : tiles);
         copy_rows_kernel<<<dim3(pairs, tiles), 256, 0, s>>>(a, sh);

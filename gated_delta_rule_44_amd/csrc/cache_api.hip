@@ -193,13 +193,21 @@ gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int
     return finish(gdr::launch_attention_decode(dt == GDR_BF16, D, a, s), s, what);
 }
 
+size_t gdr_cache_evict_workspace_bytes(int B, int Hkv, int max_pages, int page_size) {
+    if (B <= 0 || Hkv <= 0 || max_pages <= 0 || page_shift_of(page_size) < 0 ||
+        (long long)B * Hkv >= kMaxPairs)
+        return 0;
+    return gdr::evict_workspace(B * Hkv, (long long)max_pages * page_size);
+}
+
 gdr_status gdr_cache_evict(enum gdr_dtype dt, int B, int Hkv, int D, int budget, int recent,
                            int sink, void *k_cache, void *v_cache, float *scores,
                            const int32_t *page_table, const int32_t *page_table_host,
                            int max_pages, const int32_t *new_page_table,
                            const int32_t *new_page_table_host, int new_max_pages,
                            int page_size, int num_pages, const int32_t *seq_lens,
-                           int32_t *new_lens, int32_t *kept, void *stream) {
+                           int32_t *new_lens, int32_t *kept, void *workspace, size_t ws_bytes,
+                           void *stream) {
     const char *what = "gdr_cache_evict";
     gdr_status st = check_cache(what, dt, B, Hkv, D, max_pages, page_size, num_pages);
     if (st != GDR_OK) return st;
@@ -257,7 +265,11 @@ gdr_status gdr_cache_evict(enum gdr_dtype dt, int B, int Hkv, int D, int budget,
         REQUIRE_PTR(v_cache, "v_cache");
         REQUIRE_PTR(scores, "scores");
     }
+    st = check_workspace(what, workspace, ws_bytes,
+                         gdr_cache_evict_workspace_bytes(B, Hkv, max_pages, page_size));
+    if (st != GDR_OK) return st;
     gdr::EvictArgs a{};
+    a.ws = workspace;
     a.k_cache = k_cache; a.v_cache = v_cache; a.scores = scores;
     const int shift = page_shift_of(page_size);
     a.map = gdr::PageMap{page_table, max_pages, shift, num_pages};

@@ -73,8 +73,10 @@ struct EvictArgs {
     const int32_t *seq_lens;     // [B]
     int32_t *new_lens;           // [B]
     int32_t *kept;               // [B, Hkv, budget]
+    void *ws;
     int B, Hkv, budget, recent, sink;
 };
+size_t evict_workspace(int pairs, long long capacity);
 hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s);
 
 }  // namespace gdr

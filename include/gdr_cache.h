@@ -149,16 +149,22 @@ gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int
  *                seq_lens itself
  *   kept         device int32 [B, Hkv, budget] (written), -1 past the new
  *                length
+ *   workspace    device buffer of gdr_cache_evict_workspace_bytes bytes (0 for
+ *                most sizes: NULL is accepted then), 16-byte aligned; needs no
+ *                clearing; not to be shared with a concurrent call
  *
  * A kept token whose old or new page is absent is not moved.
  */
+size_t gdr_cache_evict_workspace_bytes(int B, int Hkv, int max_pages, int page_size);
+
 gdr_status gdr_cache_evict(enum gdr_dtype dt, int B, int Hkv, int D, int budget, int recent,
                            int sink, void *k_cache, void *v_cache, float *scores,
                            const int32_t *page_table, const int32_t *page_table_host,
                            int max_pages, const int32_t *new_page_table,
                            const int32_t *new_page_table_host, int new_max_pages,
                            int page_size, int num_pages, const int32_t *seq_lens,
-                           int32_t *new_lens, int32_t *kept, void *stream);
+                           int32_t *new_lens, int32_t *kept, void *workspace, size_t ws_bytes,
+                           void *stream);
 
 #ifdef __cplusplus
 }

@@ -37,7 +37,7 @@ def test_library_exports_every_declared_symbol(lib):
     src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(gdr_[a-z_]+)\s*\(", src)))
     assert names == ["gdr_attention_decode", "gdr_attention_workspace_bytes", "gdr_cache_append",
-                     "gdr_cache_evict"]
+                     "gdr_cache_evict", "gdr_cache_evict_workspace_bytes"]
     for name in names:
         assert hasattr(ctypes.CDLL(gdr.lib_path()), name), name
 
@@ -128,9 +128,10 @@ def test_attend_rejects(lib, kw, code, msg):
 
 def evict(lib, dt=1, B=2, Hkv=2, D=128, budget=40, recent=8, sink=4, kc=FAKE, vc=FAKE, sc=FAKE,
           table=FAKE, host=None, M=4, new=None, new_host=None, M2=0, page=16, P=9, lens=FAKE,
-          new_lens=FAKE, kept=FAKE):
+          new_lens=FAKE, kept=FAKE, ws=None, ws_bytes=0):
     return lib.gdr_cache_evict(dt, B, Hkv, D, budget, recent, sink, kc, vc, sc, table, hp(host), M,
-                               new, hp(new_host), M2, page, P, lens, new_lens, kept, None)
+                               new, hp(new_host), M2, page, P, lens, new_lens, kept, ws, ws_bytes,
+                               None)
 
 
 @pytest.mark.parametrize("kw,code,msg", CACHE + [
@@ -156,6 +157,8 @@ def evict(lib, dt=1, B=2, Hkv=2, D=128, budget=40, recent=8, sink=4, kc=FAKE, vc
     (dict(new=FAKE, M2=3, new_host=[[0, 1, 2], [3, 10, 4]]), EINVAL, "outside"),
     (dict(new=FAKE, M2=3, host=[[5, 6, 7, 8], [5, 6, 7, 4]], new_host=[[0, 1, 2], [3, -1, 4]]),
      EINVAL, "page 4 is in both tables"),
+    (dict(M=1000), EINVAL, "workspace of"),
+    (dict(M=1000, ws=MIS, ws_bytes=1 << 30), EINVAL, "workspace is not 16-byte aligned"),
 ])
 def test_evict_rejects(lib, kw, code, msg):
     assert evict(lib, **kw) == code
@@ -171,6 +174,12 @@ def test_workspace_sizes(lib):
     assert ws(2, 1, 4, 2, 128, 0, 16) == 0
     # grows with the table where logits are kept for the scores
     assert ws(2, 1, 4, 2, 128, 64, 16, True) >= ws(2, 1, 4, 2, 128, 64, 16)
+
+
+    # the selection by many workgroups: few pairs, long tables
+    assert gdr.evict_workspace_bytes(2, 2, 4, 16) == 0
+    assert gdr.evict_workspace_bytes(200, 2, 4000, 16) == 0
+    assert gdr.evict_workspace_bytes(2, 2, 4000, 16) > 0
 
 
 def test_binding_rejects_host_tensors():

@@ -465,15 +465,31 @@ def test_evict_long_and_large_budget(pages):
             run_evict(kc, vc, s, table, lens, budget, 100, 10, new_table, kind)
 
 
-@pytest.mark.parametrize("kind", ["weights", "ties"])
-def test_evict_longer_than_a_workgroup_holds(kind):
-    """Past 65,536 tokens, and just at that length."""
-    announce("evict very long %s" % kind)
-    lens = [70001, 65536, 131]
+@pytest.mark.parametrize("kind", ["weights", "ties", "special", "close"])
+@pytest.mark.parametrize("others", [0, 70])
+def test_evict_very_long(kind, others):
+    """Past 65,536 tokens, and just at that length: with few sequences a pair's
+    selection is spread over workgroups, among many it is one workgroup's."""
+    announce("evict very long %s others=%d" % (kind, others))
+    lens = [70001, 65536, 131] + [9] * others
     kc, vc, sc, table = make_cache(lens, 1, 64, 256, torch.bfloat16, seed=90)
     s = odd_scores(sc, kind, 91)
-    run_evict(kc, vc, s, table, lens, 30000, 1000, 10, None, kind)
-    run_evict(kc, vc, s, table, lens, 100, 0, 0, None, kind)
+    for budget, recent, sink in ((30000, 1000, 10), (100, 0, 0), (5000, 4000, 1000), (66000, 1, 1)):
+        run_evict(kc, vc, s, table, lens, budget, recent, sink, None, kind)
+
+
+@pytest.mark.parametrize("others", [0, 70])
+def test_evict_long_with_absent_pages(others):
+    """More tokens wanted than are present: of those on absent pages the lowest
+    are kept, across the borders of the workgroups' shares too."""
+    announce("evict long absent others=%d" % others)
+    lens = [13000, 9000, 8500] + [5] * others
+    kc, vc, sc, table = make_cache(lens, 1, 64, 16, torch.float32, seed=92)
+    rng = np.random.default_rng(93)
+    table[0, rng.random(table.shape[1]) < 0.7] = -1
+    table[1, :] = -1
+    for budget, recent, sink in ((6000, 0, 0), (8000, 500, 70), (8990, 3, 4200)):
+        run_evict(kc, vc, sc, table, lens, budget, recent, sink, None, "absent")
 
 
 def test_evict_absent_pages():
