@@ -48,9 +48,9 @@ __device__ inline Span seq_span(int len, int n, int window) {
 //   The card holds kResident workgroups at once, and workgroups of a like
 // size end together: with sum ceil(len / C) <= total / C + B slots, C is taken
 // such that they fill the card once, or twice or four times where B
-// sequences' last chunks would leave over a quarter of it idle (64 rows a
-// head, 16 contexts: 77 us with C for 1,024 workgroups, XX us so; 130,001
-// tokens: 57 and XX us).  With more sequences than that, C is for 1,024.
+// sequences' last chunks would leave over a quarter of it idle (130,001
+// tokens: 57 us with C for 1,024 workgroups, 52 us so).  With more sequences
+// than that, C is for 1,024.
 constexpr int kResident = 512;
 constexpr int kMinChunk = 512;
 struct Plan {
