@@ -21,6 +21,7 @@ _Tensor, _INT32, _FLOAT32 = torch.Tensor, torch.int32, torch.float32
 _DTYPES = {torch.bfloat16: _BF16, torch.float32: _F32}
 # the current stream's handle, without a torch.cuda.Stream object around it
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 # A decode step is microseconds of GPU work, so the checks cost as little as
@@ -79,12 +80,12 @@ def _host_table(name, x, shape):
     return a
 
 
-def _scratch(workspace, nbytes, dev):
-    """The caller's workspace if it will do, a new one if there is none."""
+def _scratch(workspace, dev):
+    """The bytes of a workspace; the library says if they are too few."""
     if not (isinstance(workspace, _Tensor) and workspace.device == dev
-            and workspace.is_contiguous() and workspace.nbytes >= nbytes):
-        workspace = _workspace(workspace, nbytes, dev)
-    return workspace
+            and workspace.is_contiguous()):
+        _dense("workspace", workspace, None, dev)
+    return workspace.nbytes
 
 
 def _p(t):
@@ -98,7 +99,7 @@ def _hp(a):
 def _call(dev, fn, *args):
     """fn(*args, stream): the current stream of dev, with dev current."""
     i = dev.index
-    if i == torch.cuda.current_device():
+    if i == _current_device():
         rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
@@ -185,8 +186,10 @@ def attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, wind
         _shape("o", o, shape)
     _int("window", window, 0)
     lib = _load()
-    nbytes = lib.gdr_attention_workspace_bytes(B, n, Hq, Hkv, D, M, page, scores is not None)
-    workspace = _scratch(workspace, nbytes, dev)
+    if workspace is None:
+        workspace = _workspace(None, lib.gdr_attention_workspace_bytes(
+            B, n, Hq, Hkv, D, M, page, scores is not None), dev)
+    nbytes = _scratch(workspace, dev)
     _call(dev, lib.gdr_attention_decode, dt, B, n, Hq, Hkv, D,
           D ** -0.5 if scale is None else scale, window, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), page_table.data_ptr(), _hp(host), M, page, P, seq_lens.data_ptr(),
@@ -243,11 +246,14 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
         _gpu("kept", kept, _INT32, dev)
         _shape("kept", kept, (B, Hkv, budget))
     lib = _load()
-    nbytes = lib.gdr_cache_evict_workspace_bytes(B, Hkv, M, page)
-    if nbytes:
-        workspace = _scratch(workspace, nbytes, dev)
+    if workspace is None:
+        nbytes = lib.gdr_cache_evict_workspace_bytes(B, Hkv, M, page)
+        if nbytes:
+            workspace = _workspace(None, nbytes, dev)
+    else:
+        nbytes = _scratch(workspace, dev)
     _call(dev, lib.gdr_cache_evict, dt, B, Hkv, D, budget, recent, sink, k_cache.data_ptr(),
           v_cache.data_ptr(), scores.data_ptr(), page_table.data_ptr(), _hp(host), M,
           _p(new_page_table), _hp(host2), M2, page, P, seq_lens.data_ptr(), new_lens.data_ptr(),
-          kept.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes)
+          kept.data_ptr(), _p(workspace), nbytes)
     return new_lens, kept

@@ -5,10 +5,12 @@
 // attends to the cached tokens j <= p (and j > p - window):
 //     s_j = scale q.k_j,   w_j = e^{s_j} / sum e^{s_i},   o = sum w_j v_j.
 //
-// One pass over K and V with a running maximum m and sum l (in units of
-// log2: x = s log2 e): for a tile of tokens, m' = max(m, max x),
-// l = l 2^{m - m'} + sum 2^{x - m'}, o likewise.  Parts of a sequence join by
-// the same rule.
+// One pass over K and V with a running maximum m and sum l: with c = |scale|
+// log2 e (a negative scale's sign goes into q) and y = q.k, for a tile of
+// tokens m' = max(m, max y), l = l 2^{c (m - m')} + sum 2^{c (y - m')}, o
+// likewise.  Parts of a sequence join by the same rule.  (The difference is
+// taken before the product: near the maximum, where the weights are, it is
+// exact.)
 //
 // The G = Hq / Hkv query heads of a key-value head and the n new tokens make
 // n G rows that read the same K and V: a workgroup has up to 32 of them (16 in
@@ -78,8 +80,8 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 int block_rows(bool bf16_io, long long rows) { return bf16_io && rows > 16 ? 32 : 16; }
 
 // Workspace: {first slot, slots} of every sequence; (m, l) of every slot, unit
-// and row; o of the same, unnormalised; with scores, the logits x of every row and
-// token [B, Hkv, nG, cap].
+// and row; o of the same, unnormalised; with scores, the products q.k of every row
+// and token [B, Hkv, nG, cap].
 struct WsMap {
     size_t sched, ml, o, logits, total;
 };
@@ -106,6 +108,8 @@ struct KArgs {
     float *po;
     float *logits;        // nullptr: no scores
     long long cap32;      // tokens of a logits row
+    float c;              // |scale| log2 e, above 0
+    bool negative;        // scale < 0
     bool parts;           // a sequence may have several slots
 };
 
@@ -275,6 +279,11 @@ template <int D, int RW> struct Tile<bf16, D, RW> {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) q.f[i] = bload16(r, off + 16 * kGroups * i + 16 * (lane / RW));
     }
+    __device__ static inline void negate(Q &q) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            q.f[i] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q.f[i]) ^ 0x80008000u);
+    }
     // kc + src[b].at: the rows of block b of 16 tokens
     template <bool STREAM>
     __device__ static inline void load_k(K &k, const char *kc, const Src (&src)[2], bool one_page,
@@ -420,6 +429,10 @@ template <int D> struct Tile<float, D, 16> {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) q.f[i] = bload16f(r, off + 64 * i + 16 * (lane >> 4));
     }
+    __device__ static inline void negate(Q &q) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) q.f[i] = -q.f[i];
+    }
     template <bool STREAM>
     __device__ static inline void load_k(K &k, const char *kc, const Src (&src)[1], bool, int lane) {
         const rsrc_t rs = make_rsrc(kc + src[0].at, src[0].bytes);
@@ -523,6 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0;
         if (row < rows) sp = token_span(len, a.n, a.window, t);
         TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + hg) * (D * (unsigned)sizeof(T)), lane);
+        if (k.negative) TL::negate(q);
     }
     // the block's tokens: what its rows attend to, within the slot
     const Span first = token_span(len, a.n, a.window, row0 / a.G);
@@ -537,7 +551,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const int tiles = k_hi > k_lo ? (k_hi + kTile - 1) / kTile - tile0 : 0;
 
     const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
-    const float c1 = a.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     typename TL::Acc acc[PER];
 #pragma unroll
@@ -549,14 +562,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     auto row_max = [](float x) { return swap_max32(RW == 16 ? swap_max16(x) : x); };
     auto row_sum = [](float x) { return swap_sum32(RW == 16 ? swap_sum16(x) : x); };
 
-    // One tile's logits (before scaling) and values into m, l and o.  full:
+    // One tile's products q.k and values into m, l and o.  full:
     // every row attends to all of it; here: which of its blocks are there.
     // (Past the length and on absent pages V is zeros.)
     auto absorb = [&](int j0, float (&x)[kVals], typename TL::V &vf, bool full,
                       const bool (&here)[kBlocks]) {
         float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) x[i] *= c1;
         if (k.logits && row < rows) {
 #pragma unroll
             for (int i = 0; i < kVals; i += 4)
@@ -576,7 +587,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         for (int i = 0; i < kVals; ++i) top = fmaxf(top, x[i]);
         const float mn = fmaxf(m, row_max(top)), ms = finite_top(mn);
         if (__builtin_amdgcn_ballot_w64(mn != m)) {
-            const float al = exp2_(m - ms);
+            const float al = exp2_((m - ms) * k.c);
             l *= al;
 #pragma unroll
             for (int c = 0; c < PER; ++c) acc[c] *= al;
@@ -584,7 +595,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         }
 #pragma unroll
         for (int i = 0; i < kVals; ++i) {
-            x[i] = exp2_(x[i] - ms);
+            x[i] = exp2_((x[i] - ms) * k.c);
             l += x[i];
         }
         const typename TL::P p = TL::weights(x);
@@ -707,7 +718,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sm[i][r]);
-    const float f = exp2_(m - finite_top(top));
+    const float f = exp2_((m - finite_top(top)) * k.c);
     // acc[c][e] is channel dim(c, e, g); those of adjacent c lie together
     constexpr int kRun = PER < 4 ? PER : 4;
     typedef float run_t __attribute__((ext_vector_type(kRun)));
@@ -730,7 +741,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
         for (int x = 0; x < kWaves; ++x) rtop = fmaxf(rtop, sm[x][lr]);
 #pragma unroll
-        for (int x = 0; x < kWaves; ++x) rl += sl[x][lr] * exp2_(sm[x][lr] - finite_top(rtop));
+        for (int x = 0; x < kWaves; ++x) rl += sl[x][lr] * exp2_((sm[x][lr] - finite_top(rtop)) * k.c);
         const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * RW + lr;
         const bool alone = sl_.count == 1;
         if ((!alone || k.logits) && (tid & 15) == 0) k.ml[part] = float2{rtop, rl};
@@ -757,20 +768,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 
 // (m, l) of one row over a sequence's slots, `stride` parts apart, by one
 // wave: lanes take slots in turn.
-__device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, int count) {
+__device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, int count, float c) {
     const int lane = threadIdx.x & 63;
     float top = -INFINITY, l = 0.f;
     for (int i = lane; i < count; i += 64) {
         const float2 x = ml[part + i * stride];
         const float mn = fmaxf(top, x.x), ms = finite_top(mn);
-        l = l * exp2_(top - ms) + x.y * exp2_(x.x - ms);
+        l = l * exp2_((top - ms) * c) + x.y * exp2_((x.x - ms) * c);
         top = mn;
     }
     float all = top;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) all = fmaxf(all, __shfl_xor(all, m));
     all = finite_top(all);
-    l *= exp2_(top - all);
+    l *= exp2_((top - all) * c);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) l += __shfl_xor(l, m);
     return float2{all, l};
@@ -780,9 +791,9 @@ __device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, i
 struct Joined {
     float m, l;
     f32x4 y;
-    __device__ inline void add(float mo, float lo, f32x4 yo) {
+    __device__ inline void add(float mo, float lo, f32x4 yo, float c) {
         const float mn = fmaxf(m, mo), ms = finite_top(mn);
-        const float f = exp2_(m - ms), fo = exp2_(mo - ms);
+        const float f = exp2_((m - ms) * c), fo = exp2_((mo - ms) * c);
         l = l * f + lo * fo;
         y = y * f + yo * fo;
         m = mn;
@@ -793,7 +804,7 @@ struct Joined {
 // in turn: D / 4 lanes across a row, the others across slots, a row per wave
 // or (many slots) per workgroup.  With scores, further workgroups each add
 // the weights of 1,024 tokens of a (sequence, head): a thread sums
-// 2^{x - m} / l over the rows, in their order, for four tokens.
+// 2^{c (y - m)} / l over the rows, in their order, for four tokens.
 template <typename T, int D, int RW>
 __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, long long joins,
                                                         long long score_blocks) {
@@ -820,14 +831,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
                 for (int i = (together ? w : 0) * kGroups + grp; i < sc.y; i += kGroups * each) {
                     const size_t at = part + i * stride;
                     const float2 ml = k.ml[at];
-                    x.add(ml.x, ml.y, *reinterpret_cast<const f32x4 *>(k.po + at * D + d));
+                    x.add(ml.x, ml.y, *reinterpret_cast<const f32x4 *>(k.po + at * D + d), k.c);
                 }
             }
 #pragma unroll
             for (int m = kAcross; m < 64; m <<= 1)
                 x.add(__shfl_xor(x.m, m), __shfl_xor(x.l, m),
                       f32x4{__shfl_xor(x.y.x, m), __shfl_xor(x.y.y, m), __shfl_xor(x.y.z, m),
-                            __shfl_xor(x.y.w, m)});
+                            __shfl_xor(x.y.w, m)}, k.c);
             if (together) {
                 __syncthreads();               // the last row's have been read
                 if (grp == 0) other[w][lane] = x;
@@ -836,7 +847,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
 #pragma unroll
                 for (int i = 1; i < kWaves; ++i) {
                     const Joined o = other[i][lane % kAcross];
-                    x.add(o.m, o.l, o.y);
+                    x.add(o.m, o.l, o.y, k.c);
                 }
             }
             if (q < a.n * a.Hq && grp == 0) {
@@ -873,7 +884,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
                 const size_t part = (size_t)sc.x * stride +
                                     ((size_t)h * k.plan.row_blocks + row / RW) * RW +
                                     row % RW;
-                const float2 x = join_ml(k.ml, part, stride, sc.y);
+                const float2 x = join_ml(k.ml, part, stride, sc.y, k.c);
                 if ((tid & 63) == 0) st[r] = float2{x.x, x.y == 0.f ? 0.f : 1.f / x.y};
             }
             __syncthreads();
@@ -885,7 +896,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
                     const f32x4 v = *reinterpret_cast<const f32x4 *>(x + r * k.cap32);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j + e >= sp.lo && j + e < sp.hi) sum[e] += exp2_(v[e] - st[r].x) * st[r].y;
+                        if (j + e >= sp.lo && j + e < sp.hi) sum[e] += exp2_((v[e] - st[r].x) * k.c) * st[r].y;
                 }
             }
         }
@@ -915,6 +926,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     k.po = reinterpret_cast<float *>(ws + w.o);
     k.logits = a.scores ? reinterpret_cast<float *>(ws + w.logits) : nullptr;
     k.cap32 = (cap + 31) / 32 * 32;
+    // (a scale of zero: the smallest number, whose products vanish, as
+    // 0 times a masked token's -inf would be NaN)
+    k.c = fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f);
+    k.negative = a.scale < 0.f;
     k.parts = k.plan.max_slots > a.B;
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
