@@ -538,15 +538,20 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(EvictArgs a, int lpr_shi
     }
 }
 
-// The same in place: a workgroup has 64 bytes of the rows of one (sequence,
-// head), of K (even blockIdx.y) or V, and goes through the rows in order, a
+constexpr int kCloseRows = 4;
+
+// The same in place: a workgroup has a column of the rows of one (sequence,
+// head), of K (even blockIdx.y) or V, 16 << slice_shift bytes wide, and goes through the rows in order, a
 // tile of them read, then written.  kept[i] >= i and kept ascends, so that a
 // tile's writes lie at or below its own reads and below all later ones, and
-// the next tile can be read before this one is written.
-__global__ __launch_bounds__(256) void close_up_kernel(EvictArgs a, int lpr_shift) {
-    constexpr int kRows = 64 * kMoveRows;
+// the next tile can be read before this one is written.  Columns are 64 bytes
+// wide, or 16 where the pairs are too few to fill the card (16,384 tokens kept
+// of 8 heads: 149 us at 64, 81 us at 16).
+__global__ __launch_bounds__(256) void close_up_kernel(EvictArgs a, int lpr_shift,
+                                                       int slice_shift) {
+    const int across = 256 >> slice_shift, tile_rows = across * kCloseRows;
     const int pair = blockIdx.x, b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x;
-    const int slice = blockIdx.y >> 1, c = 4 * slice + (tid & 3);
+    const int lane = tid & ((1 << slice_shift) - 1), c = ((blockIdx.y >> 1) << slice_shift) + lane;
     const int len = cached_len(a.seq_lens, b, a.map);
     const int m = len < a.budget ? len : a.budget;
     // (new_lens may be seq_lens: what another workgroup has written gives the
@@ -554,22 +559,22 @@ __global__ __launch_bounds__(256) void close_up_kernel(EvictArgs a, int lpr_shif
     if (blockIdx.y == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
     const int32_t *kept = a.kept + (size_t)pair * a.budget;
     u32x4 *cache = static_cast<u32x4 *>(blockIdx.y & 1 ? a.v_cache : a.k_cache);
-    const bool scores = blockIdx.y == 0 && (tid & 3) == 0;
+    const bool scores = blockIdx.y == 0 && lane == 0;
     struct Tile {
-        size_t dst[kMoveRows];
-        bool move[kMoveRows];
-        u32x4 x[kMoveRows];
-        float sc[kMoveRows];
+        size_t dst[kCloseRows];
+        bool move[kCloseRows];
+        u32x4 x[kCloseRows];
+        float sc[kCloseRows];
     };
     auto load = [&](int base, Tile &t) {
-        size_t src[kMoveRows];
+        size_t src[kCloseRows];
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            const int i = base + 64 * u + (tid >> 2), j = i < m ? kept[i] : i;
+        for (int u = 0; u < kCloseRows; ++u) {
+            const int i = base + across * u + (tid >> slice_shift), j = i < m ? kept[i] : i;
             t.move[u] = i != j && row_move(a, b, h, i, j, src[u], t.dst[u]);
         }
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
+        for (int u = 0; u < kCloseRows; ++u)
             if (t.move[u]) {
                 t.x[u] = cache[(src[u] << lpr_shift) + c];
                 if (scores) t.sc[u] = a.scores[src[u]];
@@ -577,14 +582,14 @@ __global__ __launch_bounds__(256) void close_up_kernel(EvictArgs a, int lpr_shif
     };
     Tile t;
     load(0, t);
-    for (int base = 0; base < m; base += kRows) {
+    for (int base = 0; base < m; base += tile_rows) {
         // the tile is read (vmcnt(0)) by every wave before any of it is written
         __builtin_amdgcn_s_waitcnt(0x0f70);
         __syncthreads();
         Tile next;
-        load(base + kRows, next);
+        load(base + tile_rows, next);
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
+        for (int u = 0; u < kCloseRows; ++u)
             if (t.move[u]) {
                 cache[(t.dst[u] << lpr_shift) + c] = t.x[u];
                 if (scores) a.scores[t.dst[u]] = t.sc[u];
@@ -628,7 +633,8 @@ hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s) 
         if (e != hipSuccess) return e;
     }
     if (a.in_place) {
-        close_up_kernel<<<dim3(pairs, 2 << (sh - 2)), 256, 0, s>>>(a, sh);
+        const int slice = pairs * (2 << (sh - 2)) >= 256 ? 2 : 0;
+        close_up_kernel<<<dim3(pairs, 2 << (sh - slice)), 256, 0, s>>>(a, sh, slice);
     } else {
         const int most = a.budget < capacity ? a.budget : (int)capacity;
         const int tile = (256 >> sh) * kMoveRows;
