@@ -53,7 +53,13 @@ __device__ inline Span seq_span(int len, int n, int window) {
 // sequences' last chunks would leave over a quarter of it idle (130,001
 // tokens: 57 us with C for 1,024 workgroups, 52 us so).  With more sequences
 // than that, C is for 1,024.
+//   Which slot is whose each workgroup finds for itself from the lengths, or,
+// with more than kScan sequences, a launch before finds for all (4,096
+// sequences of up to 1,000 tokens: 461 us and 378 us).  Past kMaxShared
+// sequences each is one slot.
 constexpr int kResident = 512;
+constexpr int kScan = 256;
+constexpr int kMaxShared = 1 << 16;
 constexpr int kMinChunk = 512;
 struct Plan {
     int units;            // workgroups of one slot: key-value heads x row blocks
@@ -72,6 +78,7 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
     const long long by_len = (capacity + kMinChunk - 1) / kMinChunk * B;
     const long long bound = (long long)p.want_slots + B;
     p.max_slots = (int)(by_len < bound ? (by_len < B ? B : by_len) : bound);
+    if (B > kMaxShared) p.max_slots = B;
     return p;
 }
 // Rows of a workgroup's block (RW), those of one MFMA tile.  More rows are
@@ -79,11 +86,12 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 // of 32 would need twice the registers there are.
 int block_rows(bool bf16_io, long long rows) { return bf16_io && rows > 16 ? 32 : 16; }
 
-// Workspace: {first slot, slots} of every sequence; (m, l) of every slot, unit
+// Workspace: {first slot, slots} of every sequence; with more than kScan of
+// them, every slot's {sequence, its first slot, its slots, tokens of one}; (m, l) of every slot, unit
 // and row; o of the same, unnormalised; with scores, the products q.k of every row
 // and token [B, Hkv, nG, cap].
 struct WsMap {
-    size_t sched, ml, o, logits, total;
+    size_t sched, slots, ml, o, logits, total;
 };
 WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bool with_scores) {
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -92,7 +100,8 @@ WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bo
     const bool parts = p.max_slots > B;
     WsMap w{};
     w.sched = 0;
-    w.ml = r256((size_t)B * 2 * sizeof(int));
+    w.slots = r256((size_t)B * 2 * sizeof(int));
+    w.ml = w.slots + (parts && B > kScan ? r256((size_t)p.max_slots * sizeof(int4)) : 0);
     w.o = w.ml + (parts || with_scores ? r256(rows * 2 * sizeof(float)) : 0);
     w.logits = w.o + (parts ? r256(rows * D * sizeof(float)) : 0);
     w.total = w.logits + (with_scores ? (size_t)B * Hkv * n * G * ((capacity + 31) / 32 * 32) *
@@ -104,6 +113,7 @@ struct KArgs {
     AttnArgs a;
     Plan plan;
     int2 *sched;
+    int4 *slots;          // nullptr: found by each workgroup
     float2 *ml;
     float *po;
     float *logits;        // nullptr: no scores
@@ -113,9 +123,9 @@ struct KArgs {
     bool parts;           // a sequence may have several slots
 };
 
-// Sum over the workgroup's threads before this one and over all; lds holds
-// kWaves values.
-template <typename N>
+// Sum over the workgroup's threads before this one and over all; lds holds a
+// value per wave.
+template <int WAVES, typename N>
 __device__ inline N group_scan(N x, N &total, N *lds) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     N incl = x;
@@ -129,7 +139,7 @@ __device__ inline N group_scan(N x, N &total, N *lds) {
     N before = 0;
     total = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
         const N v = lds[i];
         before += i < w ? v : 0;
         total += v;
@@ -141,54 +151,90 @@ __device__ inline N group_scan(N x, N &total, N *lds) {
 // A value that is the same in all lanes, for a scalar register.
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-struct Slot { int b, len, first, count, chunk; };  // sequence, its first slot, its slots, tokens of one
-// The sequence that slot s belongs to (b = -1: past the last slot).  Thread
-// i of the workgroup looks after sequences i per .. i per + per - 1.
+struct Slot { int b, first, count, chunk; };      // sequence, its first slot, its slots, tokens of one
+
+// Shares the sequences' slots out over a workgroup of 64 WAVES threads, thread
+// t looking after sequences t per .. t per + per - 1: begin() gives the
+// thread's first slot and all slots, next() goes through its sequences.
+template <int WAVES>
+struct Sharing {
+    const KArgs &k;
+    int per, b, end, at, chunk;
+    __device__ Sharing(const KArgs &k) : k(k) {
+        per = (k.a.B + 64 * WAVES - 1) / (64 * WAVES);
+        b = threadIdx.x * per;
+        end = b + per < k.a.B ? b + per : k.a.B;
+    }
+    __device__ inline int tokens(int i) const {
+        const AttnArgs &a = k.a;
+        const Span sp = seq_span(cached_len(a.seq_lens, i, a.map), a.n, a.window);
+        return sp.hi - sp.lo;
+    }
+    __device__ inline int slots_of(int tok) const {
+        const int n = (tok + chunk - 1) / chunk;
+        return n > 1 ? n : 1;
+    }
+    // returns all slots
+    __device__ inline int begin(int &mine) {
+        __shared__ long long lds64[WAVES];
+        __shared__ int lds32[WAVES];
+        long long sum = 0, total;
+#pragma unroll 4
+        for (int i = b; i < end; ++i) sum += tokens(i);
+        group_scan<WAVES, long long>(sum, total, lds64);
+        long long c = (total + k.plan.want_slots - 1) / k.plan.want_slots;
+        c = c < kMinChunk ? kMinChunk : (c > (1 << 30) ? 1 << 30 : c);
+        chunk = (int)((c + 127) / 128 * 128);
+        mine = 0;
+        int all;
+#pragma unroll 4
+        for (int i = b; i < end; ++i) mine += slots_of(tokens(i));
+        at = group_scan<WAVES, int>(mine, all, lds32);
+        return all;
+    }
+    // the slots of sequence b: alike, in multiples of 128 tokens
+    __device__ inline Slot next() {
+        const int tok = tokens(b), n = slots_of(tok);
+        const Slot s{b, at, n, ((tok + n - 1) / n + 127) & ~127};
+        ++b;
+        at += n;
+        return s;
+    }
+};
+
+// Every slot's owner, by one workgroup for all.
+__global__ __launch_bounds__(1024) void slots_kernel(KArgs k) {
+    Sharing<16> sh(k);
+    int mine;
+    const int all = sh.begin(mine);
+    while (sh.b < sh.end) {
+        const Slot s = sh.next();
+        for (int i = 0; i < s.count; ++i) k.slots[s.first + i] = int4{s.b, s.first, s.count, s.chunk};
+    }
+    for (int i = all + threadIdx.x; i < k.plan.max_slots; i += 1024) k.slots[i] = int4{-1, 0, 0, 0};
+}
+
+// The sequence that slot s belongs to (b = -1: past the last slot).
 __device__ inline Slot find_slot(const KArgs &k, int s) {
-    // too short a table for a second slot: slot and sequence are one
-    if (!k.parts) {
-        if (s >= k.a.B) return Slot{-1, 0, 0, 0, 0};
-        return Slot{s, uniform(cached_len(k.a.seq_lens, s, k.a.map)), s, 1, 1 << 29};
+    // no sequence has a second slot: slot and sequence are one
+    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 29};
+    if (k.slots) {
+        if (s >= k.plan.max_slots) return Slot{-1, 0, 0, 0};
+        const int4 x = k.slots[s];
+        return Slot{uniform(x.x), uniform(x.y), uniform(x.z), uniform(x.w)};
     }
-    __shared__ long long lds64[kWaves];
-    __shared__ int lds32[kWaves], found[5];
-    const AttnArgs &a = k.a;
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-    long long sum = 0, total;
-    for (int b = b0; b < b0 + per && b < a.B; ++b) {
-        const Span sp = seq_span(cached_len(a.seq_lens, b, a.map), a.n, a.window);
-        sum += sp.hi - sp.lo;
-    }
-    group_scan<long long>(sum, total, lds64);
-    long long c = (total + k.plan.want_slots - 1) / k.plan.want_slots;
-    c = c < kMinChunk ? kMinChunk : (c > (1 << 30) ? 1 << 30 : c);
-    const int chunk = (int)((c + 127) / 128 * 128);
-    int mine = 0, slots;
-    for (int b = b0; b < b0 + per && b < a.B; ++b) {
-        const Span sp = seq_span(cached_len(a.seq_lens, b, a.map), a.n, a.window);
-        const int ns = (sp.hi - sp.lo + chunk - 1) / chunk;
-        mine += ns > 1 ? ns : 1;
-    }
-    if (threadIdx.x == 0) found[0] = -1;
-    int at = group_scan<int>(mine, slots, lds32);
-    if (s >= at && s < at + mine) {
-        for (int b = b0; b < b0 + per && b < a.B; ++b) {
-            const int len = cached_len(a.seq_lens, b, a.map);
-            const Span sp = seq_span(len, a.n, a.window);
-            int ns = (sp.hi - sp.lo + chunk - 1) / chunk;
-            ns = ns > 1 ? ns : 1;
-            if (s < at + ns) {
-                found[0] = b; found[1] = at; found[2] = ns; found[4] = len;
-                // the sequence's slots alike, in multiples of 128 tokens
-                found[3] = ((sp.hi - sp.lo + ns - 1) / ns + 127) & ~127;
-                break;
-            }
-            at += ns;
-        }
+    __shared__ Slot found;
+    if (threadIdx.x == 0) found.b = -1;
+    Sharing<kWaves> sh(k);
+    int mine;
+    sh.begin(mine);
+    if (s >= sh.at && s < sh.at + mine) {
+        Slot x;
+        do x = sh.next(); while (s >= sh.at);
+        found = x;
     }
     __syncthreads();
-    return Slot{uniform(found[0]), uniform(found[4]), uniform(found[1]), uniform(found[2]),
-                uniform(found[3])};
+    return Slot{uniform(found.b), uniform(found.first), uniform(found.count), uniform(found.chunk)};
 }
 
 __device__ inline float swap_max16(float x) {
@@ -522,7 +568,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const Slot sl_ = find_slot(k, slot);
     const int b = sl_.b;
     if (b < 0) return;
-    const int len = sl_.len;
+    const int len = uniform(cached_len(a.seq_lens, b, a.map));
     const Span seq = seq_span(len, a.n, a.window);
     if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
 
@@ -931,6 +977,12 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     k.c = fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f);
     k.negative = a.scale < 0.f;
     k.parts = k.plan.max_slots > a.B;
+    k.slots = k.parts && a.B > kScan ? reinterpret_cast<int4 *>(ws + w.slots) : nullptr;
+    if (k.slots) {
+        slots_kernel<<<1, 1024, 0, s>>>(k);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
     if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, true><<<grid, kThreads, 0, s>>>(k);

@@ -164,6 +164,19 @@ def test_attend_many_sequences(dt):
     check_attend(q, kc, vc, table, lens, 0.2, 0, sc, what="scores")
 
 
+@pytest.mark.parametrize("B", [1025, 4096, 4500])
+def test_attend_thousands_of_sequences(B):
+    """Several sequences per thread of the search, and more than it takes; one
+    of them long."""
+    announce("attend %d sequences" % B)
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 20, B)]
+    lens[B // 2] = 1400
+    kc, vc, sc, table = make_cache(lens, 1, 64, 32, torch.bfloat16, seed=6)
+    q = queries(B, 1, 1, 64, torch.bfloat16, seed=7)
+    check_attend(q, kc, vc, table, lens, 0.2, 0, sc, what="scores")
+
+
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 def test_attend_absent_pages_and_odd_lengths(dt):
     """Pages that are absent (below, above and far outside the range), a
