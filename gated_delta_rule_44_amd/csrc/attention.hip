@@ -17,7 +17,9 @@
 // fp32), so that a token is read from HBM once for all of them, as MFMA
 // operands.  Bytes bound the kernel: 2 D elements a token against 4 D flops
 // per row and token is at most 32 flops a byte, where the card turns at
-// about 250.
+// about 250.  64 contexts of 512 to 8,192 tokens, 8 heads of 128 in bf16 (681
+// MB): 116 us, 5.9 TB/s, where a plain read of that size reaches 6.2 to 6.5 and
+// a copy 5.0; the same with K and V only loaded: 112 us.
 #include "cache_internal.h"
 #include "gdr_internal.h"
 #include "device_util.h"
@@ -548,7 +550,9 @@ template <int D> struct Tile<float, D, 16> {
 // joined through LDS at the end.  K and V go from HBM straight into the
 // registers that MFMA reads: the next tile to come is requested into a tile's
 // registers as they fall free, K after its logits are formed, V after its
-// product.
+// product.  The 180 registers of a thread (RW = 16, D = 128) let two
+// workgroups share a CU, 64 KiB on their way in each; three, by spilling,
+// measured 141 us where two take 120 (64 contexts).
 template <typename T, int D, int RW, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D, RW>;
