@@ -89,9 +89,9 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 int block_rows(bool bf16_io, long long rows) { return bf16_io && rows > 16 ? 32 : 16; }
 
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
-// them, every slot's {sequence, its first slot, its slots, tokens of one}; (m, l) of every slot, unit
-// and row; o of the same, unnormalised; with scores, the products q.k of every row
-// and token [B, Hkv, nG, cap].
+// them, every slot's {sequence, its first slot, its slots, tokens of one};
+// (m, l) of every slot, unit and row; o of the same, unnormalised; with
+// scores, the products q.k of every row and token [B, Hkv, nG, cap].
 struct WsMap {
     size_t sched, slots, ml, o, logits, total;
 };
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(1024) void slots_kernel(KArgs k) {
 // The sequence that slot s belongs to (b = -1: past the last slot).
 __device__ inline Slot find_slot(const KArgs &k, int s) {
     // no sequence has a second slot: slot and sequence are one
-    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 29};
+    if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 30};
     if (k.slots) {
         if (s >= k.plan.max_slots) return Slot{-1, 0, 0, 0};
         const int4 x = k.slots[s];
@@ -649,10 +649,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
             l += x[i];
         }
         const typename TL::P p = TL::weights(x);
-        // Where some row does not attend to a token that is there, its weight of
-        // zero must not meet an infinity or NaN.  Such values are taken out of V, and a
-        // row that attends to one gets +inf, -inf or (both, or NaN) their
-        // sum in that channel.
+        // Where some row does not attend to a token that is there, its weight
+        // of zero must not meet an infinity or NaN.  Such values are taken out
+        // of V, and a row that attends to one gets +inf, -inf or (both, or
+        // NaN) their sum in that channel.
         const int j1 = j0 + kTile < len ? j0 + kTile : len;
         if ((j0 < all_lo || j1 > all_hi) && __builtin_amdgcn_ballot_w64(TL::odd(vf))) {
             float in[kVals];
@@ -977,8 +977,8 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     k.logits = a.scores ? reinterpret_cast<float *>(ws + w.logits) : nullptr;
     k.cap32 = (cap + 31) / 32 * 32;
     // (a scale of zero: the smallest number, whose products vanish, as
-    // 0 times a masked token's -inf would be NaN)
-    k.c = fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f);
+    // 0 times a masked token's -inf would be NaN; nor is it infinite)
+    k.c = fminf(fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f), 3.4e38f);
     k.negative = a.scale < 0.f;
     k.parts = k.plan.max_slots > a.B;
     k.slots = k.parts && a.B > kScan ? reinterpret_cast<int4 *>(ws + w.slots) : nullptr;

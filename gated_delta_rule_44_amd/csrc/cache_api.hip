@@ -30,6 +30,11 @@ bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
                                       what, name);                                 \
     } while (0)
 
+// a * b * c >= limit, for non-negative factors whose product may not fit
+bool reaches(long long a, long long b, long long c, long long limit) {
+    return (__int128)a * b * c >= limit;
+}
+
 // the log2 of a supported page size, or -1
 int page_shift_of(int page_size) {
     for (int s = 4; s <= 8; ++s)
@@ -133,7 +138,8 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
 size_t gdr_attention_workspace_bytes(int B, int n_tok, int Hq, int Hkv, int D, int max_pages,
                                      int page_size, int with_scores) {
     if (B <= 0 || n_tok <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_pages <= 0 ||
-        page_shift_of(page_size) < 0)
+        page_shift_of(page_size) < 0 || (long long)max_pages * page_size >= (1LL << 30) ||
+        reaches(B, n_tok, Hq, kMaxQueryRows))
         return 0;
     return gdr::attention_workspace(B, n_tok, Hq, Hkv, D, (long long)max_pages * page_size,
                                     with_scores != 0);
@@ -154,9 +160,9 @@ gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int
         return fail(GDR_EINVAL, "%s: Hq (%d) is not a multiple of Hkv (%d)", what, Hq, Hkv);
     if (!isfinite(scale)) return fail(GDR_EINVAL, "%s: scale is not finite", what);
     if (window < 0) return fail(GDR_EINVAL, "%s: window = %d; 0 means none", what, window);
-    if ((long long)B * n_tok * Hq >= kMaxQueryRows)
-        return fail(GDR_EUNSUPPORTED, "%s: %lld query rows exceed %lld", what,
-                    (long long)B * n_tok * Hq, kMaxQueryRows);
+    if (reaches(B, n_tok, Hq, kMaxQueryRows))
+        return fail(GDR_EUNSUPPORTED, "%s: %d x %d x %d query rows exceed %lld", what, B, n_tok, Hq,
+                    kMaxQueryRows);
     if (page_table_host) {
         unsigned char *once = nullptr;
         if (scores) {
@@ -195,7 +201,7 @@ gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int
 
 size_t gdr_cache_evict_workspace_bytes(int B, int Hkv, int max_pages, int page_size) {
     if (B <= 0 || Hkv <= 0 || max_pages <= 0 || page_shift_of(page_size) < 0 ||
-        (long long)B * Hkv >= kMaxPairs)
+        (long long)B * Hkv >= kMaxPairs || (long long)max_pages * page_size >= (1LL << 30))
         return 0;
     return gdr::evict_workspace(B * Hkv, (long long)max_pages * page_size);
 }

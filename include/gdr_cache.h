@@ -23,7 +23,7 @@
  * row-major tensors, 16-byte alignment -- page tables, lengths and offsets
  * 4-byte --, host checks before any HIP call, no allocation or
  * synchronisation, gdr_status codes, gdr_last_error, GDR_DEBUG).  Results
- * are the same bits on every run: nothing is summed by atomics.
+ * are the same bits on every run: no floating-point sum goes through atomics.
  *
  * Supported shapes: D in {64, 128}; page_size in {16, 32, 64, 128, 256};
  * max_pages * page_size < 2^30; num_pages * Hkv < 2^31; per call fewer than

@@ -112,6 +112,7 @@ def attend(lib, dt=1, B=2, n=1, Hq=4, Hkv=2, D=128, scale=1.0, window=0, q=FAKE,
     (dict(scale=float("inf")), EINVAL, "scale"),
     (dict(window=-1), EINVAL, "window"),
     (dict(B=1 << 13, n=1 << 8), EUNSUPPORTED, "query rows"),
+    (dict(B=1 << 30, n=1 << 30, Hq=16), EUNSUPPORTED, "query rows"),
     (dict(q=None), EINVAL, "q is NULL"),
     (dict(o=MIS), EINVAL, "o is not 16-byte aligned"),
     (dict(lens=None), EINVAL, "seq_lens is NULL"),
@@ -172,6 +173,10 @@ def test_workspace_sizes(lib):
     assert ws(2, 1, 5, 2, 128, 4, 16) == 0
     assert ws(2, 1, 4, 2, 128, 4, 24) == 0
     assert ws(2, 1, 4, 2, 128, 0, 16) == 0
+    big = 2 ** 31 - 1
+    assert ws(big, big, big, 1, 128, 4, 16) == 0
+    assert ws(1 << 30, 1 << 30, 16, 16, 128, 4, 16) == 0
+    assert ws(2, 1, 4, 2, 128, big, 256) == 0
     # grows with the table where logits are kept for the scores
     assert ws(2, 1, 4, 2, 128, 64, 16, True) >= ws(2, 1, 4, 2, 128, 64, 16)
 
@@ -180,6 +185,7 @@ def test_workspace_sizes(lib):
     assert gdr.evict_workspace_bytes(2, 2, 4, 16) == 0
     assert gdr.evict_workspace_bytes(200, 2, 4000, 16) == 0
     assert gdr.evict_workspace_bytes(2, 2, 4000, 16) > 0
+    assert gdr.evict_workspace_bytes(2, 2, big, 256) == 0
 
 
 def test_binding_rejects_host_tensors():
