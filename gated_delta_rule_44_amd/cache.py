@@ -26,21 +26,18 @@ _current_device = torch._C._cuda_getDevice
 
 # A decode step is microseconds of GPU work, so the checks cost as little as
 # they can: one test per tensor, and a message only for one that fails.
-def _gpu(name, t, dtype, dev):
-    if not (isinstance(t, _Tensor) and t.dtype == dtype and t.device == dev
+def _gpu(name, t, dtype, dev, shape=None):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.device == dev
             and t.is_contiguous()):
         _dense(name, t, dtype, dev)
-
-
-def _shape(name, t, shape):
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise GdrError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
 
 
 def _cache(k_cache, v_cache, scores):
-    """Checks of the caches and their scores; returns their device, dtype
-    code and P, Hkv, page, D."""
-    if not isinstance(k_cache, _Tensor) or not k_cache.is_cuda:
+    """Checks of the caches and their scores; returns their device, dtype,
+    dtype code and shape (P, Hkv, page, D)."""
+    if not (isinstance(k_cache, _Tensor) and k_cache.is_cuda and k_cache.is_contiguous()):
         _dense("k_cache", k_cache)
     dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
     dt = _DTYPES.get(dtype)
@@ -48,13 +45,10 @@ def _cache(k_cache, v_cache, scores):
         raise GdrError("the cache must be bfloat16 or float32, got %s" % dtype)
     if len(shape) != 4 or shape[1] < 1:
         raise GdrError("k_cache must be [P,Hkv,page,D], got %s" % list(shape))
-    _gpu("k_cache", k_cache, dtype, dev)
-    _gpu("v_cache", v_cache, dtype, dev)
-    _shape("v_cache", v_cache, shape)
+    _gpu("v_cache", v_cache, dtype, dev, shape)
     if scores is not None:
-        _gpu("scores", scores, _FLOAT32, dev)
-        _shape("scores", scores, shape[:3])
-    return dev, dt, shape
+        _gpu("scores", scores, _FLOAT32, dev, shape[:3])
+    return dev, dtype, dt, shape
 
 
 def _int(name, x, lo):
@@ -119,11 +113,10 @@ def cache_append(k, v, start, page_table, k_cache, v_cache, scores=None, cu_seql
     Positions outside the table or on an absent page are left out.  scores,
     when given, are set to 0 at every position written.
     """
-    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
-    _gpu("k", k, k_cache.dtype, dev)
-    _gpu("v", v, k_cache.dtype, dev)
+    dev, dtype, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("k", k, dtype, dev)
     shape, host = k.shape, None
-    _shape("v", v, shape)
+    _gpu("v", v, dtype, dev, shape)
     if cu_seqlens is None:
         _need(len(shape) == 4 and shape[2:] == (Hkv, D), "k must be [B,n,Hkv,D]")
         B, n = shape[0], shape[1]
@@ -137,8 +130,7 @@ def cache_append(k, v, start, page_table, k_cache, v_cache, scores=None, cu_seql
         if cu_seqlens_host is not None:
             host = _host_i32(cu_seqlens_host, B + 1, "cu_seqlens_host")
     _int("the number of tokens", T, 0)
-    _gpu("start", start, _INT32, dev)
-    _shape("start", start, (B,))
+    _gpu("start", start, _INT32, dev, (B,))
     M = _table("page_table", page_table, B, dev)
     _call(dev, _load().gdr_cache_append, dt, B, n, T, Hkv, D, k.data_ptr(), v.data_ptr(),
           _p(cu_seqlens), _hp(host), start.data_ptr(), page_table.data_ptr(), M, page, P,
@@ -167,23 +159,23 @@ def attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, wind
     to one sequence; page_table_host, a host copy, makes the library validate
     that).  A row that attends to nothing gives zeros.  Returns o [B,n,Hq,D].
     """
-    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
-    _gpu("q", q, k_cache.dtype, dev)
+    dev, dtype, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("q", q, dtype, dev)
     shape = q.shape
     if len(shape) != 4 or shape[3] != D:
         raise GdrError("q must be [B,n,Hq,D] with D = %d, got %s" % (D, list(shape)))
     B, n, Hq, _ = shape
     if Hq < 1 or Hq % Hkv:
         raise GdrError("Hq (%d) must be a multiple of Hkv (%d)" % (Hq, Hkv))
-    _gpu("seq_lens", seq_lens, _INT32, dev)
-    _shape("seq_lens", seq_lens, (B,))
+    _gpu("seq_lens", seq_lens, _INT32, dev, (B,))
     M = _table("page_table", page_table, B, dev)
-    host = _host_table("page_table_host", page_table_host, (B, M))
+    host = None
+    if page_table_host is not None:
+        host = _host_table("page_table_host", page_table_host, (B, M))
     if o is None:
         o = torch.empty_like(q)
     else:
-        _gpu("o", o, k_cache.dtype, dev)
-        _shape("o", o, shape)
+        _gpu("o", o, dtype, dev, shape)
     _int("window", window, 0)
     lib = _load()
     if workspace is None:
@@ -220,7 +212,7 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     evict_workspace_bytes(...) bytes) is allocated when needed and not given.
     """
     _need(scores is not None, "scores are required")
-    dev, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    dev, _, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
     _gpu("seq_lens", seq_lens, _INT32, dev)
     _need(seq_lens.dim() == 1, "seq_lens must be [B]")
     B = seq_lens.shape[0]
@@ -233,18 +225,19 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
     if new_page_table is not None:
         M2 = _table("new_page_table", new_page_table, B, dev)
         host2 = _host_table("new_page_table_host", new_page_table_host, (B, M2))
+        # (an empty table has no address, which would mean in place)
+        _need(M2 * page >= min(budget, M * page), "new_page_table holds %d tokens, %d are kept"
+              % (M2 * page, min(budget, M * page)))
     else:
         _need(new_page_table_host is None, "new_page_table_host given without new_page_table")
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
     else:
-        _gpu("new_lens", new_lens, _INT32, dev)
-        _shape("new_lens", new_lens, (B,))
+        _gpu("new_lens", new_lens, _INT32, dev, (B,))
     if kept is None:
         kept = torch.empty((B, Hkv, budget), device=dev, dtype=_INT32)
     else:
-        _gpu("kept", kept, _INT32, dev)
-        _shape("kept", kept, (B, Hkv, budget))
+        _gpu("kept", kept, _INT32, dev, (B, Hkv, budget))
     lib = _load()
     if workspace is None:
         nbytes = lib.gdr_cache_evict_workspace_bytes(B, Hkv, M, page)

@@ -361,6 +361,72 @@ def test_attend_other_stream_and_graph():
             assert same(a, b), "replay %d" % rep
 
 
+def test_two_calls_at_once_on_two_streams():
+    """Different batches on two streams, each with a workspace of its own."""
+    runs, want = [], []
+    for i, lens in enumerate(([3000, 10, 700], [900, 1200, 2])):
+        kc, vc, sc, table = make_cache(lens, 2, 128, 32, torch.bfloat16, seed=95 + i)
+        q = queries(3, 2, 8, 128, torch.bfloat16, seed=97 + i)
+        args = [gpu(q), gpu(kc), gpu(vc), i32(table), i32(lens)]
+        runs.append((args, torch.nan_to_num(gpu(sc))))
+    sync()
+    for args, sc in runs:
+        s = sc.clone()
+        want.append((gdr.attention_decode(*args, scores=s), s))
+    sync()
+    streams = [torch.cuda.Stream(DEV) for _ in runs]
+    for rep in range(5):
+        got = []
+        for st, (args, sc) in zip(streams, runs):
+            with torch.cuda.stream(st):
+                s = sc.clone()
+                got.append((gdr.attention_decode(*args, scores=s), s))
+        sync()
+        for a, b in zip(got, want):
+            assert same(a[0], b[0]) and same(a[1], b[1]), rep
+
+
+def test_refusals_of_the_binding():
+    """Wrong dtypes, shapes, places and strides raise and write nothing."""
+    kc, vc, sc, table = make_cache([40, 20], 2, 64, 16, torch.bfloat16, seed=99)
+    k, v, s, t, lens = gpu(kc), gpu(vc), gpu(sc), i32(table), i32([40, 20])
+    q = gpu(queries(2, 1, 4, 64, torch.bfloat16, seed=100))
+    new = gpu(queries(2, 1, 2, 64, torch.bfloat16, seed=101))
+    good = dict(q=q, k_cache=k, v_cache=v, page_table=t, seq_lens=lens)
+    for name, bad in [("q", q.float()), ("q", q[:, :, :3].contiguous()), ("q", q.cpu()), ("q", None),
+                      ("q", q[:, 0]), ("q", q.expand(2, 1, 4, 64).transpose(1, 2)),
+                      ("k_cache", k.half()), ("k_cache", k[:, :, :8]), ("k_cache", kc),
+                      ("v_cache", v[:-1]), ("v_cache", v.float()), ("page_table", t.long()),
+                      ("page_table", t[:1].contiguous()), ("page_table", t.t()),
+                      ("seq_lens", lens.float()), ("seq_lens", lens[:1]), ("seq_lens", [40, 20]),
+                      ("window", -1), ("window", 2 ** 32), ("scores", s[:, :1].contiguous()),
+                      ("scores", s.double()), ("o", q.float()), ("o", q[:1]),
+                      ("scale", float("nan")), ("page_table_host", table[:, :1]),
+                      ("page_table_host", table + 1000),
+                      ("workspace", torch.empty(8, dtype=torch.uint8, device=DEV)),
+                      ("workspace", torch.empty(1 << 20, dtype=torch.uint8))]:
+        with pytest.raises(gdr.GdrError):
+            gdr.attention_decode(**{**good, name: bad})
+    good = dict(k=new, v=new, start=lens, page_table=t, k_cache=k, v_cache=v)
+    for name, bad in [("k", new.float()), ("k", new[:, :, :1].contiguous()), ("v", new[:1]),
+                      ("start", lens.long()), ("start", lens[:1]), ("cu_seqlens", lens),
+                      ("cu_seqlens_host", [0, 1, 2]), ("scores", s[:-1])]:
+        with pytest.raises(gdr.GdrError):
+            gdr.cache_append(**{**good, name: bad})
+    good = dict(k_cache=k, v_cache=v, scores=s, page_table=t, seq_lens=lens, budget=16)
+    twice = table.copy()
+    twice[1, 0] = twice[0, 0]
+    for name, bad in [("scores", None), ("budget", 0), ("budget", 2 ** 31), ("recent", -1),
+                      ("recent", 17), ("sink", 17), ("new_lens", lens.long()),
+                      ("new_lens", lens[:1]), ("page_table_host", twice),
+                      ("kept", torch.empty(2, 2, 15, dtype=torch.int32, device=DEV)),
+                      ("new_page_table", t[:, :0].contiguous()), ("new_page_table_host", table)]:
+        with pytest.raises(gdr.GdrError):
+            gdr.cache_evict(**{**good, name: bad})
+    sync()
+    assert same(k, kc) and same(v, vc) and same(s, sc)
+
+
 # --------------------------------------------------------------------- append
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("D,page,Hkv,n", [(128, 16, 2, 1), (64, 64, 3, 5), (128, 256, 1, 40),
