@@ -86,7 +86,19 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 // Rows of a workgroup's block (RW), those of one MFMA tile.  More rows are
 // several blocks, which read K and V from L2 after the first.  In fp32 a block
 // of 32 would need twice the registers there are.
-int block_rows(bool bf16_io, long long rows) { return bf16_io && rows > 16 ? 32 : 16; }
+//   Over 32 rows with much to read, 64: two tiles of rows share the tokens
+// through LDS (16 new tokens, 4 heads of 4 rows each: 16 contexts of 2,000
+// tokens 27 us against 40 in blocks of 32, 2 of 16,000 28 against 37).  With
+// little to read the two blocks side by side are done sooner (16 contexts of
+// 1,000: 21 us against 26; one of 300: 11 against 17).  The lengths are on the
+// device, so what the table and the window let a sequence attend to decides.
+constexpr long long kShareBytes = 64LL << 20;
+int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long long capacity,
+               int window) {
+    if (!bf16_io || rows <= 16) return 16;
+    const long long seen = window > 0 && window < capacity - n ? window + n : capacity;
+    return rows > 32 && seen * B * Hkv * D * 4 >= kShareBytes ? 64 : 32;
+}
 
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
 // them, every slot's {sequence, its first slot, its slots, tokens of one};
@@ -280,6 +292,14 @@ struct Src { size_t at; unsigned bytes; };
 //     acc[c][i] is channel dim(c, m(i, g)) of query row r.
 template <typename T, int D, int RW> struct Tile;
 
+// Where chunk c (16 bytes) of a row lies in a tile in LDS: row by row, the
+// chunks exchanged by the row's number, so that the rows of a K operand are in
+// different banks.
+template <int ROW_BYTES>
+__device__ inline int chunk_at(int row, int c) {
+    const int swap = ROW_BYTES >= 256 ? row & 15 : (row >> 1) & 7;
+    return row * ROW_BYTES + ((c ^ swap) << 4);
+}
 // two keys' values of one channel pair -> channel c of both
 __device__ inline unsigned pick2(unsigned k0, unsigned k1, int c) {
     return __builtin_amdgcn_perm(k1, k0, c & 1 ? 0x07060302u : 0x05040100u);
@@ -383,6 +403,22 @@ template <int D, int RW> struct Tile<bf16, D, RW> {
             } else {
                 v.w[i][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc[block(i)], off, 0, STREAM ? 2 : 0);
             }
+        }
+    }
+    // the same from a tile that lies in LDS (RW = 32)
+    __device__ static inline void lds_k(K &k, const char *t, int lane) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            k.f[0][i] = *reinterpret_cast<const bf16x8 *>(
+                t + chunk_at<kRowBytes>(lane % RW, kGroups * i + lane / RW));
+    }
+    __device__ static inline void lds_v(V &v, const char *t, int lane) {
+        const int g = lane / RW, at = lane % RW * PER * 2;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) {
+            const char *p = t + chunk_at<kRowBytes>(key(i, g), at >> 4) + (at & 15);
+#pragma unroll
+            for (int j = 0; j < PER / 2; ++j) v.w[i][j] = reinterpret_cast<const unsigned *>(p)[j];
         }
     }
     __device__ static inline void logits(float (&x)[kVals], const K &k, const Q &q) {
@@ -545,24 +581,33 @@ template <int D> struct Tile<float, D, 16> {
     }
 };
 
-// Workgroup = (slot, key-value head, row block of RW rows).  Its four waves
-// take the slot's tiles of tokens in turn, each with m, l and o of its own,
-// joined through LDS at the end.  K and V go from HBM straight into the
-// registers that MFMA reads: the next tile to come is requested into a tile's
-// registers as they fall free, K after its logits are formed, V after its
-// product.  The 180 registers of a thread (RW = 16, D = 128) let two
-// workgroups share a CU, 64 KiB on their way in each; three, by spilling,
-// measured 141 us where two take 120 (64 contexts).
-template <typename T, int D, int RW, bool STREAM>
+// Workgroup = (slot, key-value head, block of RW RT rows).  Its four waves are
+// RT tiles of rows times 4 / RT shares, which take the slot's tiles of tokens
+// in turn, each wave with m, l and o of its own, joined through LDS at the end.
+//   RT = 1: K and V go from HBM straight into the registers that MFMA reads:
+// the next tile to come is requested into a tile's registers as they fall
+// free, K after its logits are formed, V after its product.  The 180 registers of
+// a thread (RW = 16, D = 128) let two workgroups share a CU, 64 KiB on their way
+// in each; three, by spilling, measured 141 us where two take 120 (64 contexts).
+//   RT = 2: two waves read each tile, which all threads bring into LDS
+// together, a stage (a tile per share) at a time: one stage is worked on while
+// the next comes into registers, to be written beside it.  At D = 128 the 34
+// registers that the path for infinities and NaN in V costs are spilled: 62 us
+// for 16 contexts of 1,000 to 6,000, 55 without that path, 74 with RT = 1.
+template <typename T, int D, int RW, int RT, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D, RW>;
     constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = TL::kTile, kVals = TL::kVals;
-    constexpr int kPad = D + 4;
+    constexpr int kPad = D + 4, kShares = kWaves / RT, kRows = RW * RT;
+    constexpr int kTileBytes = kTile * TL::kRowBytes, kStage = kShares * 2 * kTileBytes;
+    constexpr int kOBytes = kWaves * RW * kPad * (int)sizeof(float);
     __shared__ float sm[kWaves][RW], sl[kWaves][RW];
-    __shared__ __align__(16) float so[kWaves][RW][kPad];
+    // the two stages, and at the end every wave's o
+    __shared__ __align__(16) char lds[RT > 1 && 2 * kStage > kOBytes ? 2 * kStage : kOBytes];
+    float(*so)[RW][kPad] = reinterpret_cast<float(*)[RW][kPad]>(lds);
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane % RW, g = lane / RW;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), rt = w % RT, share = w / RT;
     // the row blocks of one (slot, head) follow each other on one XCD, which
     // holds their K and V in its L2 (workgroups go to the eight XCDs in turn)
     const int wg = blockIdx.x;
@@ -577,7 +622,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
 
     // this lane's query row and what it attends to
-    const int rows = a.n * a.G, row0 = rb * RW, row = row0 + r;
+    const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + RW * rt + r;
     Span sp{0, 0};
     typename TL::Q q;
     {
@@ -591,7 +636,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     // the block's tokens: what its rows attend to, within the slot
     const Span first = token_span(len, a.n, a.window, row0 / a.G);
     const Span last = token_span(len, a.n, a.window,
-                                 ((row0 + RW < rows ? row0 + RW : rows) - 1) / a.G);
+                                 ((row0 + kRows < rows ? row0 + kRows : rows) - 1) / a.G);
     const int c_lo = seq.lo + (slot - sl_.first) * sl_.chunk;
     const int c_hi = c_lo + sl_.chunk < len ? c_lo + sl_.chunk : len;
     const int k_lo = first.lo > c_lo ? first.lo : c_lo, k_hi = last.hi < c_hi ? last.hi : c_hi;
@@ -679,12 +724,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         for (int c = 0; c < PER; ++c) acc[c] = TL::pv(vf, c, p, acc[c]);
     };
 
-    // Pages of this wave's next 64 tiles, one per lane (of the table's
-    // entries past the length too, which block_src leaves out).
+    // Pages of the next 64 tiles from i0 on, kStep apart, one per lane (of the
+    // table's entries past the length too, which block_src leaves out).
+    constexpr int kStep = RT == 1 ? kWaves : 1;
     const int cap = a.map.max_pages << a.map.page_shift;
     int pg[kBlocks];
     auto load_pages = [&](int i0) {
-        const int j = (tile0 + i0 + kWaves * lane) * kTile;
+        const int j = (tile0 + i0 + kStep * lane) * kTile;
 #pragma unroll
         for (int blk = 0; blk < kBlocks; ++blk)
             pg[blk] = j + 16 * blk < cap ? page_of(a.map, b, j + 16 * blk) : -1;
@@ -704,60 +750,137 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         if (!some) s.at = 0;
         return s;
     };
-    // D = 64: two tiles on their way, in two sets of registers.  D = 128: one,
-    // as a second set's 64 registers would spill (64 contexts 125 -> 136 us
-    // with it; D = 64 in fp32, 8 contexts: 35 -> 31 us).
-    constexpr bool kTwo = D == 64;
-    struct Ahead {
-        typename TL::K kf;
-        typename TL::V vf;
-        Src src[kBlocks];
-    } s0, s1;
-    int at = 0;                                 // tiles whose loads have been issued
-    auto load_k = [&](Ahead &s) {
-        if ((at & 63) == 0) load_pages(w + kWaves * at);
+    if constexpr (RT == 1) {
+        // D = 64: two tiles on their way, in two sets of registers.  D = 128: one,
+        // as a second set's 64 registers would spill (64 contexts 125 -> 136 us
+        // with it; D = 64 in fp32, 8 contexts: 35 -> 31 us).
+        constexpr bool kTwo = D == 64;
+        struct Ahead {
+            typename TL::K kf;
+            typename TL::V vf;
+            Src src[kBlocks];
+        } s0, s1;
+        int at = 0;                                 // tiles whose loads have been issued
+        auto load_k = [&](Ahead &s) {
+            if ((at & 63) == 0) load_pages(w + kWaves * at);
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk)
-            s.src[blk] = block_src(w + kWaves * at, at & 63, blk);
-        TL::template load_k<STREAM>(s.kf, kc, s.src, a.map.page_shift > 4, lane);
-        ++at;
-    };
-    auto load_v = [&](Ahead &s) {
-        rsrc_t rs[kBlocks];
+            for (int blk = 0; blk < kBlocks; ++blk)
+                s.src[blk] = block_src(w + kWaves * at, at & 63, blk);
+            TL::template load_k<STREAM>(s.kf, kc, s.src, a.map.page_shift > 4, lane);
+            ++at;
+        };
+        auto load_v = [&](Ahead &s) {
+            rsrc_t rs[kBlocks];
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) rs[blk] = make_rsrc(vc + s.src[blk].at, s.src[blk].bytes);
-        TL::template load_v<STREAM>(s.vf, rs, lane);
-    };
-    auto work = [&](int i, Ahead &s) {
-        const int j0 = (tile0 + i) * kTile;
-        float x[kVals];
-        bool here[kBlocks], full = j0 >= all_lo && j0 + kTile <= all_hi;
-        TL::logits(x, s.kf, q);
+            for (int blk = 0; blk < kBlocks; ++blk)
+                rs[blk] = make_rsrc(vc + s.src[blk].at, s.src[blk].bytes);
+            TL::template load_v<STREAM>(s.vf, rs, lane);
+        };
+        auto work = [&](int i, Ahead &s) {
+            const int j0 = (tile0 + i) * kTile;
+            float x[kVals];
+            bool here[kBlocks], full = j0 >= all_lo && j0 + kTile <= all_hi;
+            TL::logits(x, s.kf, q);
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) {
-            here[blk] = s.src[blk].bytes != 0;
-            full &= here[blk];
-        }
-        load_k(s);
-        absorb(j0, x, s.vf, full, here);
-        load_v(s);
-    };
-    load_k(s0);
-    load_v(s0);
-    if constexpr (kTwo) {
-        load_k(s1);
-        load_v(s1);
-    }
-    for (int i = w; i < tiles; i += kWaves) {
-        work(i, s0);
+            for (int blk = 0; blk < kBlocks; ++blk) {
+                here[blk] = s.src[blk].bytes != 0;
+                full &= here[blk];
+            }
+            load_k(s);
+            absorb(j0, x, s.vf, full, here);
+            load_v(s);
+        };
+        load_k(s0);
+        load_v(s0);
         if constexpr (kTwo) {
-            i += kWaves;
-            if (i >= tiles) break;
-            work(i, s1);
+            load_k(s1);
+            load_v(s1);
+        }
+        for (int i = w; i < tiles; i += kWaves) {
+            work(i, s0);
+            if constexpr (kTwo) {
+                i += kWaves;
+                if (i >= tiles) break;
+                work(i, s1);
+            }
+        }
+    } else {
+        constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTileBytes / 16 / kThreads;
+        static_assert(kUnits * kThreads * 16 == kTileBytes && 64 / kChunks <= 16,
+                      "threads cover a tile, a wave's rows lie in one block of 16");
+        // 16 bytes of K and of V per thread, share and unit, and which blocks
+        // of this wave's own tile are there
+        u32x4 kv[kShares][kUnits][2];
+        bool come[kBlocks];
+        int paged = 0;                          // the tile that lane 0 of pg stands for
+        load_pages(0);
+        auto load = [&](int it) {
+#pragma unroll
+            for (int x = 0; x < kShares; ++x) {
+                const int i = it * kShares + x;
+                if (i >= paged + 64) {
+                    paged = i;
+                    load_pages(i);
+                }
+                Src src[kBlocks];
+#pragma unroll
+                for (int blk = 0; blk < kBlocks; ++blk) {
+                    src[blk] = block_src(i, i - paged, blk);
+                    if (x == share) come[blk] = src[blk].bytes != 0;
+                }
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int unit = tid + kThreads * u, row = unit / kChunks;
+                    const bool second = uniform(row >> 4) != 0;
+                    const size_t at = second ? src[kBlocks - 1].at : src[0].at;
+                    const unsigned bytes = second ? src[kBlocks - 1].bytes : src[0].bytes;
+                    const unsigned off = (row & 15) * TL::kRowBytes + unit % kChunks * 16;
+                    kv[x][u][0] = load16<STREAM>(make_rsrc(kc + at, bytes), off);
+                    kv[x][u][1] = load16<STREAM>(make_rsrc(vc + at, bytes), off);
+                }
+            }
+        };
+        auto put = [&](char *to, bool (&here)[kBlocks]) {
+#pragma unroll
+            for (int x = 0; x < kShares; ++x)
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const int unit = tid + kThreads * u;
+                    char *p = to + 2 * x * kTileBytes +
+                              chunk_at<TL::kRowBytes>(unit / kChunks, unit % kChunks);
+                    *reinterpret_cast<u32x4 *>(p) = kv[x][u][0];
+                    *reinterpret_cast<u32x4 *>(p + kTileBytes) = kv[x][u][1];
+                }
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) here[blk] = come[blk];
+        };
+        const int its = (tiles + kShares - 1) / kShares;
+        bool here[kBlocks];
+        load(0);
+        put(lds, here);
+        __syncthreads();
+        for (int it = 0; it < its; ++it) {
+            load(it + 1);                       // past the last tile: zeros
+            const int j0 = (tile0 + it * kShares + share) * kTile;
+            const char *t = lds + (it & 1) * kStage + 2 * share * kTileBytes;
+            float x[kVals];
+            bool full = j0 >= all_lo && j0 + kTile <= all_hi;
+#pragma unroll
+            for (int blk = 0; blk < kBlocks; ++blk) full &= here[blk];
+            {
+                typename TL::K kf;
+                TL::lds_k(kf, t, lane);
+                TL::logits(x, kf, q);
+            }
+            typename TL::V vf;
+            TL::lds_v(vf, t + kTileBytes, lane);
+            absorb(j0, x, vf, full, here);
+            put(lds + ((it + 1) & 1) * kStage, here);
+            __syncthreads();
         }
     }
 
-    // join the waves: every wave's o in units of their common maximum, summed
+    // join the shares: every wave's o in units of the common maximum, summed
     // row by row
     l = row_sum(l);
     if (g == 0) {
@@ -767,7 +890,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, sm[i][r]);
+    for (int i = 0; i < kShares; ++i) top = fmaxf(top, sm[rt + RT * i][r]);
     const float f = exp2_((m - finite_top(top)) * k.c);
     // acc[c][e] is channel dim(c, e, g); those of adjacent c lie together
     constexpr int kRun = PER < 4 ? PER : 4;
@@ -784,15 +907,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     __syncthreads();
     // 16 threads per row, four channels at a time
 #pragma unroll
-    for (int i = 0; i < RW / 16; ++i) {
-        const int lr = 16 * i + (tid >> 4), orow = row0 + lr;
+    for (int i = 0; i < kRows / 16; ++i) {
+        const int br = 16 * i + (tid >> 4), orow = row0 + br, ot = br / RW, lr = br % RW;
         if (orow >= rows) break;
         float rtop = -INFINITY, rl = 0.f;
 #pragma unroll
-        for (int x = 0; x < kWaves; ++x) rtop = fmaxf(rtop, sm[x][lr]);
+        for (int x = 0; x < kShares; ++x) rtop = fmaxf(rtop, sm[ot + RT * x][lr]);
 #pragma unroll
-        for (int x = 0; x < kWaves; ++x) rl += sl[x][lr] * exp2_((sm[x][lr] - finite_top(rtop)) * k.c);
-        const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * RW + lr;
+        for (int x = 0; x < kShares; ++x)
+            rl += sl[ot + RT * x][lr] * exp2_((sm[ot + RT * x][lr] - finite_top(rtop)) * k.c);
+        const size_t part = ((size_t)slot * k.plan.units + h * k.plan.row_blocks + rb) * kRows + br;
         const bool alone = sl_.count == 1;
         if ((!alone || k.logits) && (tid & 15) == 0) k.ml[part] = float2{rtop, rl};
         const float inv = 1.f / rl;
@@ -801,9 +925,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
         for (int u = 0; u < D / 64; ++u) {
             const int d = 64 * u + 4 * (tid & 15);
-            f32x4 y = *reinterpret_cast<const f32x4 *>(&so[0][lr][d]);
+            f32x4 y = *reinterpret_cast<const f32x4 *>(&so[ot][lr][d]);
 #pragma unroll
-            for (int x = 1; x < kWaves; ++x) y += *reinterpret_cast<const f32x4 *>(&so[x][lr][d]);
+            for (int x = 1; x < kShares; ++x)
+                y += *reinterpret_cast<const f32x4 *>(&so[ot + RT * x][lr][d]);
             if (!alone) {
                 *reinterpret_cast<f32x4 *>(k.po + part * D + d) = y;
             } else {
@@ -963,14 +1088,15 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
     }
 }
 
-template <typename T, int D, int RW>
+template <typename T, int D, int RW, int RT>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
+    constexpr int kRows = RW * RT;
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
-    const WsMap w = ws_map(a.B, a.n, a.G, a.Hkv, D, RW, cap, a.scores != nullptr);
+    const WsMap w = ws_map(a.B, a.n, a.G, a.Hkv, D, kRows, cap, a.scores != nullptr);
     char *ws = static_cast<char *>(a.ws);
     KArgs k{};
     k.a = a;
-    k.plan = make_plan(a.B, a.n, a.G, a.Hkv, RW, cap);
+    k.plan = make_plan(a.B, a.n, a.G, a.Hkv, kRows, cap);
     k.sched = reinterpret_cast<int2 *>(ws + w.sched);
     k.ml = reinterpret_cast<float2 *>(ws + w.ml);
     k.po = reinterpret_cast<float *>(ws + w.o);
@@ -989,8 +1115,8 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     }
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
-    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, true><<<grid, kThreads, 0, s>>>(k);
-    else                        attn_kernel<T, D, RW, false><<<grid, kThreads, 0, s>>>(k);
+    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, RT, true><<<grid, kThreads, 0, s>>>(k);
+    else                        attn_kernel<T, D, RW, RT, false><<<grid, kThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // about 4,096 workgroups join, and at most one per row: sequences in one
@@ -1002,16 +1128,20 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     long long score_blocks = a.scores ? (long long)a.B * a.Hkv * ((k.cap32 + 1023) / 1024) : 0;
     if (score_blocks > (1 << 20)) score_blocks = 1 << 20;
     if (joins + score_blocks == 0) return hipSuccess;
-    join_kernel<T, D, RW><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(k, join_wgs, joins,
-                                                                              score_blocks);
+    join_kernel<T, D, kRows><<<(unsigned)(joins + score_blocks), kThreads, 0, s>>>(
+        k, join_wgs, joins, score_blocks);
     return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
-    if (!bf16_io) return launch<float, D, 16>(a, s);
-    return block_rows(true, (long long)a.n * a.G) == 32 ? launch<bf16, D, 32>(a, s)
-                                                        : launch<bf16, D, 16>(a, s);
+    if (!bf16_io) return launch<float, D, 16, 1>(a, s);
+    const long long cap = (long long)a.map.max_pages << a.map.page_shift;
+    switch (block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window)) {
+    case 16: return launch<bf16, D, 16, 1>(a, s);
+    case 32: return launch<bf16, D, 32, 1>(a, s);
+    default: return launch<bf16, D, 32, 2>(a, s);
+    }
 }
 
 }  // namespace
@@ -1019,10 +1149,14 @@ hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
                            bool with_scores) {
     const int G = Hq / Hkv;
-    // one size for both dtypes
-    const size_t x = ws_map(B, n, G, Hkv, D, block_rows(true, (long long)n * G), capacity, with_scores).total;
-    const size_t y = ws_map(B, n, G, Hkv, D, block_rows(false, (long long)n * G), capacity, with_scores).total;
-    return x > y ? x : y;
+    // one size for every dtype and window: the largest over the blocks there can be
+    const long long rows = (long long)n * G;
+    size_t most = 0;
+    for (int rw = 16; rw <= 64 && (rw == 16 || rows > rw / 2); rw *= 2) {
+        const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
+        if (x > most) most = x;
+    }
+    return most;
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {

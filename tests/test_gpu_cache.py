@@ -138,6 +138,44 @@ def test_attend(dt, D, page, Hkv, G, n, window):
     assert torch.equal(o2, o3) and same(s2, s3)
 
 
+@pytest.mark.parametrize("D,page,n,G,window", [
+    (128, 16, 16, 4, 0), (128, 64, 9, 4, 0), (64, 32, 33, 2, 0), (128, 32, 70, 1, 0),
+    (64, 16, 20, 5, 0), (128, 16, 40, 2, 75), (64, 256, 13, 3, 20)])
+def test_attend_many_rows_long_table(D, page, n, G, window):
+    """Over 32 rows a head and a table for many tokens: two tiles of rows that
+    share the tokens."""
+    announce("attend rows D=%d page=%d n=%d G=%d window=%d" % (D, page, n, G, window))
+    lens = [1, 0, 33, 700, 65, 1500]
+    kc, vc, sc, table = make_cache(lens, 2, D, page, torch.bfloat16, seed=D + n,
+                                   extra=(48 << 20) // (len(lens) * 2 * D * page))
+    q = queries(len(lens), n, 2 * G, D, torch.bfloat16, seed=n)
+    o = check_attend(q, kc, vc, table, lens, D ** -0.5, window, what="plain")
+    table[3, 2] = -1
+    check_attend(q, kc, vc, table, lens, D ** -0.5, window, sc, what="absent, scores")
+    # infinities and NaN where a row does not attend
+    clean = vc.clone()
+    for b, j, x in ((5, 1499, NAN), (5, 1490, float("inf")), (4, 64, -float("inf")), (2, 20, NAN)):
+        p, s = ref.place(table, kc.shape[0], page, b, j)
+        vc[p, :, s, 3] = x
+        clean[p, :, s, 3] = 0
+    got = gdr.attention_decode(gpu(q), gpu(kc), gpu(vc), i32(table), i32(lens), window=window)
+    want = gdr.attention_decode(gpu(q), gpu(kc), gpu(clean), i32(table), i32(lens), window=window)
+    got, want = got.float().cpu().numpy(), want.float().cpu().numpy()
+    for b, L in enumerate(lens):
+        for t in range(n):
+            p = L - n + t
+            seen = [x for bb, j, x in ((5, 1499, NAN), (5, 1490, np.inf), (4, 64, -np.inf), (2, 20, NAN))
+                    if bb == b and j <= p and (not window or j > p - window)]
+            total = sum(seen) if seen else 0.0
+            here, there = got[b, t, :, 3], want[b, t, :, 3]
+            if not seen:
+                assert np.array_equal(here, there), (b, t)
+            else:
+                assert (np.isnan(here).all() if np.isnan(total) else (here == total).all()), (b, t)
+    o2 = np.delete(got, 3, axis=-1)
+    assert np.array_equal(o2, np.delete(want, 3, axis=-1)) and o is not None
+
+
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("lens,n,G,window", [
     ([4097], 1, 4, 0), ([9000, 40], 1, 8, 0), ([2500, 1, 777], 3, 2, 0), ([6000], 2, 4, 2100),
