@@ -88,11 +88,12 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 // of 32 would need twice the registers there are.
 //   Over 32 rows with much to read, 64: two tiles of rows share the tokens
 // through LDS (16 new tokens, 4 heads of 4 rows each: 16 contexts of 2,000
-// tokens 27 us against 40 in blocks of 32, 2 of 16,000 28 against 37).  With
-// little to read the two blocks side by side are done sooner (16 contexts of
-// 1,000: 21 us against 26; one of 300: 11 against 17).  The lengths are on the
-// device, so what the table and the window let a sequence attend to decides.
-constexpr long long kShareBytes = 64LL << 20;
+// tokens 25 us against 39 in blocks of 32, of 1,500 24 against 31, 2 of 16,000
+// 25 against 37).  With little to read the two blocks side by side are done
+// sooner (16 contexts of 1,000: 21 us against 23; one of 300: 11 against 17).
+// The lengths are on the device, so what the table and the window let a
+// sequence attend to decides.
+constexpr long long kShareBytes = 40LL << 20;
 int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long long capacity,
                int window) {
     if (!bf16_io || rows <= 16) return 16;
@@ -292,14 +293,6 @@ struct Src { size_t at; unsigned bytes; };
 //     acc[c][i] is channel dim(c, m(i, g)) of query row r.
 template <typename T, int D, int RW> struct Tile;
 
-// Where chunk c (16 bytes) of a row lies in a tile in LDS: row by row, the
-// chunks exchanged by the row's number, so that the rows of a K operand are in
-// different banks.
-template <int ROW_BYTES>
-__device__ inline int chunk_at(int row, int c) {
-    const int swap = ROW_BYTES >= 256 ? row & 15 : (row >> 1) & 7;
-    return row * ROW_BYTES + ((c ^ swap) << 4);
-}
 // two keys' values of one channel pair -> channel c of both
 __device__ inline unsigned pick2(unsigned k0, unsigned k1, int c) {
     return __builtin_amdgcn_perm(k1, k0, c & 1 ? 0x07060302u : 0x05040100u);
@@ -324,6 +317,9 @@ template <int D, int RW> struct Tile<bf16, D, RW> {
     static constexpr int kVals = kTile / kGroups;  // logits of a lane
     static constexpr int PER = D / RW;             // channels of a lane's V rows, blocks of acc
     static constexpr int kRowBytes = D * 2;
+    // a row in LDS: 16 bytes more, so that the rows of a K operand start in
+    // different banks
+    static constexpr int kPitch = kRowBytes + 16;
     static constexpr int kSteps = D / (8 * kGroups);     // MFMAs of a block of keys
     static constexpr int kKeyBlocks = kTile / RW;        // S^T tiles: 2 (RW = 16) or 1
     typedef std::conditional_t<RW == 16, f32x4, f32x16> Acc;
@@ -410,13 +406,13 @@ template <int D, int RW> struct Tile<bf16, D, RW> {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             k.f[0][i] = *reinterpret_cast<const bf16x8 *>(
-                t + chunk_at<kRowBytes>(lane % RW, kGroups * i + lane / RW));
+                t + lane % RW * kPitch + 16 * (kGroups * i + lane / RW));
     }
     __device__ static inline void lds_v(V &v, const char *t, int lane) {
         const int g = lane / RW, at = lane % RW * PER * 2;
 #pragma unroll
         for (int i = 0; i < kVals; ++i) {
-            const char *p = t + chunk_at<kRowBytes>(key(i, g), at >> 4) + (at & 15);
+            const char *p = t + key(i, g) * kPitch + at;
 #pragma unroll
             for (int j = 0; j < PER / 2; ++j) v.w[i][j] = reinterpret_cast<const unsigned *>(p)[j];
         }
@@ -591,15 +587,18 @@ template <int D> struct Tile<float, D, 16> {
 // in each; three, by spilling, measured 141 us where two take 120 (64 contexts).
 //   RT = 2: two waves read each tile, which all threads bring into LDS
 // together, a stage (a tile per share) at a time: one stage is worked on while
-// the next comes into registers, to be written beside it.  At D = 128 the 34
-// registers that the path for infinities and NaN in V costs are spilled: 62 us
-// for 16 contexts of 1,000 to 6,000, 55 without that path, 74 with RT = 1.
+// the next comes into registers, to be written beside it.  (16 contexts of
+// 1,000 to 6,000, 64 rows a head: 53 us, 74 with RT = 1.  Rows in LDS are
+// padded rather than exchanged: with a 16-byte chunk's place depending on its
+// row by an exclusive or, the addresses alone took so many registers that 34
+// others were spilled, 62 us.)
 template <typename T, int D, int RW, int RT, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D, RW>;
     constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = TL::kTile, kVals = TL::kVals;
     constexpr int kPad = D + 4, kShares = kWaves / RT, kRows = RW * RT;
-    constexpr int kTileBytes = kTile * TL::kRowBytes, kStage = kShares * 2 * kTileBytes;
+    constexpr int kPitch = TL::kRowBytes + 16, kTileBytes = kTile * kPitch;
+    constexpr int kStage = kShares * 2 * kTileBytes;
     constexpr int kOBytes = kWaves * RW * kPad * (int)sizeof(float);
     __shared__ float sm[kWaves][RW], sl[kWaves][RW];
     // the two stages, and at the end every wave's o
@@ -805,8 +804,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
             }
         }
     } else {
-        constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTileBytes / 16 / kThreads;
-        static_assert(kUnits * kThreads * 16 == kTileBytes && 64 / kChunks <= 16,
+        constexpr int kChunks = TL::kRowBytes / 16, kUnits = kTile * kChunks / kThreads;
+        static_assert(kUnits * kThreads == kTile * kChunks && 64 / kChunks <= 16,
                       "threads cover a tile, a wave's rows lie in one block of 16");
         // 16 bytes of K and of V per thread, share and unit, and which blocks
         // of this wave's own tile are there
@@ -846,8 +845,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
                 for (int u = 0; u < kUnits; ++u) {
                     const int unit = tid + kThreads * u;
-                    char *p = to + 2 * x * kTileBytes +
-                              chunk_at<TL::kRowBytes>(unit / kChunks, unit % kChunks);
+                    char *p = to + 2 * x * kTileBytes + unit / kChunks * kPitch +
+                              unit % kChunks * 16;
                     *reinterpret_cast<u32x4 *>(p) = kv[x][u][0];
                     *reinterpret_cast<u32x4 *>(p + kTileBytes) = kv[x][u][1];
                 }

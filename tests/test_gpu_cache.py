@@ -176,6 +176,25 @@ def test_attend_many_rows_long_table(D, page, n, G, window):
     assert np.array_equal(o2, np.delete(want, 3, axis=-1)) and o is not None
 
 
+@pytest.mark.parametrize("D,page,n,window", [(128, 64, 10, 900), (64, 16, 17, 1800)])
+def test_attend_many_rows_wide_window(D, page, n, window):
+    """The same with a window that cuts into the longer sequences and is wide
+    enough for rows to share tokens."""
+    announce("attend rows D=%d page=%d n=%d window=%d" % (D, page, n, window))
+    lens = [window + 500, 30, 0, window + 5, window - 3, window + n] + [33] * 18
+    kc, vc, sc, table = make_cache(lens, 4, D, page, torch.bfloat16, seed=D, extra=2)
+    q = queries(len(lens), n, 16, D, torch.bfloat16, seed=n)
+    check_attend(q, kc, vc, table, lens, D ** -0.5, window, what="plain")
+    check_attend(q, kc, vc, table, lens, D ** -0.5, window, sc, what="scores")
+    # an infinity that the first rows alone attend to
+    b, j = 0, lens[0] - n - window + 1
+    p, s = ref.place(table, kc.shape[0], page, b, j)
+    vc[p, :, s, 5] = float("inf")
+    got = gdr.attention_decode(gpu(q), gpu(kc), gpu(vc), i32(table), i32(lens), window=window).cpu()
+    assert (got[b, 0, :, 5] == float("inf")).all()
+    assert torch.isfinite(got[b, 1:]).all() and torch.isfinite(got[1:]).all()
+
+
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("lens,n,G,window", [
     ([4097], 1, 4, 0), ([9000, 40], 1, 8, 0), ([2500, 1, 777], 3, 2, 0), ([6000], 2, 4, 2100),
