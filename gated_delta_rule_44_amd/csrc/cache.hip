@@ -79,10 +79,10 @@ __device__ inline unsigned key_of(float x) {
 }
 
 // Which tokens a (sequence, head) keeps, bound by the latency of its passes:
-// 9 us for 600 to 1,000 tokens (8 pairs), 10 us for 1,500 to 4,096 (128 pairs).
-// One workgroup per pair, which holds
-// the keys of up to kHeld tokens, read once: four adjacent tokens per thread
-// and round, the first eight rounds in registers, the others in LDS.  The m-th largest key of the tokens between
+// 8 us for 600 to 1,000 tokens (8 pairs), 9 us for 1,500 to 4,096 (128 pairs).
+// One workgroup per pair, which holds the keys of up to kHeld tokens, read
+// once: four adjacent tokens per thread and round, the first eight rounds in
+// registers, the others in LDS.  The m-th largest key of the tokens between
 // sink and recent is found digit by digit: 8 bits a step, from the top, by a
 // histogram of the keys that share the digits found so far, which ends when
 // a digit's keys are all wanted.  The kept tokens' places then follow from
@@ -98,6 +98,17 @@ constexpr int kCopies = 16, kCopyStride = 257;
 
 typedef unsigned keys4 __attribute__((ext_vector_type(4)));
 
+// Sum of x over this lane and those below it: shifts by 1, 2, 4 and 8 within
+// each 16 lanes, then the sums of 16 and of 32 lanes handed to those above.
+__device__ inline int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
 // The digit of the `want`-th largest key: thread t < 256 brings how many keys
 // have digit 255 - t.
 struct Digit {
@@ -108,11 +119,7 @@ __device__ inline Digit find_digit(int count, int want) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     int incl = count;                              // keys with this digit or a larger one
     if (tid < 256) {
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int y = __shfl_up(incl, m);
-            if (lane >= m) incl += y;
-        }
+        incl = wave_scan(count);
         if (lane == 63) waves[w] = incl;
     }
     __syncthreads();
@@ -192,6 +199,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         }
     };
     const bool once = len <= kHeld;
+    for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
     load_held(0);
 
     // (Tokens outside lo .. hi have key 0 as well: they add to the count of
@@ -202,7 +210,6 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
     if (none) prefix = 0xFFFFFFFFu;                // above every key
     bool ties = false;                             // more keys equal the threshold than wanted
     for (int shift = 24; shift >= 0 && !none; shift -= 8) {
-        for (int i = tid; i < kCopies * kCopyStride; i += kSelThreads) hist[i] = 0;
         __syncthreads();
         int *mine = hist + (lane & (kCopies - 1)) * kCopyStride;
         const unsigned span = digit_span(shift);
@@ -221,7 +228,10 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         int count = 0;
         if (tid < 256)
 #pragma unroll
-            for (int c = 0; c < kCopies; ++c) count += hist[c * kCopyStride + 255 - tid];
+            for (int c = 0; c < kCopies; ++c) {        // cleared for the next digit
+                count += hist[c * kCopyStride + 255 - tid];
+                hist[c * kCopyStride + 255 - tid] = 0;
+            }
         const Digit f = find_digit(count, want);
         prefix |= (unsigned)f.digit << shift;
         want = f.want;                             // wanted among the keys with this prefix
@@ -268,12 +278,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
         int2 c{0, 0}, t{0, 0};
         if (tid < 256) {
             if (base + (tid / kSelWaves) * kPerRound < len) c = counts[tid / kSelWaves][tid % kSelWaves];
-            t = c;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const int x = __shfl_up(t.x, m), y = __shfl_up(t.y, m);
-                if (lane >= m) { t.x += x; t.y += y; }
-            }
+            t = int2{wave_scan(c.x), wave_scan(c.y)};
             if (lane == 63) wave_counts[w] = t;
         }
         __syncthreads();
@@ -314,7 +319,7 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
 // last digit from all chunks' histograms (each writes its own), adds up which of
 // its keys that puts above the threshold, and makes its histogram of the next
 // digit; the last launch places the chunk's kept tokens behind those of the
-// chunks before it.  (65,001 tokens, 8 heads: 53 us by one workgroup, 33 us so.)
+// chunks before it.  (65,001 tokens, 8 heads: 53 us by one workgroup, 29 us so.)
 constexpr int kSpreadPairs = 64;       // at most so many pairs ...
 constexpr int kSpreadTokens = 8192;    // ... and tables longer than this
 constexpr int kSpreadChunks = 64;
@@ -342,7 +347,10 @@ SpreadLayout spread_layout(int pairs, long long capacity) {
 }
 
 __global__ __launch_bounds__(kSelThreads) void spread_kernel(EvictArgs a, Spread s, int level) {
-    const int pairs = a.B * a.Hkv, pair = blockIdx.x / s.chunks, me = blockIdx.x % s.chunks;
+    // a pair's chunks stay on one XCD when the pairs are a multiple of eight
+    // (workgroups go to the eight in turn), and with them their histograms in
+    // its L2: the whole call 61 -> 57 us
+    const int pairs = a.B * a.Hkv, pair = blockIdx.x % pairs, me = blockIdx.x / pairs;
     const int b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int len = cached_len(a.seq_lens, b, a.map);
@@ -545,8 +553,9 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(EvictArgs a, int lpr_shi
 constexpr int kCloseRows = 4;
 
 // The same in place: a workgroup has a column of the rows of one (sequence,
-// head), of K (even blockIdx.y) or V, 16 << slice_shift bytes wide, and goes through the rows in order, a
-// tile of them read, then written.  kept[i] >= i and kept ascends, so that a
+// head), of K (even blockIdx.y) or V, 16 << slice_shift bytes wide, and goes
+// through the rows in order, a tile of them read, then written.  kept[i] >= i
+// and kept ascends, so that a
 // tile's writes lie at or below its own reads and below all later ones, and
 // the next tile can be read before this one is written.  Columns are 64 bytes
 // wide, or 16 where the pairs are too few to fill the card (16,384 tokens kept
