@@ -140,7 +140,7 @@ def test_attend(dt, D, page, Hkv, G, n, window):
 
 @pytest.mark.parametrize("D,page,n,G,window", [
     (128, 16, 16, 4, 0), (128, 64, 9, 4, 0), (64, 32, 33, 2, 0), (128, 32, 70, 1, 0),
-    (64, 16, 20, 5, 0), (128, 16, 40, 2, 75), (64, 256, 13, 3, 20)])
+    (64, 16, 20, 5, 0), (128, 16, 40, 2, 75), (64, 256, 13, 3, 20), (128, 64, 300, 4, 0)])
 def test_attend_many_rows_long_table(D, page, n, G, window):
     """Over 32 rows a head and a table for many tokens: two tiles of rows that
     share the tokens."""
