@@ -144,11 +144,8 @@ __device__ inline int lanes_below(unsigned long long x) {
                                           __builtin_amdgcn_mbcnt_lo((unsigned)x, 0));
 }
 
-__global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv, tid = threadIdx.x;
-    const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int len = cached_len(a.seq_lens, b, a.map);
-    int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
+__device__ inline void select_pair(const EvictArgs &a, int b, int h, int len, int32_t *kept) {
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (len <= a.budget) {
         for (int i = tid; i < a.budget; i += kSelThreads) kept[i] = i < len ? i : -1;
         return;
@@ -310,6 +307,69 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
                 ne += eq[e];
             }
         }
+    }
+}
+
+// The places of row i of the new order and of the row it comes from, as rows
+// of the caches; false where it is not moved.
+__device__ inline bool row_move(const EvictArgs &a, int b, int h, int i, int j, size_t &src,
+                                size_t &dst) {
+    const int from = page_of(a.map, b, j), to = page_of(a.to, b, i);
+    src = cache_row(a.map, a.Hkv, from, h, slot_of(a.map, j));
+    dst = cache_row(a.to, a.Hkv, to, h, slot_of(a.to, i));
+    return from >= 0 && to >= 0;
+}
+constexpr int kMoveRows = 4;       // rows of a thread, their loads in flight together
+
+// Rows base .. of a pair's first m, 16 bytes of K and of V per thread and row,
+// kMoveRows of THREADS / (row's threads) rows, every row on its own.
+template <int THREADS>
+__device__ inline void move_rows(const EvictArgs &a, int b, int h, int base, int m, int lpr_shift,
+                                 const int32_t *kept) {
+    const int tid = threadIdx.x, c = tid & ((1 << lpr_shift) - 1), rows = THREADS >> lpr_shift;
+    u32x4 *kc = static_cast<u32x4 *>(a.k_cache), *vc = static_cast<u32x4 *>(a.v_cache);
+    size_t src[kMoveRows], dst[kMoveRows];
+    bool move[kMoveRows];
+    u32x4 x[kMoveRows], y[kMoveRows];
+    float sc[kMoveRows];
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+        const int i = base + rows * u + (tid >> lpr_shift);
+        move[u] = i < m && row_move(a, b, h, i, kept[i < m ? i : 0], src[u], dst[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u)
+        if (move[u]) {
+            x[u] = pass_load(kc + (src[u] << lpr_shift) + c);
+            y[u] = pass_load(vc + (src[u] << lpr_shift) + c);
+            if (c == 0) sc[u] = a.scores[src[u]];
+        }
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u)
+        if (move[u]) {
+            pass_store(kc + (dst[u] << lpr_shift) + c, x[u]);
+            pass_store(vc + (dst[u] << lpr_shift) + c, y[u]);
+            if (c == 0) a.scores[dst[u]] = sc[u];
+        }
+}
+
+// MOVE: the kept rows go into the new pages here as well, which saves a launch
+// where a pair's rows are few: 128 KiB of K and V each, 8 pairs 12.5 -> 11.5 us,
+// 256 pairs 21.3 -> 19.9; 32 KiB, 1,024 pairs 41 -> 38.  With more to move one
+// workgroup per pair is too few (256 KiB, 8 pairs: 12.2 -> 14.9 us).
+constexpr int kMoveBytes = 128 << 10;
+template <bool MOVE>
+__global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a, int lpr_shift) {
+    const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+    const int len = cached_len(a.seq_lens, b, a.map);
+    int32_t *kept = a.kept + (size_t)blockIdx.x * a.budget;
+    select_pair(a, b, h, len, kept);
+    if constexpr (MOVE) {
+        const int m = len < a.budget ? len : a.budget;
+        if (h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
+        __syncthreads();                               // all of kept is there
+        for (int base = 0; base < m; base += (kSelThreads >> lpr_shift) * kMoveRows)
+            move_rows<kSelThreads>(a, b, h, base, m, lpr_shift, kept);
     }
 }
 
@@ -501,53 +561,17 @@ __global__ __launch_bounds__(kSelThreads) void spread_kernel(EvictArgs a, Spread
     }
 }
 
-// The places of row i of the new order and of the row it comes from, as rows
-// of the caches; false where it is not moved.
-__device__ inline bool row_move(const EvictArgs &a, int b, int h, int i, int j, size_t &src,
-                                size_t &dst) {
-    const int from = page_of(a.map, b, j), to = page_of(a.to, b, i);
-    src = cache_row(a.map, a.Hkv, from, h, slot_of(a.map, j));
-    dst = cache_row(a.to, a.Hkv, to, h, slot_of(a.to, i));
-    return from >= 0 && to >= 0;
-}
-constexpr int kMoveRows = 4;       // rows of a thread, their loads in flight together
-
-// Rows kept[b, h, i] -> i into other pages: 16 bytes of K and of V per
-// thread and row, every row on its own.  A copy, bound by bytes: 16 contexts
-// trimmed to 1,800 tokens (8 heads of 128, bf16), 233 MB in 48 us, 4.8 TB/s.
+// Rows kept[b, h, i] -> i into other pages.  A copy, bound by bytes: 16
+// contexts trimmed to 1,800 tokens (8 heads of 128, bf16), 233 MB in 48 us, 4.8
+// TB/s.
 __global__ __launch_bounds__(256) void copy_rows_kernel(EvictArgs a, int lpr_shift) {
-    const int pair = blockIdx.x, b = pair / a.Hkv, h = pair % a.Hkv, tid = threadIdx.x;
+    const int pair = blockIdx.x, b = pair / a.Hkv, h = pair % a.Hkv;
     const int len = cached_len(a.seq_lens, b, a.map);
     const int m = len < a.budget ? len : a.budget;
-    if (blockIdx.y == 0 && h == 0 && tid == 0) a.new_lens[b] = m;
-    const int c = tid & ((1 << lpr_shift) - 1), rows = 256 >> lpr_shift;
-    const int32_t *kept = a.kept + (size_t)pair * a.budget;
-    u32x4 *kc = static_cast<u32x4 *>(a.k_cache), *vc = static_cast<u32x4 *>(a.v_cache);
-    for (int base = blockIdx.y * rows * kMoveRows; base < m; base += gridDim.y * rows * kMoveRows) {
-        size_t src[kMoveRows], dst[kMoveRows];
-        bool move[kMoveRows];
-        u32x4 x[kMoveRows], y[kMoveRows];
-        float sc[kMoveRows];
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            const int i = base + rows * u + (tid >> lpr_shift);
-            move[u] = i < m && row_move(a, b, h, i, kept[i < m ? i : 0], src[u], dst[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
-            if (move[u]) {
-                x[u] = pass_load(kc + (src[u] << lpr_shift) + c);
-                y[u] = pass_load(vc + (src[u] << lpr_shift) + c);
-                if (c == 0) sc[u] = a.scores[src[u]];
-            }
-#pragma unroll
-        for (int u = 0; u < kMoveRows; ++u)
-            if (move[u]) {
-                pass_store(kc + (dst[u] << lpr_shift) + c, x[u]);
-                pass_store(vc + (dst[u] << lpr_shift) + c, y[u]);
-                if (c == 0) a.scores[dst[u]] = sc[u];
-            }
-    }
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
+    const int tile = (256 >> lpr_shift) * kMoveRows;
+    for (int base = blockIdx.y * tile; base < m; base += gridDim.y * tile)
+        move_rows<256>(a, b, h, base, m, lpr_shift, a.kept + (size_t)pair * a.budget);
 }
 
 constexpr int kCloseRows = 4;
@@ -641,9 +665,14 @@ hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s) 
             if (e != hipSuccess) return e;
         }
     } else {
-        select_kernel<<<pairs, kSelThreads, 0, s>>>(a);
+        // (new lengths written over the old ones would be read as such by the
+        // other heads' workgroups)
+        const bool apart = a.new_lens + a.B <= a.seq_lens || a.seq_lens + a.B <= a.new_lens;
+        const bool move = !a.in_place && apart && (long long)a.budget * row_bytes * 2 <= kMoveBytes;
+        if (move) select_kernel<true><<<pairs, kSelThreads, 0, s>>>(a, sh);
+        else      select_kernel<false><<<pairs, kSelThreads, 0, s>>>(a, sh);
         const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if (move || e != hipSuccess) return e;
     }
     if (a.in_place) {
         const int slice = pairs * (2 << (sh - 2)) >= 256 ? 2 : 0;

@@ -673,6 +673,30 @@ def test_evict_lens_in_place():
         assert same(a, b)
 
 
+@pytest.mark.parametrize("budget", [100, 255, 256, 257, 700])
+@pytest.mark.parametrize("alias", [False, True])
+def test_evict_into_new_pages(budget, alias):
+    """Rows moved by the selection's own workgroups or by a launch of their
+    own; the new lengths may be written over the old ones either way."""
+    announce("evict new pages budget=%d alias=%s" % (budget, alias))
+    lens = [900, 40, 0, 701, 256] + [300] * 40
+    need = -(-budget // 32)
+    kc, vc, sc, table = make_cache(lens, 8, 128, 32, torch.bfloat16, seed=budget,
+                                   spare=len(lens) * need)
+    free = np.setdiff1d(np.arange(kc.shape[0]), table[table >= 0])
+    new_table = free[:len(lens) * need].reshape(len(lens), need).astype(np.int32)
+    new_table[3, 1] = -1
+    dk, dv, ds, dl = gpu(kc), gpu(vc), gpu(sc), i32(lens)
+    nl, kept = gdr.cache_evict(dk, dv, ds, i32(table), dl, budget, 20, 3,
+                               new_page_table=i32(new_table), new_lens=dl if alias else None)
+    sync()
+    want = ref.evict(kc, vc, sc, table, lens, budget, 20, 3, new_table)
+    assert np.array_equal(nl.cpu().numpy(), want[3])
+    assert np.array_equal(kept.cpu().numpy(), want[4])
+    for a, b in zip((dk, dv, ds), want):
+        assert same(a, b)
+
+
 # -------------------------------------------------------- as a serving loop runs
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 def test_serving_run(dt):
