@@ -104,16 +104,18 @@ int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long 
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
 // them, every slot's {sequence, its first slot, its slots, tokens of one};
 // (m, l) of every slot, unit and row; o of the same, unnormalised; with
-// scores, the products q.k of every row and token [B, Hkv, nG, cap].
+// scores, the products q.k of every row and token [B, Hkv, nG, cap].  Of a
+// table without pages, nothing: there is one launch, which writes none of it.
 struct WsMap {
     size_t sched, slots, ml, o, logits, total;
 };
 WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bool with_scores) {
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
+    WsMap w{};
+    if (capacity == 0) return w;
     const Plan p = make_plan(B, n, G, Hkv, rw, capacity);
     const size_t rows = (size_t)p.max_slots * p.units * rw;
     const bool parts = p.max_slots > B;
-    WsMap w{};
     w.sched = 0;
     w.slots = r256((size_t)B * 2 * sizeof(int));
     w.ml = w.slots + (parts && B > kScan ? r256((size_t)p.max_slots * sizeof(int4)) : 0);
@@ -127,7 +129,7 @@ WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bo
 struct KArgs {
     AttnArgs a;
     Plan plan;
-    int2 *sched;
+    int2 *sched;          // nullptr: a table without pages
     int4 *slots;          // nullptr: found by each workgroup
     float2 *ml;
     float *po;
@@ -618,7 +620,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     if (b < 0) return;
     const int len = uniform(cached_len(a.seq_lens, b, a.map));
     const Span seq = seq_span(len, a.n, a.window);
-    if (h == 0 && rb == 0 && slot == sl_.first && tid == 0) k.sched[b] = int2{sl_.first, sl_.count};
+    if (k.sched && h == 0 && rb == 0 && slot == sl_.first && tid == 0)
+        k.sched[b] = int2{sl_.first, sl_.count};
 
     // this lane's query row and what it attends to
     const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + RW * rt + r;
@@ -1096,10 +1099,10 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
     k.plan = make_plan(a.B, a.n, a.G, a.Hkv, kRows, cap);
-    k.sched = reinterpret_cast<int2 *>(ws + w.sched);
+    k.sched = cap > 0 ? reinterpret_cast<int2 *>(ws + w.sched) : nullptr;
     k.ml = reinterpret_cast<float2 *>(ws + w.ml);
     k.po = reinterpret_cast<float *>(ws + w.o);
-    k.logits = a.scores ? reinterpret_cast<float *>(ws + w.logits) : nullptr;
+    k.logits = a.scores && cap > 0 ? reinterpret_cast<float *>(ws + w.logits) : nullptr;
     k.cap32 = (cap + 31) / 32 * 32;
     // (a scale of zero: the smallest number, whose products vanish, as
     // 0 times a masked token's -inf would be NaN; nor is it infinite)

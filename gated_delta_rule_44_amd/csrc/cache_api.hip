@@ -137,7 +137,7 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
 
 size_t gdr_attention_workspace_bytes(int B, int n_tok, int Hq, int Hkv, int D, int max_pages,
                                      int page_size, int with_scores) {
-    if (B <= 0 || n_tok <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_pages <= 0 ||
+    if (B <= 0 || n_tok <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_pages < 0 ||
         page_shift_of(page_size) < 0 || (long long)max_pages * page_size >= (1LL << 30) ||
         reaches(B, n_tok, Hq, kMaxQueryRows))
         return 0;

@@ -99,8 +99,9 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
  *                may be shared).
  *   page_table_host  host copy of page_table, optional: validated first
  *                (values in -1..num_pages-1; with scores, no page twice)
- *   workspace    device buffer of gdr_attention_workspace_bytes bytes,
- *                16-byte aligned; needs no clearing; not to be shared with a
+ *   workspace    device buffer of gdr_attention_workspace_bytes bytes (0 for a
+ *                table without pages: NULL is accepted then), 16-byte
+ *                aligned; needs no clearing; not to be shared with a
  *                concurrent call
  *
  * Numerics: fp32 accumulation, logits, softmax statistics and weights; with
