@@ -105,8 +105,8 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
  *                concurrent call
  *
  * Numerics: fp32 accumulation, logits, softmax statistics and weights; with
- * bf16 inputs the weights are rounded to bf16 as operands of the product
- * with V (scores take them unrounded).
+ * bf16 inputs a weight enters the product with V as the sum of two bf16
+ * numbers, off by at most 2^-15 of it (scores take it unrounded).
  */
 size_t gdr_attention_workspace_bytes(int B, int n_tok, int Hq, int Hkv, int D, int max_pages,
                                      int page_size, int with_scores);

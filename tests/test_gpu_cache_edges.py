@@ -63,3 +63,97 @@ def test_evict_and_append_no_pages(new):
     torch.cuda.synchronize(DEV)
     assert bool((nl == 0).all()) and bool((kept == -1).all())
     assert bool(torch.isnan(kc).all()) and bool(torch.isnan(sc).all())
+
+
+# ------------------------------------------------------ precision of the weights
+def exact_inputs(lens, Hkv, G, n, D, page, wide, seed):
+    """q and k on a grid (multiples of 1/2 up to 2, of 1/4 up to 1/2) whose dot
+    products fp32 holds exactly, v random but for a constant taken off per
+    sequence, head and channel, such that the last row of each head's first
+    query head sums its values to nearly nothing.  Returns the call's tensors
+    and, per sequence, the rows' weights [Hkv, n, G, L] and v [Hkv, L, D] in
+    64 bits."""
+    rng = np.random.default_rng(seed)
+    B, need = len(lens), [-(-l // page) for l in lens]
+    P, M = sum(need) + 1, max(need) + wide
+    q = rng.integers(-4, 5, (B, n, Hkv * G, D)) / 2
+    kc = np.full((P, Hkv, page, D), NAN, np.float32)
+    vc, table = kc.copy(), np.full((B, M), -1, np.int32)
+    pages, at, rows, scale = rng.permutation(P), 0, [], 1.0 / D ** 0.5
+    for b, L in enumerate(lens):
+        k = rng.integers(-2, 3, (Hkv, L, D)) / 4
+        v = rng.standard_normal((Hkv, L, D))
+        qb = q[b].reshape(n, Hkv, G, D).transpose(1, 0, 2, 3)
+        s = scale * np.einsum("hngd,hld->hngl", qb, k)
+        pos = L - n + np.arange(n)
+        s = np.where(np.arange(L) <= pos[:, None, None], s, -np.inf)
+        w = np.exp(s - s.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        v -= np.einsum("hl,hld->hd", w[:, -1, 0], v)[:, None]
+        v = torch.from_numpy(v).bfloat16().double().numpy()
+        table[b, :need[b]] = pages[at:at + need[b]]
+        at += need[b]
+        for i, p in enumerate(table[b, :need[b]]):
+            m = min(page, L - i * page)
+            kc[p, :, :m] = k[:, i * page:i * page + m]
+            vc[p, :, :m] = v[:, i * page:i * page + m]
+        rows.append((w, v, np.abs(s[np.isfinite(s)]).max()))
+    return (torch.from_numpy(q).bfloat16().to(DEV), torch.from_numpy(kc).bfloat16().to(DEV),
+            torch.from_numpy(vc).bfloat16().to(DEV), i32(table), i32(lens)), rows
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (64, 16)])
+@pytest.mark.parametrize("n,G,wide", [(1, 4, 0), (1, 1, 0), (5, 4, 0), (10, 4, 1)])
+def test_attend_weights_of_bf16_values(D, page, n, G, wide):
+    """Where the values of a row nearly cancel, o shows the weights' rounding.
+    With u = 2^-24 and N tokens, logits exact but for their scaling:
+      * a weight is off by e = 2 (8 u max |s| + 4 u) + (N + 16) u relative;
+      * as two bf16 numbers, the first cut (a rest below 2^-7) and the rest,
+        with 2^-23 added, rounded (2^-8 of it), by 2^-15 + 2^-22;
+      * the 2 N products' sum by (2 N + 16) u of sum w |v|;
+      * storing o adds its half step, 2^-8 |o|."""
+    announce("attend weights D=%d page=%d n=%d G=%d wide=%d" % (D, page, n, G, wide))
+    lens, Hkv, u = [200, 65, 16, 1500], 2, 2.0 ** -24
+    table_wide = (48 << 20) // (len(lens) * Hkv * D * 4 * page) if wide else 0
+    args, rows = exact_inputs(lens, Hkv, G, n, D, page, table_wide, seed=D + n + G)
+    o = gdr.attention_decode(*args).double().cpu().numpy()
+    worst = 0.0
+    for b, (L, (w, v, s)) in enumerate(zip(lens, rows)):
+        want = np.einsum("hngl,hld->hngd", w, v)
+        size = np.einsum("hngl,hld->hngd", w, np.abs(v))
+        rel = 2 * (8 * u * s + 4 * u) + (L + 16) * u + 2.0 ** -15 + 2.0 ** -22 + (2 * L + 16) * u
+        lim = (rel * size + 2.0 ** -8 * np.abs(want)) * (1 + 2.0 ** -6)
+        err = np.abs(o[b].reshape(n, Hkv, G, D).transpose(1, 0, 2, 3) - want)
+        worst = max(worst, (err / lim).max())
+    announce("  worst error / bound %.3f" % worst)
+    assert worst <= 1
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("n,G", [(1, 4), (5, 4), (10, 4)])
+def test_attend_infinite_values_of_attended_tokens(dt, bad, n, G):
+    """Every row attends to the tokens before the new ones: an infinite value of
+    one of them is the row's result in that channel, also where the token's
+    weight is a short binary number (the row's maximum, or all weights equal)."""
+    announce("attend infinite values %s %s n=%d G=%d" % (dt, bad, n, G))
+    B, Hkv, D, page, L = 2, 2, 64, 16, 150
+    M = (48 << 20) // (B * Hkv * D * 4 * page)         # blocks of 64 rows where there are over 32
+    g = torch.Generator(device=DEV).manual_seed(3)
+    kc, vc = (torch.randn((B * 10, Hkv, page, D), device=DEV, generator=g).to(DTYPES[dt])
+              for _ in range(2))
+    q = torch.randn((B, n, Hkv * G, D), device=DEV, generator=g).to(DTYPES[dt])
+    q[1] = 0                                           # all weights equal
+    table = torch.full((B, M), -1, device=DEV, dtype=torch.int32)
+    table[:, :10] = torch.arange(B * 10, device=DEV, dtype=torch.int32).view(B, 10)
+    lens = i32([L] * B)
+    clean = gdr.attention_decode(q, kc, vc, table, lens)
+    s = torch.einsum("rd,hjd->rhj", q[0].reshape(-1, D).float(),
+                     kc[:10].transpose(0, 1).reshape(Hkv, -1, D).float())
+    top = int(s[0, 0, :L - n].argmax())                # the first row's maximum of these
+    for b, j, c in ((0, top, 3), (0, 40, 5), (1, 0, 7), (1, L - n - 1, 11)):
+        vc[b * 10 + j // page, :, j % page, c] = bad
+        clean[b, :, :, c] = bad
+    o = gdr.attention_decode(q, kc, vc, table, lens)
+    torch.cuda.synchronize(DEV)
+    assert torch.equal(o, clean)
