@@ -20,8 +20,10 @@ from . import (GdrError, _BF16, _F32, _check, _dense, _host_i32, _load, _need,
 _Tensor, _INT32, _FLOAT32 = torch.Tensor, torch.int32, torch.float32
 _DTYPES = {torch.bfloat16: _BF16, torch.float32: _F32}
 # the current stream's handle, without a torch.cuda.Stream object around it
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (where this torch has no such function, by way of one)
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 # A decode step is microseconds of GPU work, so the checks cost as little as
