@@ -112,8 +112,10 @@ def cache_append(k, v, start, page_table, k_cache, v_cache, scores=None, cu_seql
     k, v [B,n,Hkv,D], or packed [T_tot,Hkv,D] with cu_seqlens int32 [B+1] on
     the GPU (rows behind the last sequence are left out; cu_seqlens_host, a
     host copy, makes the library validate it); start int32 [B] on the GPU.
-    Positions outside the table or on an absent page are left out.  scores,
-    when given, are set to 0 at every position written.
+    Positions outside the table or on an absent page are left out.  No two
+    tokens of a call may name the same place (its contents are unspecified
+    then): pages written belong to one sequence each.  scores, when given, are
+    set to 0 at every position written.
     """
     dev, dtype, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
     _gpu("k", k, dtype, dev)

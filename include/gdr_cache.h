@@ -61,7 +61,10 @@ extern "C" {
  *   scores       NULL, or the accumulated weights: set to 0 at every
  *                position written (a page may come from an earlier request)
  *
- * Two tokens of one call that name the same place leave one of the two there.
+ * The places of one call's tokens must differ: sequences may share pages that
+ * the call does not write, but a place that two tokens name (a page under two
+ * sequences, or twice in a table) is left with unspecified contents, K and V
+ * of different tokens or pieces of both among them.
  */
 gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, int Hkv, int D,
                             const void *k, const void *v, const int32_t *cu_seqlens,
