@@ -157,3 +157,103 @@ def test_attend_infinite_values_of_attended_tokens(dt, bad, n, G):
     o = gdr.attention_decode(q, kc, vc, table, lens)
     torch.cuda.synchronize(DEV)
     assert torch.equal(o, clean)
+
+
+# ------------------------------------- long slots, and more sequences than split
+def check_rows(o, q, kc, vc, table, lens, scale, which, what):
+    """o of the sequences `which` against 64 bits on the GPU.  With u = 2^-24, N
+    tokens, products of D terms, the bound of each row is that of fp32 logits,
+    weights and sums (a weight off by 2 e + (N + 16) u, e the largest logit's
+    error), of weights as two bf16 numbers (2^-15 + 2^-22, none in fp32), of the
+    sum over 2 N products, and of storing o (2^-8 or u)."""
+    B, n, Hq, D = q.shape
+    P, Hkv, page, _ = kc.shape
+    G, u = Hq // Hkv, 2.0 ** -24
+    bf16 = q.dtype == torch.bfloat16
+    worst = 0.0
+    for b in which:
+        L = lens[b]
+        if L == 0:
+            assert bool((o[b] == 0).all())
+            continue
+        j = torch.arange(L, device=DEV)
+        pg = table[b].long()[j // page]
+        j = j[(pg >= 0) & (pg < P)]
+        pg = pg[(pg >= 0) & (pg < P)]
+        k, v = (x[pg, :, j % page].transpose(0, 1).contiguous().double() for x in (kc, vc))
+        qb = q[b].double().view(n, Hkv, G, D).transpose(0, 1).reshape(Hkv, n * G, D)
+        s = scale * torch.matmul(qb, k.transpose(1, 2).contiguous())
+        pos = (L - n + torch.arange(n, device=DEV)).repeat_interleave(G)
+        seen = j[None, :] <= pos[:, None]
+        s = s.masked_fill(~seen[None], -float("inf"))
+        w = torch.nan_to_num(torch.softmax(s, -1))
+        want = torch.matmul(w, v)
+        size = torch.matmul(w, v.abs())
+        e = ((D + 2) * u * abs(scale) * torch.matmul(qb.abs(), k.abs().transpose(1, 2).contiguous()).amax(-1)
+             + 8 * u * s.masked_fill(~seen[None], 0).abs().amax(-1) + 4 * u)
+        N = len(j)
+        rel = 2 * e + (N + 16 + 2 * N + 16) * u + (2.0 ** -15 + 2.0 ** -22 if bf16 else 0)
+        lim = (rel[..., None] * size + (2.0 ** -8 if bf16 else u) * want.abs()) * (1 + 2.0 ** -6)
+        got = o[b].double().view(n, Hkv, G, D).transpose(0, 1).reshape(Hkv, n * G, D)
+        err = (got - want).abs()
+        bad = err > lim
+        assert not bool(bad.any()), "%s: sequence %d at %s" % (what, b, bad.nonzero()[:4].tolist())
+        worst = max(worst, (err / lim.clamp_min(1e-300)).max().item())
+    announce("  %s worst error / bound %.3f" % (what, worst))
+
+
+# (sequences of about a third of a slot's tokens, 32 heads, so that 12 slots of
+# them fill the card; a wave holds the page numbers of 64 of its tiles: 8,192
+# tokens of a slot, fp32 4,096, blocks of 64 rows 2,048)
+@pytest.mark.parametrize("dt,n,G,lens", [
+    ("bf16", 1, 4, [26000, 26100, 25900, 26000]),
+    ("bf16", 5, 4, [26000, 3, 51000, 26000]),
+    ("bf16", 10, 4, [7000, 20001, 0, 7000]),
+    ("fp32", 2, 3, [13000, 13100, 1, 26000])])
+@pytest.mark.parametrize("D,page", [(64, 64), (128, 16)])
+def test_attend_slots_past_the_pages_held(dt, n, G, lens, D, page):
+    announce("attend long slots %s n=%d G=%d D=%d page=%d" % (dt, n, G, D, page))
+    Hkv, P = 32, 200
+    g = torch.Generator(device=DEV).manual_seed(D + n)
+    kc, vc = (torch.randn((P, Hkv, page, D), device=DEV, generator=g).to(DTYPES[dt]) for _ in range(2))
+    q = (2 * torch.randn((len(lens), n, Hkv * G, D), device=DEV, generator=g)).to(DTYPES[dt])
+    # pages may be shared, a sequence's own ones too; some are absent
+    table = torch.randint(-1, P + 1, (len(lens), -(-max(lens) // page) + 1), device=DEV, generator=g,
+                          dtype=torch.int32)
+    o = gdr.attention_decode(q, kc, vc, table, i32(lens))
+    check_rows(o, q, kc, vc, table, lens, D ** -0.5, range(len(lens)), "long slots")
+
+
+@pytest.mark.parametrize("B", [65536, 65537])
+@pytest.mark.parametrize("dt,width,long,scored", [("bf16", 600, 9500, False), ("fp32", 64, 1000, True)])
+def test_attend_most_sequences(B, dt, width, long, scored):
+    """The most sequences whose slots are shared out, and one more: each is one
+    slot then, however long."""
+    announce("attend %d sequences %s scores=%s" % (B, dt, scored))
+    D, page, G = 64, 16, 2
+    g = torch.Generator(device=DEV).manual_seed(B)
+    need = -(-long // page)
+    P = B + need
+    kc, vc = (torch.randn((P, 1, page, D), device=DEV, generator=g).to(DTYPES[dt]) for _ in range(2))
+    lens = torch.randint(0, 17, (B,), device=DEV, generator=g, dtype=torch.int32)
+    pages = torch.randperm(P, device=DEV, generator=g, dtype=torch.int32)
+    table = torch.full((B, width), -1, device=DEV, dtype=torch.int32)
+    table[:, 0] = pages[:B]
+    at = B // 3
+    lens[at] = long
+    table[at, 1:need] = pages[B:B + need - 1]
+    q = (2 * torch.randn((B, 1, G, D), device=DEV, generator=g)).to(DTYPES[dt])
+    sc = torch.zeros((P, 1, page), device=DEV) if scored else None
+    o = gdr.attention_decode(q, kc, vc, table, lens, scores=sc)
+    host = lens.tolist()
+    which = [0, 1, at, B - 2, B - 1] + list(range(5, B, B // 300))
+    check_rows(o, q, kc, vc, table, host, D ** -0.5, which, "sequences")
+    assert bool((o[lens == 0] == 0).all()) and bool(torch.isfinite(o).all())
+    if scored:
+        # a sequence's weights sum to the G rows that it has: off by at most
+        # (2 e + (N + 16) u) relative, far below 2^-12
+        each = torch.zeros(P, device=DEV, dtype=torch.float64)
+        each[:] = sc.double().sum((1, 2))
+        total = torch.where(table >= 0, each[table.long().clamp_min(0)], 0.0).sum(1)
+        want = torch.where(lens > 0, float(G), 0.0).double()
+        assert bool(((total - want).abs() <= 2.0 ** -12 * G).all())
