@@ -64,6 +64,8 @@ def _table(name, t, B, dev):
     shape = t.shape
     if len(shape) != 2 or shape[0] != B:
         raise GdrError("%s must be [B,max_pages] with B = %d, got %s" % (name, B, list(shape)))
+    if B >= 1 << 31 or shape[1] >= 1 << 31:     # (as in _int)
+        raise GdrError("%s is too large: %s" % (name, list(shape)))
     return shape[1]
 
 

@@ -257,3 +257,18 @@ def test_attend_most_sequences(B, dt, width, long, scored):
         total = torch.where(table >= 0, each[table.long().clamp_min(0)], 0.0).sum(1)
         want = torch.where(lens > 0, float(G), 0.0).double()
         assert bool(((total - want).abs() <= 2.0 ** -12 * G).all())
+
+
+def test_tables_past_2_31_pages_are_refused():
+    """(Of no sequences, which takes no memory.)  A C int would hold the low 32
+    bits of such a width."""
+    table = torch.empty((0, 2 ** 32 + 2), device=DEV, dtype=torch.int32)
+    kc, sc = torch.zeros((3, 1, 16, 64), device=DEV), torch.zeros((3, 1, 16), device=DEV)
+    none, k = i32([]), torch.zeros((0, 1, 1, 64), device=DEV)
+    for call in (lambda: gdr.cache_append(k, k, none, table, kc, kc.clone()),
+                 lambda: gdr.attention_decode(k, kc, kc.clone(), table, none),
+                 lambda: gdr.cache_evict(kc, kc.clone(), sc, table, none, 4),
+                 lambda: gdr.cache_evict(kc, kc.clone(), sc, table[:, :2].contiguous(), none, 4,
+                                         new_page_table=table)):
+        with pytest.raises(gdr.GdrError, match="too large"):
+            call()
