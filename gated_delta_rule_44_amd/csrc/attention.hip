@@ -18,7 +18,7 @@
 // operands.  Bytes bound the kernel: 2 D elements a token against 4 D flops
 // per row and token is at most 32 flops a byte, where the card turns at
 // about 250.  64 contexts of 512 to 8,192 tokens, 8 heads of 128 in bf16 (681
-// MB): 116 us, 5.9 TB/s, where a plain read of that size reaches 6.2 to 6.5 and
+// MB): 118 us, 5.8 TB/s, where a plain read of that size reaches 6.2 to 6.5 and
 // a copy 5.0; the same with K and V only loaded: 112 us.
 #include "cache_internal.h"
 #include "gdr_internal.h"
@@ -87,12 +87,15 @@ Plan make_plan(int B, int n, int G, int Hkv, int rw, long long capacity) {
 // several blocks, which read K and V from L2 after the first.  In fp32 a block
 // of 32 would need twice the registers there are.
 //   Over 32 rows with much to read, 64: two tiles of rows share the tokens
-// through LDS (16 new tokens, 4 heads of 4 rows each: 16 contexts of 2,000
-// tokens 25 us against 39 in blocks of 32, of 1,500 24 against 31, 2 of 16,000
-// 25 against 37).  With little to read the two blocks side by side are done
-// sooner (16 contexts of 1,000: 21 us against 23; one of 300: 11 against 17).
-// The lengths are on the device, so what the table and the window let a
-// sequence attend to decides.
+// through LDS (16 new tokens, 4 heads of 4 rows each, from cold caches: 16
+// contexts of 2,000 tokens 31 us against 46 in blocks of 32, of 1,500 30
+// against 37, 2 of 16,000 29 against 42).  With little to read the two blocks
+// side by side are done sooner (16 contexts of 1,000: 26 us against 29; one of
+// 300: 12 against 16).  The lengths are on the device, so what the table and
+// the window let a sequence attend to decides, and short contexts under a wide
+// table lose by it (the one of 300 under a table of 131,072 tokens, a call
+// with its second launch: 18 us, 10 under a table of its length; 16 of 300 to
+// 1,000 with 8 heads: 29 either way).
 constexpr long long kShareBytes = 40LL << 20;
 int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long long capacity,
                int window) {
@@ -271,8 +274,10 @@ __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ inline float finite_top(float m) { return m == -INFINITY ? 0.f : m; }
 
 // K and V that one workgroup reads once pass through the caches without
-// staying there (64 contexts, 680 MB: 142 -> 129 us); what several row blocks
-// read is kept.
+// staying there (64 contexts of 4,096 tokens: 169 us, 195 without the hint);
+// what several row blocks read is kept.  Which pages sequences share only the
+// device knows: of shared ones the caches then keep less (half of each context
+// shared by all 64: 137 us, 121 without the hint).
 template <bool STREAM>
 __device__ inline u32x4 load16(rsrc_t r, unsigned off) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, STREAM ? 2 : 0);
@@ -621,7 +626,8 @@ template <int D> struct Tile<float, D, 16> {
 //   RT = 2: two waves read each tile, which all threads bring into LDS
 // together, a stage (a tile per share) at a time: one stage is worked on while
 // the next comes into registers, to be written beside it.  (16 contexts of
-// 1,000 to 6,000, 64 rows a head: 53 us, 74 with RT = 1.  Rows in LDS are
+// 1,000 to 6,000, 64 rows a head: 58 us; with one bf16 number a weight 53, and
+// 74 with RT = 1.  Rows in LDS are
 // padded rather than exchanged: with a 16-byte chunk's place depending on its
 // row by an exclusive or, the addresses alone took so many registers that 34
 // others were spilled, 62 us.)
@@ -1012,7 +1018,9 @@ struct Joined {
 // in turn: D / 4 lanes across a row, the others across slots, a row per wave
 // or (many slots) per workgroup.  With scores, further workgroups each add
 // the weights of 1,024 tokens of a (sequence, head): a thread sums
-// 2^{c (y - m)} / l over the rows, in their order, for four tokens.
+// 2^{c (y - m)} / l over the rows, in their order, for four tokens.  These
+// cover the table's width, and those past a sequence's length end at once (32
+// contexts of up to 6,100 tokens: a call 115 us, 169 under a table of 131,072).
 template <typename T, int D, int RW>
 __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, long long joins,
                                                         long long score_blocks) {

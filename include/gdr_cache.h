@@ -98,14 +98,22 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
  *   scores       NULL, or the accumulated weights, to which the call adds
  *                for every token and key-value head the sum of w_j over the
  *                n_tok * Hq / Hkv rows that read it.  A page must then
- *                belong to one sequence of the call (without scores, pages
- *                may be shared).
+ *                be in the table once (without scores, pages may be shared).
  *   page_table_host  host copy of page_table, optional: validated first
  *                (values in -1..num_pages-1; with scores, no page twice)
  *   workspace    device buffer of gdr_attention_workspace_bytes bytes (0 for a
  *                table without pages: NULL is accepted then), 16-byte
  *                aligned; needs no clearing; not to be shared with a
- *                concurrent call
+ *                concurrent call.  With scores it holds the products q.k of
+ *                every row and place of the table, 4 * B * n_tok * Hq *
+ *                max_pages * page_size bytes whatever the lengths and the
+ *                window are (64 sequences, one token, 32 heads, a table of
+ *                131,072 tokens: 1 GiB)
+ *
+ * The lengths are on the device: sizes, launches and the choice of a kernel
+ * follow the table's width.  A table no wider than the longest sequence of
+ * the call needs less memory and, for short sequences, less time than one as
+ * wide as the longest context served.
  *
  * Numerics: fp32 accumulation, logits, softmax statistics and weights; with
  * bf16 inputs a weight enters the product with V as the sum of two bf16
