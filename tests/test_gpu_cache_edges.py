@@ -129,6 +129,31 @@ def test_attend_weights_of_bf16_values(D, page, n, G, wide):
     assert worst <= 1
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_fp32_logits_of_many_small_products(D):
+    """Two tokens: one's product with q is 1, the other's 1 and, in every fourth
+    channel but one, 0.9 * 2^-24 more, each less than half of fp32's step at 1.
+    Their values are -1 and 1, so that o = tanh(scale * difference / 2).  Summed
+    in four parts of D / 16 products that are not 0, a logit is off by at most
+    (D / 16 + 3) u with u = 2^-24 (one sum would lose all D / 4 - 1 of them); that
+    many times scale / 2, and 24 u of the weights and their sum, is o's bound."""
+    announce("attend fp32 logits D=%d" % D)
+    u, scale = 2.0 ** -24, 64.0
+    small = [16 * i + e for i in range(D // 16) for e in range(4)][1:]
+    kc, vc = (torch.zeros((1, 1, 16, D), device=DEV) for _ in range(2))
+    q = torch.zeros((1, 1, 1, D), device=DEV)
+    q[..., [0] + small] = 1
+    kc[0, 0, :2, 0] = 1
+    kc[0, 0, 1, small] = 0.9 * u
+    vc[0, 0, 0], vc[0, 0, 1] = -1, 1
+    o = gdr.attention_decode(q, kc, vc, i32([[0]]), i32([2]), scale=scale).double().cpu().numpy()
+    diff = kc[0, 0, 1, small].double().sum().item()
+    err = np.abs(o - np.tanh(scale * diff / 2)).max()
+    lim = (D / 16 + 3) * u * scale / 2 + 24 * u
+    announce("  error / bound %.3f" % (err / lim))
+    assert err <= lim
+
+
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
 @pytest.mark.parametrize("n,G", [(1, 4), (5, 4), (10, 4)])
