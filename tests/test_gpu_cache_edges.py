@@ -297,3 +297,100 @@ def test_tables_past_2_31_pages_are_refused():
                                          new_page_table=table)):
         with pytest.raises(gdr.GdrError, match="too large"):
             call()
+
+
+# --------------------------- several launches: captured, and two calls at once
+def same(a, b):
+    """Equal bit for bit (NaN included)."""
+    kind = {2: torch.int16, 4: torch.int32}[a.element_size()]
+    return a.shape == b.shape and torch.equal(a.contiguous().view(kind), b.contiguous().view(kind))
+
+
+def paged(lens, Hkv, D, page, width, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    need = [-(-l // page) for l in lens]
+    P = sum(need) + 1
+    kc, vc = (torch.randn((P, Hkv, page, D), device=DEV, generator=g).bfloat16() for _ in range(2))
+    sc = torch.rand((P, Hkv, page), device=DEV, generator=g)
+    table = np.full((len(lens), width), -1, np.int32)
+    order, at = np.random.default_rng(seed).permutation(P), 0
+    for b, c in enumerate(need):
+        table[b, :c] = order[at:at + c]
+        at += c
+    return kc, vc, sc, i32(table), i32(lens)
+
+
+def many_short(seed):
+    """300 sequences, two of them split: a launch finds the slots' owners."""
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(0, 40, 300)]
+    lens[7], lens[250] = 1500 + seed, 900
+    kc, vc, sc, table, dl = paged(lens, 1, 64, 16, 110, seed)
+    q = torch.randn((300, 2, 4, 64), device=DEV).bfloat16()
+    ws = torch.empty(gdr.attention_workspace_bytes(300, 2, 4, 1, 64, 110, 16, True), device=DEV,
+                     dtype=torch.uint8)
+    inputs = [q, kc, vc, sc, dl]
+
+    def call(q, kc, vc, sc, dl, ws):
+        return [gdr.attention_decode(q, kc, vc, table, dl, scores=sc, workspace=ws), sc]
+    return inputs, ws, call
+
+
+def long_trim(seed):
+    """Two pairs of 9,000 tokens and more, in place: a launch per digit."""
+    kc, vc, sc, table, dl = paged([9000 + seed, 8700], 1, 64, 128, 80, seed)
+    ws = torch.empty(gdr.evict_workspace_bytes(2, 1, 80, 128), device=DEV, dtype=torch.uint8)
+    assert ws.numel() > 0
+
+    def call(kc, vc, sc, dl, ws):
+        nl, kept = gdr.cache_evict(kc, vc, sc, table, dl, 3001, 200, 4, workspace=ws)
+        return [nl, kept, kc, vc, sc]
+    return [kc, vc, sc, dl], ws, call
+
+
+@pytest.mark.parametrize("make", [many_short, long_trim])
+def test_several_launches_captured(make):
+    """Replays on new contents equal eager calls made between them."""
+    announce("capture %s" % make.__name__)
+    inputs, ws, call = make(1)
+    held = [x.clone() for x in inputs]
+    call(*[x.clone() for x in inputs], ws)
+    torch.cuda.synchronize(DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(*held, ws)
+    for rep in range(3):
+        announce("  replay %d" % rep)
+        new = [x.clone() for x in inputs]
+        for x in new:
+            if x.is_floating_point():
+                x.copy_(torch.rand(x.shape, device=DEV).to(x.dtype))
+            else:
+                x.sub_(rep * (x > 50).int())
+        want = call(*[x.clone() for x in new], torch.empty_like(ws))
+        for x, y in zip(held, new):
+            x.copy_(y)
+        torch.cuda.synchronize(DEV)
+        graph.replay()
+        torch.cuda.synchronize(DEV)
+        for a, b in zip(out, want):
+            assert same(a, b), rep
+
+
+@pytest.mark.parametrize("make", [many_short, long_trim])
+def test_several_launches_on_two_streams(make):
+    announce("two streams %s" % make.__name__)
+    runs = [make(2), make(3)]
+    want = [call(*[x.clone() for x in inputs], ws) for inputs, ws, call in runs]
+    streams = [torch.cuda.Stream(DEV) for _ in runs]
+    for rep in range(3):
+        copies = [[x.clone() for x in inputs] for inputs, _, _ in runs]
+        torch.cuda.synchronize(DEV)
+        got = []
+        for st, c, (_, ws, call) in zip(streams, copies, runs):
+            with torch.cuda.stream(st):
+                got.append(call(*c, ws))
+        torch.cuda.synchronize(DEV)
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert same(x, y), rep
