@@ -442,7 +442,7 @@ template <int D, int RW> struct Tile<bf16, D, RW> {
     // that lo is above 0 wherever the weight is and an infinity of V that a row
     // attends to meets no 0 of a weight that one number holds.
     //   The second product costs nothing where bytes bound the call (64 contexts
-    // 120 us either way), 6 % in blocks of 64 rows (54 -> 58 us), and brings o
+    // 120 us either way), 7 % in blocks of 64 rows (55 -> 59 us), and brings o
     // from 1.08 to 1.00 times the error of fp32 weights against 64 bits.
     struct P { bf16x8 hi[kVals / 8], lo[kVals / 8]; };
     __device__ static inline P weights(const float (&x)[kVals]) {
@@ -631,7 +631,7 @@ template <int D> struct Tile<float, D, 16> {
 //   RT = 2: two waves read each tile, which all threads bring into LDS
 // together, a stage (a tile per share) at a time: one stage is worked on while
 // the next comes into registers, to be written beside it.  (16 contexts of
-// 1,000 to 6,000, 64 rows a head: 58 us; with one bf16 number a weight 53, and
+// 1,000 to 6,000, 64 rows a head: 59 us; with one bf16 number a weight 55, and
 // 74 with RT = 1.  Rows in LDS are
 // padded rather than exchanged: with a 16-byte chunk's place depending on its
 // row by an exclusive or, the addresses alone took so many registers that 34
