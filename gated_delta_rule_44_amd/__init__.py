@@ -24,7 +24,8 @@ __all__ = ["prefill", "prefill_varlen", "prefill_varlen_pool", "decode_step",
            "prefill_fused", "prefill_varlen_fused", "decode_tokens_fused",
            "fused_workspace_bytes", "backward", "backward_varlen",
            "cache_append", "attention_decode", "attention_workspace_bytes", "cache_evict",
-           "evict_workspace_bytes",
+           "evict_workspace_bytes", "attention_prefill", "attention_backward",
+           "attention_backward_workspace_bytes",
            "version", "GdrError", "lib_path",
            "FA", "SWA", "GDN", "KDA"]
 
@@ -114,6 +115,14 @@ def _load():
     lib.gdr_cache_evict_workspace_bytes.argtypes = [I, I, I, I]
     lib.gdr_cache_evict.argtypes = [I, I, I, I, I, I, I, P, P, P, P, P, I, P, P, I, I, I, P, P,
                                     P, P, Z, P]
+    # include/gdr_attention.h
+    lib.gdr_attention_prefill.restype = I
+    lib.gdr_attention_prefill.argtypes = [I, I, I, I, I, I, I, F, I, P, P, P, P, P, P, P, P]
+    lib.gdr_attention_backward_workspace_bytes.restype = Z
+    lib.gdr_attention_backward_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.gdr_attention_backward.restype = I
+    lib.gdr_attention_backward.argtypes = [I, I, I, I, I, I, I, F, I, P, P, P, P, P, P, P, P, P,
+                                           P, P, P, Z, P]
     _lib = lib
     return lib
 
@@ -654,3 +663,6 @@ def backward_varlen(q, k, v, g, beta, do, cu_seqlens, h0=None, dht=None, scale: 
 # the paged key-value cache of the attention layers (include/gdr_cache.h)
 from .cache import (attention_decode, attention_workspace_bytes, cache_append,  # noqa: E402
                     cache_evict, evict_workspace_bytes)
+# attention of whole prompts (include/gdr_attention.h)
+from .attention import (attention_backward, attention_backward_workspace_bytes,  # noqa: E402
+                        attention_prefill)

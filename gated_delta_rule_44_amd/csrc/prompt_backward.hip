@@ -1,0 +1,259 @@
+// prompt_backward.hip -- the gradients of attention over whole prompts, for
+// gfx950.
+//
+// With s_ij = scale q_i.k_j, w_ij = e^{s_ij - lse_i}, delta_i = do_i.o_i:
+//     ds_ij = w_ij (do_i.v_j - delta_i),
+//     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+//     dv_j = sum_i w_ij do_i.
+//
+// Two kernels, so that no sum is shared between workgroups: query_kernel walks
+// a block of rows over its tokens (s, do.v and dq: three products), key_kernel
+// a block of tokens over the rows of every head of its group that attend to
+// it (s, do.v, dv and dk: four).  Seven products where five would do, for
+// results that do not depend on the order of workgroups.
+#include "prompt_internal.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kWaves = 4;                  // waves of a workgroup, 32 rows or tokens each
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;
+
+// Workspace: lse log2 e (+inf for a row without weights) and delta of every
+// row, head by head.
+struct KArgs {
+    PromptArgs a;
+    float c;              // scale log2 e
+    int blocks;           // block_bound
+    float *lse2, *delta;  // [Hq, T_total]
+};
+
+template <typename T> __device__ inline float dot_part(const T *x, const T *y, int n) {
+    float s = 0.f;
+    for (int i = 0; i < n; i += 4) {
+        const f32x4 u = Elem<T>::load4(x + i), v = Elem<T>::load4(y + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = fmaf(u[e], v[e], s);
+    }
+    return s;
+}
+
+// Workgroup = (block of 128 rows, query head), 32 rows a wave.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 128 ? 1 : 2)) void query_kernel(KArgs k) {
+    using R = Rows<T, D>;
+    constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols;
+    __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
+    const PromptArgs &a = k.a;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int w = uniform(tid >> 6);
+    const int head = blockIdx.x % a.Hq;
+    const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
+    if (bl.i < 0) return;
+    const int i0 = bl.i * kRows, iw = i0 + 32 * w, i = iw + r;
+    const int hk = head / a.G;
+    const unsigned kpitch = a.Hkv * D * (unsigned)sizeof(T);
+    const T *kh = static_cast<const T *>(a.k) + (size_t)hk * D;
+    const T *vh = static_cast<const T *>(a.v) + (size_t)hk * D;
+    const typename R::At at = R::at(lane);
+
+    typename R::B q, g;
+    float lse2, delta;
+    {
+        const int row = bl.row0 + (i < bl.len ? i : bl.len - 1);
+        const size_t at_row = ((size_t)row * a.Hq + head) * D;
+        R::load(q, static_cast<const T *>(a.q) + at_row, h);
+        R::load(g, static_cast<const T *>(a.d_o) + at_row, h);
+        const float x = a.lse[(size_t)row * a.Hq + head];
+        lse2 = x == -INFINITY ? INFINITY : x * kLog2e;
+        delta = swap_sum32(dot_part(static_cast<const T *>(a.d_o) + at_row + D / 2 * h,
+                                    static_cast<const T *>(a.o) + at_row + D / 2 * h, D / 2));
+        if (i < bl.len && h == 0) {
+            k.lse2[(size_t)head * a.T_total + row] = lse2;
+            k.delta[(size_t)head * a.T_total + row] = delta;
+        }
+    }
+    const int last = i0 + kRows < bl.len ? i0 + kRows - 1 : bl.len - 1;
+    const int first = a.window > 0 && i0 >= a.window ? i0 - a.window + 1 : 0;
+    const int t0 = first / kTok, t1 = last / kTok + 1;
+    auto attends = [&](int j) { return j <= i && (a.window == 0 || j > i - a.window); };
+    auto stage = [&](int t) {
+        const size_t row = (size_t)bl.row0 + t * kTok;
+        const int left = bl.len - t * kTok;
+        fetch<T, D, kWaves, kTok>(lds[t & 1][0], kh, row, left, kpitch, w, lane);
+        fetch<T, D, kWaves, kTok>(lds[t & 1][1], vh, row, left, kpitch, w, lane);
+    };
+    f32x16 acc[kCols];
+    auto walk = [&](auto clear) {
+        constexpr bool CLEAR = decltype(clear)::value;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
+        stage(t0);
+        R::settle(q);
+        R::settle(g);
+        asm volatile("" : "+v"(lse2), "+v"(delta));
+        for (int t = t0; t < t1; ++t) {
+            tile_landed();
+            if (t + 1 < t1) stage(t + 1);
+            const int j0 = t * kTok;
+            const char *kt = lds[t & 1][0], *vt = lds[t & 1][1];
+            if (iw >= bl.len || j0 > iw + 31 || (a.window > 0 && j0 + kTok <= iw - a.window + 1))
+                continue;
+            const bool full = j0 + kTok - 1 <= iw && (a.window == 0 || j0 > iw + 31 - a.window);
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b) {
+                f32x16 x = R::rows(kt, b, at, q);
+                const f32x16 dp = R::rows(vt, b, at, g);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[e] = exp2_(fmaf(x[e], k.c, -lse2)) * (dp[e] - delta);
+                if (!full) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = attends(j0 + 32 * b + R::key(e, h)) ? x[e] : 0.f;
+                }
+                if (CLEAR && !full) R::template cols<CLEAR>(acc, kt, b, at, R::operand(x));
+                else                R::template cols<false>(acc, kt, b, at, R::operand(x));
+            }
+        }
+    };
+    walk(std::false_type{});
+    // (0 times an infinity or NaN of a key that a row does not attend to: again
+    // without those)
+    if (__syncthreads_or(R::any_odd(acc))) walk(std::true_type{});
+    if (i >= bl.len) return;
+    R::store(static_cast<T *>(a.dq) + ((size_t)(bl.row0 + i) * a.Hq + head) * D, acc, h, a.scale);
+}
+
+// Workgroup = (block of 128 tokens, key-value head), 32 tokens a wave: lane
+// (h, r) has token r of them as a column, tiles of rows pass through LDS.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
+    using R = Rows<T, D>;
+    constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols;
+    __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
+    __shared__ __align__(16) float stats[2][2][kTok];      // lse2 and delta of a tile's rows
+    const PromptArgs &a = k.a;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int w = uniform(tid >> 6);
+    const int hk = blockIdx.x % a.Hkv;
+    const Block bl = find_block<kRows>(a, blockIdx.x / a.Hkv);
+    if (bl.i < 0) return;
+    const int j0 = bl.i * kRows, jw = j0 + 32 * w, j = jw + r;
+    const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
+    const typename R::At at = R::at(lane);
+
+    typename R::B kf, vf;
+    const int row = bl.row0 + (j < bl.len ? j : bl.len - 1);
+    R::load(kf, static_cast<const T *>(a.k) + ((size_t)row * a.Hkv + hk) * D, h);
+    R::load(vf, static_cast<const T *>(a.v) + ((size_t)row * a.Hkv + hk) * D, h);
+    // rows that attend to a token of the block
+    const int over = a.window > 0 && bl.len - j0 > kRows + a.window - 1 ? j0 + kRows + a.window - 1
+                                                                         : bl.len;
+    const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
+
+    // tile n: rows t0 + n % tiles of head hk G + n / tiles
+    auto stage = [&](int n) {
+        const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
+        const size_t first = (size_t)bl.row0 + t * kTok;
+        const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
+        const T *gh = static_cast<const T *>(a.d_o) + (size_t)head * D;
+        fetch<T, D, kWaves, kTok>(lds[n & 1][0], qh, first, left, qpitch, w, lane);
+        fetch<T, D, kWaves, kTok>(lds[n & 1][1], gh, first, left, qpitch, w, lane);
+        if (w < 2) {
+            const int at_row = lane < left ? lane : left - 1;
+            fetch_words<kTok>(stats[n & 1][w], (w ? k.delta : k.lse2) + (size_t)head * a.T_total + first,
+                              at_row, lane);
+        }
+    };
+    f32x16 dk[kCols], dv[kCols];
+    auto walk = [&](auto clear) {
+        constexpr bool CLEAR = decltype(clear)::value;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dk[c][e] = dv[c][e] = 0.f;
+        stage(0);
+        R::settle(kf);
+        R::settle(vf);
+        for (int n = 0; n < all; ++n) {
+            tile_landed();
+            if (n + 1 < all) stage(n + 1);
+            const int i0 = (t0 + n % tiles) * kTok;
+            const char *qt = lds[n & 1][0], *gt = lds[n & 1][1];
+            const float *lse2 = stats[n & 1][0], *delta = stats[n & 1][1];
+            if (jw >= bl.len || i0 + kTok <= jw || (a.window > 0 && i0 >= jw + 31 + a.window)) continue;
+            const bool full = i0 >= jw + 31 && i0 + kTok <= bl.len &&
+                              (a.window == 0 || i0 + kTok - 1 < jw + a.window);
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b) {
+                f32x16 x = R::rows(qt, b, at, kf);
+                f32x16 dp = R::rows(gt, b, at, vf);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse2 + 32 * b + R::key(e, h));
+                    const f32x4 de = *reinterpret_cast<const f32x4 *>(delta + 32 * b + R::key(e, h));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        x[e + u] = exp2_(fmaf(x[e + u], k.c, -ls[u]));
+                        dp[e + u] = x[e + u] * (dp[e + u] - de[u]);
+                    }
+                }
+                if (!full) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int i = i0 + 32 * b + R::key(e, h);
+                        const bool in = j <= i && i < bl.len && (a.window == 0 || j > i - a.window);
+                        x[e] = in ? x[e] : 0.f;
+                        dp[e] = in ? dp[e] : 0.f;
+                    }
+                }
+                if (CLEAR && !full) {
+                    R::template cols<CLEAR>(dv, gt, b, at, R::operand(x));
+                    R::template cols<CLEAR>(dk, qt, b, at, R::operand(dp));
+                } else {
+                    R::template cols<false>(dv, gt, b, at, R::operand(x));
+                    R::template cols<false>(dk, qt, b, at, R::operand(dp));
+                }
+            }
+        }
+    };
+    walk(std::false_type{});
+    if (__syncthreads_or(R::any_odd(dk) || R::any_odd(dv))) walk(std::true_type{});
+    if (j >= bl.len) return;
+    const size_t to = ((size_t)(bl.row0 + j) * a.Hkv + hk) * D;
+    R::store(static_cast<T *>(a.dk) + to, dk, h, a.scale);
+    R::store(static_cast<T *>(a.dv) + to, dv, h, 1.f);
+}
+
+template <typename T, int D>
+hipError_t launch(const PromptArgs &a, hipStream_t s) {
+    KArgs k{};
+    k.a = a;
+    k.c = a.scale * kLog2e;
+    const long long blocks = block_bound<kRows>(a);
+    k.blocks = (int)blocks;
+    k.lse2 = static_cast<float *>(a.ws);
+    k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
+    query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attention_backward_workspace(bool, int, int T_total, int Hq, int, int) {
+    return 2 * (size_t)Hq * T_total * sizeof(float);
+}
+
+hipError_t launch_attention_backward(bool bf16_io, int D, const PromptArgs &a, hipStream_t s) {
+    if (bf16_io) return D == 128 ? launch<bf16, 128>(a, s) : launch<bf16, 64>(a, s);
+    return D == 128 ? launch<float, 128>(a, s) : launch<float, 64>(a, s);
+}
+
+}  // namespace gdr

@@ -1,0 +1,370 @@
+// prompt_internal.h -- attention over whole prompts: the arguments of its
+// kernels, and the device pieces that the forward and the backward pass share.
+// Internal to the library: the public interface is include/gdr_attention.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "device_util.h"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+struct PromptArgs {
+    const void *q, *k, *v;       // [T_total, Hq, D], [T_total, Hkv, D]
+    const int32_t *cu;           // [B+1] or nullptr (T each)
+    void *o;                     // [T_total, Hq, D] (backward: read)
+    float *lse;                  // [T_total, Hq] or nullptr (backward: read)
+    const void *d_o;             // backward only, from here on
+    void *dq, *dk, *dv;
+    void *ws;
+    int B, T, T_total, Hq, Hkv, G;
+    float scale;
+    int window;                  // 0: none
+};
+hipError_t launch_attention_prefill(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
+hipError_t launch_attention_backward(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
+size_t attention_backward_workspace(bool bf16_io, int B, int T_total, int Hq, int Hkv, int D);
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ inline float swap_max32(float x) {
+    float a = x, b = x;
+    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+    return fmaxf(a, b);
+}
+
+// A block of RB tokens of one sequence: its number in the sequence (-1: there
+// is none), the sequence's first row and its tokens.
+struct Block { int i, row0, len; };
+
+// Blocks of a batch, numbered over the sequences.  Packed, the blocks of
+// sequence b start at cu[b] / RB + b, which leaves each at least as many as it
+// has, so that no sums over the sequences before are needed: a few searches of
+// 64 lanes over cu find the sequence.
+template <int RB>
+inline long long block_bound(const PromptArgs &a) {
+    return a.cu ? (long long)a.T_total / RB + a.B : (long long)a.B * ((a.T + RB - 1) / RB);
+}
+template <int RB>
+__device__ inline Block find_block(const PromptArgs &a, int s) {
+    Block x;
+    if (!a.cu) {
+        const int per = (a.T + RB - 1) / RB, b = s / per;
+        x.i = s % per;
+        x.row0 = b * a.T;
+        x.len = a.T;
+        return x;
+    }
+    auto at = [&](int b) {
+        const int c = a.cu[b];
+        return c < 0 ? 0 : (c > a.T_total ? a.T_total : c);
+    };
+    const int lane = threadIdx.x & 63;
+    int base = 0, count = a.B;               // the sequence is in [base, base + count)
+    while (count > 1) {
+        const int step = (count + 63) / 64, b = base + lane * step;
+        const bool before = lane * step < count && at(b) / RB + b <= s;
+        int last = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before)) - 1;
+        last = last < 0 ? 0 : last;
+        base += last * step;
+        count = count - last * step < step ? count - last * step : step;
+    }
+    const int lo = uniform(at(base)), hi = uniform(at(base + 1));
+    x.i = s - (lo / RB + base);
+    x.row0 = lo;
+    x.len = hi - lo;
+    if (x.i < 0 || x.len <= 0 || x.i > (x.len - 1) / RB) x.i = -1;
+    return x;
+}
+
+// Rows of 32 tokens as MFMA operands, and products with tiles of rows that lie
+// in LDS.  All three kernels are made of two products, with lane = 32 h + r:
+//   rows:  X = tile . b^T, b 32 rows in registers: the lane gets X[j][r] for
+//     the tile's rows j = key(e, h), value e of the accumulator;
+//   cols:  acc^T += tile^T . P, P = 32 columns of which the lane holds
+//     P[key(e, h)][r], e ascending: what `rows` gave, as it lies, the sum
+//     running over the tile's rows in whatever order both operands use.  The
+//     lane gets acc[c][e] = channel dim(c, e, h) of row r.
+//
+// A tile's rows are stored in chunks of 16 bytes, chunk c of row j at place
+// c ^ swz(j): 16 lanes that read one chunk of 16 rows (`rows`) and 32 that
+// read pieces of four rows (`cols`) then meet every bank once.
+template <typename T, int D> struct Rows;
+
+template <int D> struct Rows<bf16, D> {
+    typedef bf16 T;
+    static constexpr int kTok = 64, kRowBytes = 2 * D, kChunks = D / 8;
+    static constexpr int kTileBytes = kTok * kRowBytes;
+    static constexpr int kCols = D / 32;              // accumulators of `cols`
+    struct B { bf16x8 f[D / 16]; };
+    __device__ static inline int key(int e, int h) { return 8 * (e >> 2) + 4 * h + (e & 3); }
+    __device__ static inline int dim(int c, int e, int h) { return D / 2 * h + 16 * c + e; }
+    __device__ static inline int swz(int j) {
+        if constexpr (D == 128) return ((j & 3) << 1) | ((j >> 2) & 1) | (((j >> 3) & 1) << 3);
+        else return (((j >> 1) & 1) << 1) | ((j >> 2) & 1) | (((j >> 3) & 1) << 2);
+    }
+    // row: the lane's row of b
+    __device__ static inline void load(B &b, const T *row, int h) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) b.f[i] = ld8(row + 16 * i + 8 * h);
+    }
+    // makes the loads of b end here, not in a loop that follows
+    __device__ static inline void settle(B &b) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(b.f[i]));
+    }
+    __device__ static inline void negate(B &b) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            b.f[i] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, b.f[i]) ^ 0x80008000u);
+    }
+    // what a lane adds to a tile's address in `rows` and in `cols`
+    struct At { int row, col; };
+    __device__ static inline At at(int lane) {
+        const int r = lane & 31, h = lane >> 5, j = lane & 15;
+        At a;
+        a.row = r * kRowBytes + ((h ^ swz(r)) << 4);
+        // lane j of 16 reads four channels of row 4 h + j / 4: of the segments
+        // m / 4 = 4 (lane / 16 % 2) + j % 4 of the accumulator's rows m
+        const int seg = 4 * ((lane >> 4) & 1) + (j & 3), row = 4 * h + (j >> 2);
+        const int q = seg >> 1, chunk = D / 16 * (seg & 1) + (q >> 1);
+        a.col = row * kRowBytes + ((chunk ^ swz(row)) << 4) + 8 * (q & 1);
+        return a;
+    }
+    // rows 32 blk .. of the tile
+    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b) {
+        f32x16 s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const bf16x8 x = *reinterpret_cast<const bf16x8 *>(
+                tile + 32 * blk * kRowBytes + (a.row ^ (i << 5)));
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, b.f[i], s, 0, 0, 0);
+        }
+        return s;
+    }
+    struct P { bf16x8 f[2]; };
+    __device__ static inline P operand(const f32x16 &x) {
+        P p;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) p.f[k][u] = (bf16)x[8 * k + u];
+        return p;
+    }
+    // rows 32 blk + 16 k .. as the operand of channel block c
+    __device__ static inline bf16x8 col_frag(const char *tile, int blk, int k, int c, const At &a) {
+        const char *t = tile + (32 * blk + 16 * k) * kRowBytes;
+        const int flip = swz(8) << 4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + (a.col ^ (c << 5))));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4 *)(t + 8 * kRowBytes + (a.col ^ (c << 5) ^ flip)));
+        return cat8(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi));
+    }
+    // without infinities and NaN (an exponent of all ones)
+    __device__ static inline bf16x8 clear(bf16x8 x) {
+        u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0u : w[i] & 0xFFFFu) |
+                   ((w[i] & 0x7F800000u) == 0x7F800000u ? 0u : w[i] & 0xFFFF0000u);
+        return __builtin_bit_cast(bf16x8, w);
+    }
+    // CLEAR: without the tile's infinities and NaN
+    template <bool CLEAR>
+    __device__ static inline void cols(f32x16 (&acc)[kCols], const char *tile, int blk, const At &a,
+                                       const P &p) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                bf16x8 x = col_frag(tile, blk, k, c, a);
+                if constexpr (CLEAR) x = clear(x);
+                acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, p.f[k], acc[c], 0, 0, 0);
+            }
+    }
+    __device__ static inline bool any_odd(const f32x16 (&acc)[kCols]) {
+        bool y = false;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y |= !(fabsf(acc[c][e]) < INFINITY);
+        return y;
+    }
+    // adds a row's infinities and NaN
+    __device__ static inline void add_odd(f32x16 (&acc)[kCols], const T *row, int h) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = (float)row[dim(c, e, h)];
+                acc[c][e] += fabsf(x) < INFINITY ? 0.f : x;
+            }
+    }
+    // acc[.][.] of one row: D / 2 channels from D / 2 h on
+    __device__ static inline void store(T *row, const f32x16 (&acc)[kCols], int h, float f) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float y[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) y[u] = acc[c][8 * k + u] * f;
+                *reinterpret_cast<bf16x8 *>(row + dim(c, 8 * k, h)) = cvt8(y);
+            }
+    }
+};
+
+template <int D> struct Rows<float, D> {
+    typedef float T;
+    static constexpr int kTok = 32, kRowBytes = 4 * D, kChunks = D / 4;
+    static constexpr int kTileBytes = kTok * kRowBytes;
+    static constexpr int kCols = D / 32;
+    struct B { f32x4 f[D / 8]; };
+    __device__ static inline int key(int e, int h) { return 8 * (e >> 2) + 4 * h + (e & 3); }
+    __device__ static inline int dim(int c, int e, int h) { return kCols * key(e, h) + c; }
+    __device__ static inline int swz(int j) { return j & 15; }
+    __device__ static inline void load(B &b, const T *row, int h) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) b.f[i] = *reinterpret_cast<const f32x4 *>(row + 8 * i + 4 * h);
+    }
+    // makes the loads of b end here, not in a loop that follows
+    __device__ static inline void settle(B &b) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) asm volatile("" : "+v"(b.f[i]));
+    }
+    __device__ static inline void negate(B &b) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) b.f[i] = -b.f[i];
+    }
+    struct At { int row, col; };
+    __device__ static inline At at(int lane) {
+        const int r = lane & 31, h = lane >> 5, byte = 4 * kCols * r;
+        At a;
+        a.row = r * kRowBytes + ((h ^ swz(r)) << 4);
+        a.col = 4 * h * kRowBytes + (((byte >> 4) ^ swz(4 * h)) << 4) + (byte & 15);
+        return a;
+    }
+    __device__ static inline f32x16 mfma(float a, float b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+    }
+    // two sums of D / 2 products, then theirs
+    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b) {
+        f32x16 s, t;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = t[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(
+                tile + 32 * blk * kRowBytes + (a.row ^ (i << 5)));
+            s = mfma(x[0], b.f[i][0], s);
+            t = mfma(x[1], b.f[i][1], t);
+            s = mfma(x[2], b.f[i][2], s);
+            t = mfma(x[3], b.f[i][3], t);
+        }
+        return s + t;
+    }
+    struct P { f32x16 f; };
+    __device__ static inline P operand(const f32x16 &x) { return P{x}; }
+    typedef float run_t __attribute__((ext_vector_type(kCols)));
+    // row key(e, h) of block blk: channels kCols r ..
+    __device__ static inline run_t col_frag(const char *tile, int blk, int e, const At &a) {
+        const int j = 8 * (e >> 2) + (e & 3);
+        return *reinterpret_cast<const run_t *>(tile + (32 * blk + j) * kRowBytes +
+                                                (a.col ^ (swz(j) << 4)));
+    }
+    // (a value parameter: the bit cast of a vector's element in place takes the
+    // vector's first element)
+    __device__ static inline unsigned bits(float x) { return __builtin_bit_cast(unsigned, x); }
+    __device__ static inline bool odd(float x) { return (bits(x) & 0x7F800000u) == 0x7F800000u; }
+    template <bool CLEAR>
+    __device__ static inline void cols(f32x16 (&acc)[kCols], const char *tile, int blk, const At &a,
+                                       const P &p) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const run_t x = col_frag(tile, blk, e, a);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                acc[c] = mfma(CLEAR && odd(x[c]) ? 0.f : x[c], p.f[e], acc[c]);
+        }
+    }
+    __device__ static inline bool any_odd(const f32x16 (&acc)[kCols]) {
+        bool y = false;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y |= !(fabsf(acc[c][e]) < INFINITY);
+        return y;
+    }
+    __device__ static inline void add_odd(f32x16 (&acc)[kCols], const T *row, int h) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = row[dim(c, e, h)];
+                acc[c][e] += odd(x) ? x : 0.f;
+            }
+    }
+    __device__ static inline void store(T *row, const f32x16 (&acc)[kCols], int h, float f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            run_t y;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) y[c] = acc[c][e] * f;
+            *reinterpret_cast<run_t *>(row + dim(0, e, h)) = y;
+        }
+    }
+};
+
+// Rows row0 .. of a head ([rows, heads, D], heads * D elements apart) into a
+// tile in LDS, by the waves of a workgroup, straight from memory: a wave's
+// instruction fills 1 KiB, 16 bytes a lane in their order, so that the lane
+// asks for the chunk that belongs there.  Rows from `valid` (>= 1) on are
+// copies of the last one, which the callers mask.  (Written out: the compiler
+// would wait for a load to LDS before the next read of any LDS.)
+template <typename T, int D, int WAVES, int ROWS>
+__device__ inline void fetch(char *tile, const T *head, size_t row0, int valid, unsigned pitch,
+                             int w, int lane) {
+    using R = Rows<T, D>;
+    constexpr int kPer = 1024 / R::kRowBytes, kAll = ROWS / kPer;
+    static_assert(kAll % WAVES == 0, "the waves fetch alike");
+    const unsigned long long base = reinterpret_cast<unsigned long long>(head) + row0 * pitch;
+    const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)), 0xFFFFFFFFu,
+                   0x00020000u};
+    const unsigned to = (unsigned)uniform((int)reinterpret_cast<size_t>((lds_void *)tile));
+#pragma unroll
+    for (int i = 0; i < kAll / WAVES; ++i) {
+        const int n = w + WAVES * i, j = n * kPer + lane / R::kChunks;
+        const int chunk = lane % R::kChunks ^ R::swz(j);
+        const int row = j < valid ? j : valid - 1;
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                     :: "s"(to + 1024u * n), "v"(row * pitch + 16u * chunk), "s"(rs) : "memory");
+    }
+}
+// 4 bytes a lane of `from` (its element `index`), lanes 0 .. N - 1, into words
+// that lie together in LDS, likewise.
+template <int N>
+__device__ inline void fetch_words(float *to, const float *from, int index, int lane) {
+    const unsigned long long base = reinterpret_cast<unsigned long long>(from);
+    const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)), 0xFFFFFFFFu,
+                   0x00020000u};
+    const unsigned at = (unsigned)uniform((int)reinterpret_cast<size_t>((lds_void *)to));
+    if (lane < N)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                     :: "s"(at), "v"(4u * index), "s"(rs) : "memory");
+}
+// After fetch: waits until every wave's part is there, and until every wave is
+// done with what it read before.
+__device__ inline void tile_landed() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
+}  // namespace gdr
