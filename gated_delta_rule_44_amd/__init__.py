@@ -25,6 +25,7 @@ __all__ = ["prefill", "prefill_varlen", "prefill_varlen_pool", "decode_step",
            "fused_workspace_bytes", "backward", "backward_varlen",
            "cache_append", "attention_decode", "attention_workspace_bytes", "cache_evict",
            "evict_workspace_bytes", "attention_prefill", "attention_backward",
+           "attention_tree", "cache_accept", "cache_resize",
            "attention_backward_workspace_bytes",
            "version", "GdrError", "lib_path",
            "FA", "SWA", "GDN", "KDA"]
@@ -123,6 +124,13 @@ def _load():
     lib.gdr_attention_backward.restype = I
     lib.gdr_attention_backward.argtypes = [I, I, I, I, I, I, I, F, I, P, P, P, P, P, P, P, P, P,
                                            P, P, P, Z, P]
+    lib.gdr_attention_tree.restype = I
+    lib.gdr_attention_tree.argtypes = [I, I, I, I, I, I, F, I, P, P, P, P, P, I, I, I, P, P, P, P,
+                                       Z, P]
+    lib.gdr_cache_accept.restype = I
+    lib.gdr_cache_accept.argtypes = [I, I, I, I, I, P, I, I, I, P, P, P, P, P, P, P, P, P]
+    lib.gdr_cache_resize.restype = I
+    lib.gdr_cache_resize.argtypes = [I, I, I, I, P, P, P, P, P, P, P]
     _lib = lib
     return lib
 
@@ -661,8 +669,8 @@ def backward_varlen(q, k, v, g, beta, do, cu_seqlens, h0=None, dht=None, scale: 
 
 
 # the paged key-value cache of the attention layers (include/gdr_cache.h)
-from .cache import (attention_decode, attention_workspace_bytes, cache_append,  # noqa: E402
-                    cache_evict, evict_workspace_bytes)
+from .cache import (attention_decode, attention_tree, attention_workspace_bytes,  # noqa: E402
+                    cache_accept, cache_append, cache_evict, cache_resize, evict_workspace_bytes)
 # attention of whole prompts (include/gdr_attention.h)
 from .attention import (attention_backward, attention_backward_workspace_bytes,  # noqa: E402
                         attention_prefill)

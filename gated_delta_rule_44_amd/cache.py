@@ -1,6 +1,8 @@
 """The paged key-value cache of a placement's attention layers: the write of
 new tokens, attention of new tokens over the cache, and eviction by
-accumulated attention weight (include/gdr_cache.h states each call in full).
+accumulated attention weight (include/gdr_cache.h states each call in full);
+trees of drafted tokens over it, and page tables that follow the sequences'
+lengths (include/gdr_attention.h).
 
 k_cache, v_cache [P, Hkv, page, D] (bf16 or fp32), page one of 16, 32, 64,
 128, 256 tokens; page_table int32 [B, max_pages] on the GPU names the pages of
@@ -256,3 +258,128 @@ def cache_evict(k_cache, v_cache, scores, page_table, seq_lens, budget: int, rec
           _p(new_page_table), _hp(host2), M2, page, P, seq_lens.data_ptr(), new_lens.data_ptr(),
           kept.data_ptr(), _p(workspace), nbytes)
     return new_lens, kept
+
+
+def _attend_args(q, k_cache, v_cache, page_table, seq_lens, window, page_table_host, o):
+    dev, dtype, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, None)
+    _gpu("q", q, dtype, dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise GdrError("q must be [B,n,Hq,D] with D = %d, got %s" % (D, list(shape)))
+    B, n, Hq, _ = shape
+    if Hq < 1 or Hq % Hkv:
+        raise GdrError("Hq (%d) must be a multiple of Hkv (%d)" % (Hq, Hkv))
+    _gpu("seq_lens", seq_lens, _INT32, dev, (B,))
+    M = _table("page_table", page_table, B, dev)
+    host = None
+    if page_table_host is not None:
+        host = _host_table("page_table_host", page_table_host, (B, M))
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _gpu("o", o, dtype, dev, shape)
+    _int("window", window, 0)
+    return dev, dt, (B, n, Hq, Hkv, D, M, page, P), host, o
+
+
+def attention_tree(q, k_cache, v_cache, page_table, seq_lens, parents, scale=None, window: int = 0,
+                   o=None, workspace=None, page_table_host=None):
+    """Attention of a tree of n <= 64 drafted tokens of each sequence over its
+    cache.
+
+    q [B,n,Hq,D]; the drafts' keys and values are appended first, draft t at
+    place seq_lens[b] - n + t.  parents int32 [B,n] on the GPU: draft t follows
+    draft parents[b,t] < t, or the context (any other value, -1).  A draft
+    attends to the context and to the drafts on its way to it, itself included;
+    window W > 0: to the last W positions of that way.  workspace: a device
+    buffer of attention_workspace_bytes(...) bytes, allocated when not given.
+    Returns o [B,n,Hq,D].
+    """
+    dev, dt, (B, n, Hq, Hkv, D, M, page, P), host, o = _attend_args(
+        q, k_cache, v_cache, page_table, seq_lens, window, page_table_host, o)
+    _gpu("parents", parents, _INT32, dev, (B, n))
+    lib = _load()
+    if workspace is None:
+        workspace = _workspace(None, lib.gdr_attention_workspace_bytes(B, n, Hq, Hkv, D, M, page, 0),
+                               dev)
+    nbytes = _scratch(workspace, dev)
+    _call(dev, lib.gdr_attention_tree, dt, B, n, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
+          window, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+          _hp(host), M, page, P, seq_lens.data_ptr(), parents.data_ptr(), o.data_ptr(),
+          workspace.data_ptr(), nbytes)
+    return o
+
+
+def cache_accept(k_cache, v_cache, page_table, seq_lens, parents, leaf, scores=None, new_lens=None,
+                 path=None):
+    """Keep one way through each sequence's tree of n <= 64 drafts: the tokens
+    from the context to draft leaf[b] move, in place, to the places behind the
+    context (their scores too, when given), and the sequence ends there.
+
+    seq_lens int32 [B] with the drafts, parents int32 [B,n] as in
+    attention_tree, leaf int32 [B] (outside 0..n-1: nothing is kept), all on
+    the GPU.  Returns (new_lens int32 [B], path int32 [B,n]: the kept drafts,
+    then -1).  new_lens may be seq_lens itself.
+    """
+    dev, _, dt, (P, Hkv, page, D) = _cache(k_cache, v_cache, scores)
+    _gpu("seq_lens", seq_lens, _INT32, dev)
+    _need(seq_lens.dim() == 1, "seq_lens must be [B]")
+    B = seq_lens.shape[0]
+    _gpu("parents", parents, _INT32, dev)
+    _need(parents.dim() == 2 and parents.shape[0] == B, "parents must be [B,n]")
+    n = parents.shape[1]
+    _int("n", n, 0)
+    _gpu("leaf", leaf, _INT32, dev, (B,))
+    M = _table("page_table", page_table, B, dev)
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    else:
+        _gpu("new_lens", new_lens, _INT32, dev, (B,))
+    if path is None:
+        path = torch.empty((B, n), device=dev, dtype=_INT32)
+    else:
+        _gpu("path", path, _INT32, dev, (B, n))
+    _call(dev, _load().gdr_cache_accept, dt, B, n, Hkv, D, page_table.data_ptr(), M, page, P,
+          seq_lens.data_ptr(), parents.data_ptr(), leaf.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), _p(scores), new_lens.data_ptr(), path.data_ptr())
+    return new_lens, path
+
+
+def cache_resize(page_table, seq_lens, want, page_size: int, num_pages: int, new_lens=None,
+                 free=None, cu_seqlens=None):
+    """Make the page tables those of want[b] tokens in place of seq_lens[b],
+    in place: rows that shrink drop pages (-1), rows that grow get the
+    lowest-numbered pages that no row keeps, in their order, all that they ask
+    for or (then the row keeps its length) none.
+
+    page_table int32 [B,max_pages] with a row for every sequence that holds
+    pages of the num_pages there are; seq_lens, want int32 [B], all on the GPU.
+    cu_seqlens int32 [B+1], when given, receives the offsets of the tokens
+    that the rows grow by, for cache_append.  Returns (new_lens int32 [B],
+    free int32 [1]: the free pages left); new_lens may be seq_lens or want.  A
+    table of one column, with lengths 0 and 1, is a state pool's slot map.
+    """
+    if not (isinstance(page_table, _Tensor) and page_table.is_cuda):
+        _dense("page_table", page_table)
+    dev = page_table.device
+    _gpu("seq_lens", seq_lens, _INT32, dev)
+    _need(seq_lens.dim() == 1, "seq_lens must be [B]")
+    B = seq_lens.shape[0]
+    M = _table("page_table", page_table, B, dev)
+    _gpu("want", want, _INT32, dev, (B,))
+    _int("page_size", page_size, 1)
+    _int("num_pages", num_pages, 0)
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    else:
+        _gpu("new_lens", new_lens, _INT32, dev, (B,))
+    if free is None:
+        free = torch.empty(1, device=dev, dtype=_INT32)
+    else:
+        _gpu("free", free, _INT32, dev, (1,))
+    if cu_seqlens is not None:
+        _gpu("cu_seqlens", cu_seqlens, _INT32, dev, (B + 1,))
+    _call(dev, _load().gdr_cache_resize, B, M, page_size, num_pages, page_table.data_ptr(),
+          seq_lens.data_ptr(), want.data_ptr(), new_lens.data_ptr(), _p(cu_seqlens),
+          free.data_ptr())
+    return new_lens, free

@@ -43,6 +43,30 @@ __device__ inline Span seq_span(int len, int n, int window) {
     return Span{lo & ~31, len};
 }
 
+// A tree of drafts: draft t of a sequence follows draft parents[t] < t, or the
+// context.  Row t stands at position c + d, c the context's tokens and d the
+// drafts before it on its way, and attends to the context and to the drafts of
+// its way whose positions its window holds: one bit each, 64 at most.
+struct Way { unsigned long long drafts; int depth; };
+// By one wave, lane u for draft u: all lanes go up together, a step at a time
+// (trees are a few drafts deep).
+__device__ inline Way draft_way(const int32_t *parents, int n, int window) {
+    const int u = threadIdx.x & 63;
+    int up = u < n ? parents[u] : -1;
+    if (up >= u) up = -1;
+    Way y{1ull << u, 0};
+    int at = up < 0 ? -1 : up;
+    while (__builtin_amdgcn_ballot_w64(at >= 0)) {
+        const int next = __shfl(up, at & 63);
+        if (at >= 0) {
+            ++y.depth;
+            if (window == 0 || y.depth < window) y.drafts |= 1ull << at;
+            at = next < 0 ? -1 : next;
+        }
+    }
+    return y;
+}
+
 // How the cached tokens are shared out.  Every sequence's span is cut into
 // chunks of about C tokens, the same C for all, so that a long sequence among
 // short ones is spread over as many workgroups as its length asks for; C
@@ -637,7 +661,8 @@ template <int D> struct Tile<float, D, 16> {
 // padded rather than exchanged: with a 16-byte chunk's place depending on its
 // row by an exclusive or, the addresses alone took so many registers that 34
 // others were spilled, 62 us.)
-template <typename T, int D, int RW, int RT, bool STREAM>
+// TREE: the rows are drafts of a tree.
+template <typename T, int D, int RW, int RT, bool STREAM, bool TREE>
 __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     using TL = Tile<T, D, RW>;
     constexpr int PER = TL::PER, kBlocks = TL::kBlocks, kTile = TL::kTile, kVals = TL::kVals;
@@ -669,17 +694,35 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     // this lane's query row and what it attends to
     const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + RW * rt + r;
     Span sp{0, 0};
+    const int ctx = len - a.n;                  // TREE: the context's tokens
+    unsigned long long drafts = 0;
     typename TL::Q q;
     {
         const size_t qb = (size_t)b * a.n * a.Hq * D;
         const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + qb, 0xFFFFFFFFu);
         const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0;
-        if (row < rows) sp = token_span(len, a.n, a.window, t);
+        if constexpr (TREE) {
+            // (a place's span, but its lower end from the position)
+            const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
+            const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
+            const int depth = __shfl(y.depth, t);
+            drafts = (unsigned long long)hi << 32 | lo;
+            if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
+        } else {
+            if (row < rows) sp = token_span(len, a.n, a.window, t);
+        }
         TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + hg) * (D * (unsigned)sizeof(T)), lane);
         if (k.negative) TL::negate(q);
     }
-    // the block's tokens: what its rows attend to, within the slot
-    const Span first = token_span(len, a.n, a.window, row0 / a.G);
+    auto attends = [&](int j) {
+        bool in = j >= sp.lo && j < sp.hi;
+        if constexpr (TREE) in = in && (j < ctx || (drafts >> ((j - ctx) & 63) & 1));
+        return in;
+    };
+    // the block's tokens: what its rows attend to, within the slot (TREE: at
+    // most; a draft's position is that of its place or before)
+    const Span first = TREE ? Span{token_span(len, a.n, a.window, 0).lo, ctx}
+                            : token_span(len, a.n, a.window, row0 / a.G);
     const Span last = token_span(len, a.n, a.window,
                                  ((row0 + kRows < rows ? row0 + kRows : rows) - 1) / a.G);
     const int c_lo = seq.lo + (slot - sl_.first) * sl_.chunk;
@@ -720,7 +763,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
             for (int i = 0; i < kVals; ++i) {
                 const int j = j0 + TL::key(i, g);
-                x[i] = here[TL::block(i)] && j >= sp.lo && j < sp.hi ? x[i] : -INFINITY;
+                x[i] = here[TL::block(i)] && attends(j) ? x[i] : -INFINITY;
             }
         }
 #pragma unroll
@@ -749,7 +792,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 #pragma unroll
             for (int i = 0; i < kVals; ++i) {
                 const int j = j0 + TL::key(i, g);
-                in[i] = j >= sp.lo && j < sp.hi ? 1.f : 0.f;
+                in[i] = attends(j) ? 1.f : 0.f;
             }
             const typename TL::Ones ones = TL::ones(in);
 #pragma unroll
@@ -1135,7 +1178,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KArgs k, int join_wgs, l
     }
 }
 
-template <typename T, int D, int RW, int RT>
+template <typename T, int D, int RW, int RT, bool TREE>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
     constexpr int kRows = RW * RT;
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
@@ -1162,8 +1205,8 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     }
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
-    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, RT, true><<<grid, kThreads, 0, s>>>(k);
-    else                        attn_kernel<T, D, RW, RT, false><<<grid, kThreads, 0, s>>>(k);
+    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, RT, true, TREE><<<grid, kThreads, 0, s>>>(k);
+    else                        attn_kernel<T, D, RW, RT, false, TREE><<<grid, kThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // about 4,096 workgroups join, and at most one per row: sequences in one
@@ -1180,14 +1223,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int D>
+template <int D, bool TREE>
 hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
-    if (!bf16_io) return launch<float, D, 16, 1>(a, s);
+    if (!bf16_io) return launch<float, D, 16, 1, TREE>(a, s);
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
     switch (block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window)) {
-    case 16: return launch<bf16, D, 16, 1>(a, s);
-    case 32: return launch<bf16, D, 32, 1>(a, s);
-    default: return launch<bf16, D, 32, 2>(a, s);
+    case 16: return launch<bf16, D, 16, 1, TREE>(a, s);
+    case 32: return launch<bf16, D, 32, 1, TREE>(a, s);
+    default: return launch<bf16, D, 32, 2, TREE>(a, s);
     }
 }
 
@@ -1207,7 +1250,11 @@ size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capac
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
-    return D == 128 ? launch_d<128>(bf16_io, a, s) : launch_d<64>(bf16_io, a, s);
+    return D == 128 ? launch_d<128, false>(bf16_io, a, s) : launch_d<64, false>(bf16_io, a, s);
+}
+
+hipError_t launch_attention_tree(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
+    return D == 128 ? launch_d<128, true>(bf16_io, a, s) : launch_d<64, true>(bf16_io, a, s);
 }
 
 }  // namespace gdr

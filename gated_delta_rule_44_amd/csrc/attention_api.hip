@@ -6,23 +6,26 @@
 
 #include "../../include/gdr_attention.h"
 #include "api_util.h"
+#include "cache_check.h"
+#include "cache_internal.h"
 #include "prompt_internal.h"
 
 namespace {
 
 using gdr::aligned16;
+using gdr::aligned4;
+using gdr::check_cache;
+using gdr::check_table;
 using gdr::check_workspace;
 using gdr::fail;
 using gdr::finish;
+using gdr::kMaxPairs;
+using gdr::kMaxQueryRows;
+using gdr::page_shift_of;
+using gdr::reaches;
 
-bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
-
-#define REQUIRE_I32(p, name)                                                       \
-    do {                                                                           \
-        if (!(p)) return fail(GDR_EINVAL, "%s: %s is NULL", what, name);           \
-        if (!aligned4(p)) return fail(GDR_EINVAL, "%s: %s is not 4-byte aligned",  \
-                                      what, name);                                 \
-    } while (0)
+// a tree's drafts are bits of a word
+constexpr int kMaxDrafts = 64;
 
 gdr_status check_heads(const char *what, int dt, int Hq, int Hkv, int D, float scale, int window) {
     if (dt != GDR_F32 && dt != GDR_BF16)
@@ -149,6 +152,123 @@ gdr_status gdr_attention_backward(enum gdr_dtype dt, int B, int T, int T_total, 
     a.d_o = d_o; a.dq = dq; a.dk = dk; a.dv = dv; a.ws = workspace;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return finish(gdr::launch_attention_backward(dt == GDR_BF16, D, a, s), s, what);
+}
+
+gdr_status gdr_attention_tree(enum gdr_dtype dt, int B, int n_tok, int Hq, int Hkv, int D,
+                              float scale, int window, const void *q, const void *k_cache,
+                              const void *v_cache, const int32_t *page_table,
+                              const int32_t *page_table_host, int max_pages, int page_size,
+                              int num_pages, const int32_t *seq_lens, const int32_t *parents,
+                              void *o, void *workspace, size_t ws_bytes, void *stream) {
+    const char *what = "gdr_attention_tree";
+    gdr_status st = check_cache(what, dt, B, Hkv, D, max_pages, page_size, num_pages);
+    if (st == GDR_OK) st = check_heads(what, dt, Hq, Hkv, D, scale, window);
+    if (st != GDR_OK) return st;
+    if (n_tok < 0 || n_tok > kMaxDrafts)
+        return fail(n_tok < 0 ? GDR_EINVAL : GDR_EUNSUPPORTED, "%s: n_tok = %d drafts; 0 to %d", what,
+                    n_tok, kMaxDrafts);
+    if (reaches(B, n_tok, Hq, kMaxQueryRows))
+        return fail(GDR_EUNSUPPORTED, "%s: %d x %d x %d query rows exceed %lld", what, B, n_tok, Hq,
+                    kMaxQueryRows);
+    if (page_table_host) {
+        st = check_table(what, "page_table", page_table_host, B, max_pages, num_pages, nullptr);
+        if (st != GDR_OK) return st;
+    }
+    if (B == 0 || n_tok == 0) return GDR_OK;
+    REQUIRE_PTR(q, "q");
+    REQUIRE_PTR(o, "o");
+    REQUIRE_I32(seq_lens, "seq_lens");
+    REQUIRE_I32(parents, "parents");
+    if (max_pages > 0) REQUIRE_I32(page_table, "page_table");
+    if (num_pages > 0) {
+        REQUIRE_PTR(k_cache, "k_cache");
+        REQUIRE_PTR(v_cache, "v_cache");
+    }
+    st = check_workspace(what, workspace, ws_bytes,
+                         gdr_attention_workspace_bytes(B, n_tok, Hq, Hkv, D, max_pages, page_size, 0));
+    if (st != GDR_OK) return st;
+    gdr::AttnArgs a{};
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+    // without pages every token is absent: the kernels see empty sequences
+    a.map = gdr::PageMap{page_table, num_pages > 0 ? max_pages : 0, page_shift_of(page_size),
+                         num_pages};
+    a.seq_lens = seq_lens; a.parents = parents; a.o = o; a.ws = workspace;
+    a.B = B; a.n = n_tok; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    a.scale = scale; a.window = window;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return finish(gdr::launch_attention_tree(dt == GDR_BF16, D, a, s), s, what);
+}
+
+gdr_status gdr_cache_accept(enum gdr_dtype dt, int B, int n_tok, int Hkv, int D,
+                            const int32_t *page_table, int max_pages, int page_size,
+                            int num_pages, const int32_t *seq_lens, const int32_t *parents,
+                            const int32_t *leaf, void *k_cache, void *v_cache, float *scores,
+                            int32_t *new_lens, int32_t *path, void *stream) {
+    const char *what = "gdr_cache_accept";
+    const gdr_status st = check_cache(what, dt, B, Hkv, D, max_pages, page_size, num_pages);
+    if (st != GDR_OK) return st;
+    if (n_tok < 0 || n_tok > kMaxDrafts)
+        return fail(n_tok < 0 ? GDR_EINVAL : GDR_EUNSUPPORTED, "%s: n_tok = %d drafts; 0 to %d", what,
+                    n_tok, kMaxDrafts);
+    if ((long long)B * Hkv >= kMaxPairs)
+        return fail(GDR_EUNSUPPORTED, "%s: %lld (sequence, head) pairs exceed %lld", what,
+                    (long long)B * Hkv, kMaxPairs);
+    if (B == 0) return GDR_OK;
+    REQUIRE_I32(seq_lens, "seq_lens");
+    REQUIRE_I32(leaf, "leaf");
+    REQUIRE_I32(new_lens, "new_lens");
+    if (n_tok > 0) {
+        REQUIRE_I32(parents, "parents");
+        REQUIRE_I32(path, "path");
+    }
+    if (max_pages > 0) REQUIRE_I32(page_table, "page_table");
+    if (num_pages > 0) {
+        REQUIRE_PTR(k_cache, "k_cache");
+        REQUIRE_PTR(v_cache, "v_cache");
+    }
+    REQUIRE_ALIGNED_OR_NULL(scores, "scores");
+    gdr::AcceptArgs a{};
+    a.k_cache = k_cache; a.v_cache = v_cache; a.scores = scores;
+    a.map = gdr::PageMap{page_table, max_pages, page_shift_of(page_size), num_pages};
+    a.seq_lens = seq_lens; a.parents = parents; a.leaf = leaf;
+    a.new_lens = new_lens; a.path = path;
+    a.B = B; a.n = n_tok; a.Hkv = Hkv;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return finish(gdr::launch_cache_accept(D * (dt == GDR_BF16 ? 2 : 4), a, s), s, what);
+}
+
+gdr_status gdr_cache_resize(int B, int max_pages, int page_size, int num_pages,
+                            int32_t *page_table, const int32_t *seq_lens, const int32_t *want,
+                            int32_t *new_lens, int32_t *cu_seqlens, int32_t *free_pages,
+                            void *stream) {
+    const char *what = "gdr_cache_resize";
+    if (B < 0 || max_pages < 0 || page_size < 1 || num_pages < 0)
+        return fail(GDR_EINVAL, "%s: bad sizes B=%d max_pages=%d page_size=%d num_pages=%d", what, B,
+                    max_pages, page_size, num_pages);
+    if (num_pages > gdr::kMaxPages)
+        return fail(GDR_EUNSUPPORTED, "%s: %d pages exceed %d", what, num_pages, gdr::kMaxPages);
+    if ((long long)max_pages * page_size >= (1LL << 30))
+        return fail(GDR_EUNSUPPORTED, "%s: a table of %d pages of %d tokens is too long", what,
+                    max_pages, page_size);
+    // (sums of lengths are 32-bit numbers)
+    if (B >= (1 << 30) || ((long long)num_pages + B) * page_size >= (1LL << 31))
+        return fail(GDR_EUNSUPPORTED, "%s: %d pages of %d tokens and %d sequences are too many", what,
+                    num_pages, page_size, B);
+    if (B > 0) {
+        if (max_pages > 0) REQUIRE_I32(page_table, "page_table");
+        REQUIRE_I32(seq_lens, "seq_lens");
+        REQUIRE_I32(want, "want");
+        REQUIRE_I32(new_lens, "new_lens");
+    }
+    if (cu_seqlens) REQUIRE_I32(cu_seqlens, "cu_seqlens");
+    if (free_pages) REQUIRE_I32(free_pages, "free_pages");
+    if (B == 0 && !cu_seqlens && !free_pages) return GDR_OK;
+    gdr::ResizeArgs a{};
+    a.table = page_table; a.seq_lens = seq_lens; a.want = want; a.new_lens = new_lens;
+    a.cu_seqlens = cu_seqlens; a.free_pages = free_pages;
+    a.B = B; a.max_pages = max_pages; a.page_size = page_size; a.num_pages = num_pages;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return finish(gdr::launch_cache_resize(a, s), s, what);
 }
 
 }  // extern "C"

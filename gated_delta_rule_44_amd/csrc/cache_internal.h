@@ -60,10 +60,13 @@ struct AttnArgs {
     int B, n, Hq, Hkv, G;        // G = Hq / Hkv
     float scale;
     int window;                  // 0: none
+    const int32_t *parents;      // [B, n]: a tree of drafts; nullptr: a chain
 };
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
                            bool with_scores);
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s);
+// drafts of a tree (a.parents), 64 of a sequence at most; no scores
+hipError_t launch_attention_tree(bool bf16_io, int D, const AttnArgs &a, hipStream_t s);
 
 struct EvictArgs {
     void *k_cache, *v_cache;
@@ -78,5 +81,30 @@ struct EvictArgs {
 };
 size_t evict_workspace(int pairs, long long capacity);
 hipError_t launch_cache_evict(int row_bytes, const EvictArgs &a, hipStream_t s);
+
+struct AcceptArgs {
+    void *k_cache, *v_cache;
+    float *scores;               // or nullptr
+    PageMap map;
+    const int32_t *seq_lens;     // [B]
+    const int32_t *parents;      // [B, n]
+    const int32_t *leaf;         // [B]
+    int32_t *new_lens;           // [B]
+    int32_t *path;               // [B, n]
+    int B, n, Hkv;
+    bool ends;                   // the moves' launch writes new_lens and path as well
+};
+hipError_t launch_cache_accept(int row_bytes, const AcceptArgs &a, hipStream_t s);
+
+constexpr int kMaxPages = 1 << 20;   // of a resize
+struct ResizeArgs {
+    int32_t *table;              // [B, max_pages]
+    const int32_t *seq_lens, *want;
+    int32_t *new_lens;           // [B]
+    int32_t *cu_seqlens;         // [B+1] or nullptr
+    int32_t *free_pages;         // [1] or nullptr
+    int B, max_pages, page_size, num_pages;
+};
+hipError_t launch_cache_resize(const ResizeArgs &a, hipStream_t s);
 
 }  // namespace gdr

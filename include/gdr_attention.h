@@ -1,7 +1,9 @@
 /*
  * gdr_attention.h -- the attention layers of a placement beside the decode
  * over their cache (gdr_cache.h): the attention of whole prompts and its
- * gradients (MI355X, gfx950).
+ * gradients, the attention of a tree of drafted tokens over the cache, what is
+ * kept of such a tree, and the page tables that follow the requests' lengths
+ * (MI355X, gfx950).
  *
  * The conventions of gdr.h and gdr_cache.h hold here as well (device pointers,
  * dense row-major tensors, 16-byte alignment -- page tables, lengths, offsets
@@ -100,6 +102,96 @@ gdr_status gdr_attention_backward(enum gdr_dtype dt, int B, int T, int T_total, 
                                   const int32_t *cu_seqlens_host, const void *o,
                                   const float *lse, const void *d_o, void *dq, void *dk,
                                   void *dv, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache.  The n_tok newest
+ * tokens of sequence b (places seq_lens[b] - n_tok .. seq_lens[b] - 1, keys
+ * and values appended first) are a forest: draft t follows draft
+ * parents[b, t] < t, or the context where parents[b, t] is anything else (-1).
+ * With c = seq_lens[b] - n_tok the context's tokens, d(t) the number of
+ * drafts before t on its way to the context, and the position p = c + d(t),
+ * row t attends to
+ *     the context's tokens j < c, j > p - window if window > 0, and
+ *     the places c + u of the drafts u on its way, itself included, whose
+ *     positions are above p - window if window > 0,
+ * as far as they are at 0 or above and on a present page.  (A chain, parents
+ * t - 1, is gdr_attention_decode.)  Everything else is as there: the softmax,
+ * rows without tokens, absent pages, the numerics, the workspace
+ * (gdr_attention_workspace_bytes, without scores).
+ *
+ *   n_tok        drafts per sequence, 0..64 (a smaller tree is padded with
+ *                drafts that follow the context)
+ *   parents      device int32 [B, n_tok]
+ */
+gdr_status gdr_attention_tree(enum gdr_dtype dt, int B, int n_tok, int Hq, int Hkv, int D,
+                              float scale, int window, const void *q, const void *k_cache,
+                              const void *v_cache, const int32_t *page_table,
+                              const int32_t *page_table_host, int max_pages, int page_size,
+                              int num_pages, const int32_t *seq_lens, const int32_t *parents,
+                              void *o, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Keep one way through each sequence's tree of drafts: the tokens from the
+ * context to draft leaf[b] take the places behind the context, in their
+ * order, and the sequence ends there.
+ *
+ *   n_tok, seq_lens, parents
+ *                as in gdr_attention_tree (seq_lens with the drafts)
+ *   leaf         device int32 [B]: the last draft kept; a value outside
+ *                0..n_tok-1 (-1) keeps none
+ *   scores       NULL, or the accumulated weights, moved along
+ *   new_lens     device int32 [B]: max(seq_lens[b] - n_tok, 0) + the kept
+ *                drafts that have a place (written); may be seq_lens itself
+ *   path         device int32 [B, n_tok]: the kept drafts from the context
+ *                on, -1 past them (written)
+ *
+ * Lengths are clamped as in gdr_attention_decode; drafts at places below 0
+ * (a sequence shorter than n_tok) are not kept.  The pages of the drafts
+ * belong to one sequence each.  A token whose old or new page is absent is
+ * not moved.  Places past the new length keep their bytes.
+ */
+gdr_status gdr_cache_accept(enum gdr_dtype dt, int B, int n_tok, int Hkv, int D,
+                            const int32_t *page_table, int max_pages, int page_size,
+                            int num_pages, const int32_t *seq_lens, const int32_t *parents,
+                            const int32_t *leaf, void *k_cache, void *v_cache, float *scores,
+                            int32_t *new_lens, int32_t *path, void *stream);
+
+/*
+ * Page tables that follow the sequences' lengths.  Sequence b holds
+ * seq_lens[b] tokens, on the pages of the first ceil(seq_lens[b] / page_size)
+ * columns of its row; the call makes them the pages of want[b] tokens.  The
+ * tables are all there is: a page is free if no row keeps it, so that every
+ * sequence that holds pages has to have a row (one that is not to change asks
+ * for what it has), and pages that several sequences share stay while one of
+ * them keeps them.
+ *   * A row that shrinks drops its entries past the new length (-1), and
+ *     their pages are free if no other row keeps them.
+ *   * Rows that grow are served in their order, their new columns in theirs,
+ *     with the free pages from the lowest number up.  A row is served in full
+ *     or not at all: it is if the pages asked for by the rows up to it
+ *     (itself included, served or not) are at most the free ones.
+ *   * new_lens[b] = want[b], or seq_lens[b] for a row that is not served.
+ * A table of one column whose rows hold 0 or 1 tokens is a slot map of a
+ * state pool (gdr_decode_tokens, gdr_prefill_varlen_pool).
+ *
+ *   max_pages    columns of page_table
+ *   page_size    tokens of a page (>= 1)
+ *   num_pages    pages there are, 0..2^20 (GDR_EUNSUPPORTED above, and for
+ *                (num_pages + B) * page_size >= 2^31 tokens)
+ *   page_table   device int32 [B, max_pages] (read and written)
+ *   seq_lens, want  device int32 [B], clamped to 0..max_pages * page_size
+ *   new_lens     device int32 [B] (written); may be seq_lens or want
+ *   cu_seqlens   NULL, or device int32 [B+1] (written): where the tokens that
+ *                the rows grow by lie in a packed batch (sums of max(0,
+ *                new_lens[b] - seq_lens[b])), for gdr_cache_append with start
+ *                = seq_lens
+ *   free_pages   NULL, or device int32 [1] (written): free pages after the
+ *                call
+ */
+gdr_status gdr_cache_resize(int B, int max_pages, int page_size, int num_pages,
+                            int32_t *page_table, const int32_t *seq_lens, const int32_t *want,
+                            int32_t *new_lens, int32_t *cu_seqlens, int32_t *free_pages,
+                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -36,7 +36,9 @@ def hp(a):
 def test_library_exports_every_declared_symbol():
     src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(gdr_[a-z_]+)\s*\(", src)))
-    assert "gdr_attention_prefill" in names and "gdr_attention_backward" in names
+    assert names == ["gdr_attention_backward", "gdr_attention_backward_workspace_bytes",
+                     "gdr_attention_prefill", "gdr_attention_tree", "gdr_cache_accept",
+                     "gdr_cache_resize"]
     for name in names:
         assert hasattr(ctypes.CDLL(gdr.lib_path()), name), name
 
@@ -133,3 +135,98 @@ def test_binding_rejects_host_tensors():
         gdr.attention_prefill(q, q, q)
     with pytest.raises(gdr.GdrError, match="q must be a GPU tensor"):
         gdr.attention_backward(q, q, q, q, q, q)
+
+
+def tree(lib, dt=1, B=2, n=3, Hq=4, Hkv=2, D=128, scale=1.0, window=0, q=FAKE, kc=FAKE, vc=FAKE,
+         table=FAKE, host=None, M=4, page=16, P=9, lens=FAKE, parents=FAKE, o=FAKE, ws=FAKE,
+         ws_bytes=1 << 40):
+    return lib.gdr_attention_tree(dt, B, n, Hq, Hkv, D, F(scale), window, q, kc, vc, table, hp(host),
+                                  M, page, P, lens, parents, o, ws, ws_bytes, None)
+
+
+def accept(lib, dt=1, B=2, n=3, Hkv=2, D=128, table=FAKE, M=4, page=16, P=9, lens=FAKE,
+           parents=FAKE, leaf=FAKE, kc=FAKE, vc=FAKE, sc=None, new_lens=FAKE, path=FAKE):
+    return lib.gdr_cache_accept(dt, B, n, Hkv, D, table, M, page, P, lens, parents, leaf, kc, vc, sc,
+                                new_lens, path, None)
+
+
+def resize(lib, B=2, M=4, page=16, P=9, table=FAKE, lens=FAKE, want=FAKE, new_lens=FAKE, cu=None,
+           free=None):
+    return lib.gdr_cache_resize(B, M, page, P, table, lens, want, new_lens, cu, free, None)
+
+
+CACHE = [
+    (dict(dt=5), EINVAL, "dtype"),
+    (dict(D=96), EUNSUPPORTED, "supported widths"),
+    (dict(B=-1), EINVAL, "bad sizes"),
+    (dict(Hkv=0), EINVAL, "bad sizes"),
+    (dict(M=-1), EINVAL, "bad sizes"),
+    (dict(P=-1), EINVAL, "bad sizes"),
+    (dict(page=8), EUNSUPPORTED, "page_size"),
+    (dict(M=1 << 22, page=256), EUNSUPPORTED, "too long"),
+    (dict(P=1 << 30), EUNSUPPORTED, "too large"),
+    (dict(n=-1), EINVAL, "-1 drafts"),
+    (dict(n=65), EUNSUPPORTED, "65 drafts; 0 to 64"),
+    (dict(table=None), EINVAL, "page_table is NULL"),
+    (dict(table=MIS), EINVAL, "page_table is not 4-byte aligned"),
+    (dict(kc=None), EINVAL, "k_cache is NULL"),
+    (dict(vc=MIS), EINVAL, "v_cache is not 16-byte aligned"),
+    (dict(lens=None), EINVAL, "seq_lens is NULL"),
+    (dict(parents=MIS), EINVAL, "parents is not 4-byte aligned"),
+]
+
+
+@pytest.mark.parametrize("kw,code,msg", CACHE + [
+    (dict(Hq=5), EINVAL, "not a multiple"),
+    (dict(scale=float("nan")), EINVAL, "scale"),
+    (dict(window=-1), EINVAL, "window"),
+    (dict(B=1 << 17, n=64), EUNSUPPORTED, "query rows"),
+    (dict(q=None), EINVAL, "q is NULL"),
+    (dict(o=MIS), EINVAL, "o is not 16-byte aligned"),
+    (dict(ws=None), EINVAL, "workspace"),
+    (dict(ws_bytes=1), EINVAL, "workspace"),
+    (dict(host=[[0, 1, 2, 9], [3, 4, 5, -1]]), EINVAL, "page_table[0, 3] = 9 outside -1..8"),
+])
+def test_tree_rejects(lib, kw, code, msg):
+    assert tree(lib, **kw) == code
+    assert msg in err(lib)
+
+
+@pytest.mark.parametrize("kw,code,msg", CACHE + [
+    (dict(sc=MIS), EINVAL, "scores is not 16-byte aligned"),
+    (dict(B=1 << 20), EUNSUPPORTED, "pairs exceed"),
+    (dict(leaf=None), EINVAL, "leaf is NULL"),
+    (dict(new_lens=None), EINVAL, "new_lens is NULL"),
+    (dict(path=MIS), EINVAL, "path is not 4-byte aligned"),
+])
+def test_accept_rejects(lib, kw, code, msg):
+    assert accept(lib, **kw) == code
+    assert msg in err(lib)
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(B=-1), EINVAL, "bad sizes"),
+    (dict(M=-1), EINVAL, "bad sizes"),
+    (dict(page=0), EINVAL, "bad sizes"),
+    (dict(P=-1), EINVAL, "bad sizes"),
+    (dict(P=(1 << 20) + 1), EUNSUPPORTED, "pages exceed"),
+    (dict(M=1 << 26), EUNSUPPORTED, "too long"),
+    (dict(P=1 << 20, page=1 << 11, M=2), EUNSUPPORTED, "too many"),
+    (dict(B=1 << 30), EUNSUPPORTED, "too many"),
+    (dict(table=None), EINVAL, "page_table is NULL"),
+    (dict(lens=MIS), EINVAL, "seq_lens is not 4-byte aligned"),
+    (dict(want=None), EINVAL, "want is NULL"),
+    (dict(new_lens=None), EINVAL, "new_lens is NULL"),
+    (dict(cu=MIS), EINVAL, "cu_seqlens is not 4-byte aligned"),
+    (dict(free=MIS), EINVAL, "free_pages is not 4-byte aligned"),
+])
+def test_resize_rejects(lib, kw, code, msg):
+    assert resize(lib, **kw) == code
+    assert msg in err(lib)
+
+
+def test_empty_draft_calls_are_ok_without_gpu(lib):
+    assert tree(lib, B=0) == 0
+    assert tree(lib, n=0) == 0
+    assert accept(lib, B=0) == 0
+    assert resize(lib, B=0, table=None, lens=None) == 0
