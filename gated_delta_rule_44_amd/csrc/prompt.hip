@@ -121,13 +121,9 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
                     x[b][e] = exp2_(fmaf(x[b][e], k.c, -mc));
                     l += x[b][e];
                 }
-            if (CLEAR && !full) {
 #pragma unroll
-                for (int b = 0; b < kBlk; ++b) R::template cols<CLEAR>(acc, vt, b, at, R::operand(x[b]));
-            } else {
-#pragma unroll
-                for (int b = 0; b < kBlk; ++b) R::template cols<false>(acc, vt, b, at, R::operand(x[b]));
-            }
+            for (int b = 0; b < kBlk; ++b)
+                R::template cols<CLEAR>(acc, vt, b, at, R::operand(x[b]), full);
         }
     };
     walk(std::false_type{});

@@ -41,7 +41,7 @@ template <typename T> __device__ inline float dot_part(const T *x, const T *y, i
 
 // Workgroup = (block of 128 rows, query head), 32 rows a wave.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 128 ? 1 : 2)) void query_kernel(KArgs k) {
+__global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) void query_kernel(KArgs k) {
     using R = Rows<T, D>;
     constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols;
     __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
@@ -115,8 +115,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 128 ? 1 : 2)) vo
                     for (int e = 0; e < 16; ++e)
                         x[e] = attends(j0 + 32 * b + R::key(e, h)) ? x[e] : 0.f;
                 }
-                if (CLEAR && !full) R::template cols<CLEAR>(acc, kt, b, at, R::operand(x));
-                else                R::template cols<false>(acc, kt, b, at, R::operand(x));
+                R::template cols<CLEAR>(acc, kt, b, at, R::operand(x), full);
             }
         }
     };
@@ -211,13 +210,8 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
                         dp[e] = in ? dp[e] : 0.f;
                     }
                 }
-                if (CLEAR && !full) {
-                    R::template cols<CLEAR>(dv, gt, b, at, R::operand(x));
-                    R::template cols<CLEAR>(dk, qt, b, at, R::operand(dp));
-                } else {
-                    R::template cols<false>(dv, gt, b, at, R::operand(x));
-                    R::template cols<false>(dk, qt, b, at, R::operand(dp));
-                }
+                R::template cols<CLEAR>(dv, gt, b, at, R::operand(x), full);
+                R::template cols<CLEAR>(dk, qt, b, at, R::operand(dp), full);
             }
         }
     };
@@ -227,6 +221,144 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     const size_t to = ((size_t)(bl.row0 + j) * a.Hkv + hk) * D;
     R::store(static_cast<T *>(a.dk) + to, dk, h, a.scale);
     R::store(static_cast<T *>(a.dv) + to, dv, h, 1.f);
+}
+
+// The same in bf16, by pairs of waves: both waves of a pair hold the same 32
+// tokens' k and v, each forms w and ds for one half of a tile's 64 rows, and
+// one of them sums dv, the other dk, over all 64; what a wave has for the other
+// one (w or ds of its half) passes through LDS as the operand that it is.  A
+// wave then has 64 accumulators instead of 128, and two waves share a SIMD:
+// one's exponentials run under the other's products.  A tile's sums are formed
+// while the next one's w and ds are, so that one barrier a tile orders all.
+template <int D>
+__global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
+    typedef bf16 T;
+    using R = Rows<T, D>;
+    constexpr int kTok = R::kTok, kCols = R::kCols;
+    static_assert(kTok == 64, "a half of the rows each");
+    __shared__ __align__(1024) char lds[3][2][R::kTileBytes];
+    __shared__ __align__(16) bf16x8 given[2][2][kWaves][2][64];   // [n & 1][role][pair]
+    __shared__ __align__(16) float stats[3][2][kTok];
+    const PromptArgs &a = k.a;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int w = uniform(tid >> 6), pair = w % kWaves, role = w / kWaves;
+    const int hk = blockIdx.x % a.Hkv;
+    const Block bl = find_block<kRows>(a, blockIdx.x / a.Hkv);
+    if (bl.i < 0) return;
+    const int j0 = bl.i * kRows, jw = j0 + 32 * pair, j = jw + r;
+    const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
+    const typename R::At at = R::at(lane);
+
+    typename R::B kf, vf;
+    const int row = bl.row0 + (j < bl.len ? j : bl.len - 1);
+    R::load(kf, static_cast<const T *>(a.k) + ((size_t)row * a.Hkv + hk) * D, h);
+    R::load(vf, static_cast<const T *>(a.v) + ((size_t)row * a.Hkv + hk) * D, h);
+    const int over = a.window > 0 && bl.len - j0 > kRows + a.window - 1 ? j0 + kRows + a.window - 1
+                                                                         : bl.len;
+    const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
+
+    auto stage = [&](int n) {
+        const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
+        const size_t first = (size_t)bl.row0 + t * kTok;
+        const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
+        const T *gh = static_cast<const T *>(a.d_o) + (size_t)head * D;
+        fetch<T, D, 2 * kWaves, kTok>(lds[n % 3][0], qh, first, left, qpitch, w, lane);
+        fetch<T, D, 2 * kWaves, kTok>(lds[n % 3][1], gh, first, left, qpitch, w, lane);
+        if (w < 2) {
+            const int at_row = lane < left ? lane : left - 1;
+            fetch_words<kTok>(stats[n % 3][w], (w ? k.delta : k.lse2) + (size_t)head * a.T_total + first,
+                              at_row, lane);
+        }
+    };
+    f32x16 acc[kCols];
+    typename R::P kept;                      // this wave's half of tile n, for its own sums
+    // each of 32 rows from i on attends to all of the pair's tokens
+    auto whole = [&](int i) {
+        return i >= jw + 31 && i + 32 <= bl.len && (a.window == 0 || i + 31 < jw + a.window);
+    };
+    // w and ds of this wave's half of tile n; between() is what may run under
+    // the last of this
+    auto weights = [&](int n, auto between) {
+        const int i0 = (t0 + n % tiles) * kTok + 32 * role;
+        const char *qt = lds[n % 3][0] + 32 * role * R::kRowBytes, *gt = qt + R::kTileBytes;
+        const float *lse2 = stats[n % 3][0] + 32 * role, *delta = lse2 + kTok;
+        f32x16 x = R::rows(qt, 0, at, kf);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x16 dp = R::rows(gt, 0, at, vf);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse2 + R::key(e, h));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[e + u] = exp2_(fmaf(x[e + u], k.c, -ls[u]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        between();
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 de = *reinterpret_cast<const f32x4 *>(delta + R::key(e, h));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dp[e + u] = x[e + u] * (dp[e + u] - de[u]);
+        }
+        if (!whole(i0)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = i0 + R::key(e, h);
+                const bool in = j <= i && i < bl.len && (a.window == 0 || j > i - a.window);
+                x[e] = in ? x[e] : 0.f;
+                dp[e] = in ? dp[e] : 0.f;
+            }
+        }
+        const typename R::P p = R::operand(x), ds = R::operand(dp);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            given[n & 1][role][pair][u][lane] = role ? p.f[u] : ds.f[u];
+            kept.f[u] = role ? ds.f[u] : p.f[u];
+        }
+    };
+    // dv (role 0) or dk (role 1) of tile n, by this wave's half of it (mine) or
+    // the other's
+    auto sums = [&](int n, auto clear, const typename R::P &mine) {
+        const bool all = whole((t0 + n % tiles) * kTok + 32 * role);
+        R::template cols<decltype(clear)::value>(
+            acc, lds[n % 3][1 - role] + 32 * role * R::kRowBytes, 0, at, mine, all);
+    };
+    auto other_sums = [&](int n, auto clear) {
+        const bool all = whole((t0 + n % tiles) * kTok + 32 * (1 - role));
+        typename R::P p;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) p.f[u] = given[n & 1][1 - role][pair][u][lane];
+        R::template cols<decltype(clear)::value>(
+            acc, lds[n % 3][1 - role] + 32 * (1 - role) * R::kRowBytes, 0, at, p, all);
+    };
+    auto walk = [&](auto clear) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
+        stage(0);
+        R::settle(kf);
+        R::settle(vf);
+        tile_landed();
+        if (all > 1) stage(1);
+        weights(0, []() {});
+        for (int n = 1; n < all; ++n) {
+            tile_landed();
+            if (n + 1 < all) stage(n + 1);
+            const typename R::P mine = kept;
+            weights(n, [&]() { sums(n - 1, clear, mine); });
+            __builtin_amdgcn_sched_barrier(0);
+            other_sums(n - 1, clear);
+        }
+        __syncthreads();
+        sums(all - 1, clear, kept);
+        other_sums(all - 1, clear);
+    };
+    walk(std::false_type{});
+    if (__syncthreads_or(R::any_odd(acc))) walk(std::true_type{});
+    if (j >= bl.len) return;
+    const size_t to = ((size_t)(bl.row0 + j) * a.Hkv + hk) * D;
+    if (role) R::store(static_cast<T *>(a.dk) + to, acc, h, a.scale);
+    else      R::store(static_cast<T *>(a.dv) + to, acc, h, 1.f);
 }
 
 template <typename T, int D>
@@ -241,7 +373,10 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
+    if constexpr (sizeof(T) == 2)
+        key_pairs_kernel<D><<<(unsigned)(blocks * a.Hkv), 2 * kThreads, 0, s>>>(k);
+    else
+        key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
 

@@ -177,16 +177,16 @@ template <int D> struct Rows<bf16, D> {
                    ((w[i] & 0x7F800000u) == 0x7F800000u ? 0u : w[i] & 0xFFFF0000u);
         return __builtin_bit_cast(bf16x8, w);
     }
-    // CLEAR: without the tile's infinities and NaN
+    // CLEAR: without the tile's infinities and NaN, unless all of it counts
     template <bool CLEAR>
     __device__ static inline void cols(f32x16 (&acc)[kCols], const char *tile, int blk, const At &a,
-                                       const P &p) {
+                                       const P &p, bool all) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
                 bf16x8 x = col_frag(tile, blk, k, c, a);
-                if constexpr (CLEAR) x = clear(x);
+                if constexpr (CLEAR) x = all ? x : clear(x);
                 acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, p.f[k], acc[c], 0, 0, 0);
             }
     }
@@ -286,13 +286,13 @@ template <int D> struct Rows<float, D> {
     __device__ static inline bool odd(float x) { return (bits(x) & 0x7F800000u) == 0x7F800000u; }
     template <bool CLEAR>
     __device__ static inline void cols(f32x16 (&acc)[kCols], const char *tile, int blk, const At &a,
-                                       const P &p) {
+                                       const P &p, bool all) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const run_t x = col_frag(tile, blk, e, a);
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
-                acc[c] = mfma(CLEAR && odd(x[c]) ? 0.f : x[c], p.f[e], acc[c]);
+                acc[c] = mfma(CLEAR && !all && odd(x[c]) ? 0.f : x[c], p.f[e], acc[c]);
         }
     }
     __device__ static inline bool any_odd(const f32x16 (&acc)[kCols]) {
