@@ -54,13 +54,14 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const int first = a.window > 0 && i0 >= a.window ? i0 - a.window + 1 : 0;
     const int t0 = first / kTok, t1 = last / kTok + 1;
 
-    auto attends = [&](int j) { return j <= i && (a.window == 0 || j > i - a.window); };
+    const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
+    auto attends = [&](int j) GDR_INLINE { return (unsigned)(i - j) < span; };
     // every row of the wave attends to all of a tile (rows past the sequence's
     // end, which are not stored, among them)
-    auto tile_full = [&](int t) {
+    auto tile_full = [&](int t) GDR_INLINE {
         return t * kTok + kTok - 1 <= iw && (a.window == 0 || t * kTok > iw + 31 - a.window);
     };
-    auto stage = [&](int t) {
+    auto stage = [&](int t) GDR_INLINE {
         const size_t row = (size_t)bl.row0 + t * kTok;
         const int left = bl.len - t * kTok;
         fetch<T, D, kWaves, kTok>(lds[t & 1][0], kh, row, left, kpitch, w, lane);
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     f32x16 acc[kCols];
     // All tiles.  CLEAR: infinities and NaN are taken out of V where some row
     // does not attend to a token.
-    auto walk = [&](auto clear) {
+    auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
         m = -INFINITY;
         mc = l = 0.f;
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     // A weight of zero must not meet an infinity or NaN of V.  Where one has, a
     // result is NaN: then all is done again without such values, and the rows
     // that do attend to them get them after.
-    if (__syncthreads_or(R::any_odd(acc))) {
+    if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
         walk(std::true_type{});
         for (int j = first; j <= last; ++j)
             if (!tile_full(j / kTok) && attends(j))

@@ -77,15 +77,16 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const int last = i0 + kRows < bl.len ? i0 + kRows - 1 : bl.len - 1;
     const int first = a.window > 0 && i0 >= a.window ? i0 - a.window + 1 : 0;
     const int t0 = first / kTok, t1 = last / kTok + 1;
-    auto attends = [&](int j) { return j <= i && (a.window == 0 || j > i - a.window); };
-    auto stage = [&](int t) {
+    const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
+    auto attends = [&](int j) GDR_INLINE { return (unsigned)(i - j) < span; };
+    auto stage = [&](int t) GDR_INLINE {
         const size_t row = (size_t)bl.row0 + t * kTok;
         const int left = bl.len - t * kTok;
         fetch<T, D, kWaves, kTok>(lds[t & 1][0], kh, row, left, kpitch, w, lane);
         fetch<T, D, kWaves, kTok>(lds[t & 1][1], vh, row, left, kpitch, w, lane);
     };
     f32x16 acc[kCols];
-    auto walk = [&](auto clear) {
+    auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     walk(std::false_type{});
     // (0 times an infinity or NaN of a key that a row does not attend to: again
     // without those)
-    if (__syncthreads_or(R::any_odd(acc))) walk(std::true_type{});
+    if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) walk(std::true_type{});
     if (i >= bl.len) return;
     R::store(static_cast<T *>(a.dq) + ((size_t)(bl.row0 + i) * a.Hq + head) * D, acc, h, a.scale);
 }
@@ -150,12 +151,13 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     R::load(kf, static_cast<const T *>(a.k) + ((size_t)row * a.Hkv + hk) * D, h);
     R::load(vf, static_cast<const T *>(a.v) + ((size_t)row * a.Hkv + hk) * D, h);
     // rows that attend to a token of the block
+    const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
     const int over = a.window > 0 && bl.len - j0 > kRows + a.window - 1 ? j0 + kRows + a.window - 1
                                                                          : bl.len;
     const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
 
     // tile n: rows t0 + n % tiles of head hk G + n / tiles
-    auto stage = [&](int n) {
+    auto stage = [&](int n) GDR_INLINE {
         const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
         const size_t first = (size_t)bl.row0 + t * kTok;
         const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
         }
     };
     f32x16 dk[kCols], dv[kCols];
-    auto walk = [&](auto clear) {
+    auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
@@ -205,7 +207,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int i = i0 + 32 * b + R::key(e, h);
-                        const bool in = j <= i && i < bl.len && (a.window == 0 || j > i - a.window);
+                        const bool in = (unsigned)(i - j) < span & i < bl.len;
                         x[e] = in ? x[e] : 0.f;
                         dp[e] = in ? dp[e] : 0.f;
                     }
@@ -216,7 +218,8 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
         }
     };
     walk(std::false_type{});
-    if (__syncthreads_or(R::any_odd(dk) || R::any_odd(dv))) walk(std::true_type{});
+    if (__builtin_expect(__syncthreads_or(R::any_odd(dk) || R::any_odd(dv)), 0))
+        walk(std::true_type{});
     if (j >= bl.len) return;
     const size_t to = ((size_t)(bl.row0 + j) * a.Hkv + hk) * D;
     R::store(static_cast<T *>(a.dk) + to, dk, h, a.scale);
@@ -253,11 +256,12 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
     const int row = bl.row0 + (j < bl.len ? j : bl.len - 1);
     R::load(kf, static_cast<const T *>(a.k) + ((size_t)row * a.Hkv + hk) * D, h);
     R::load(vf, static_cast<const T *>(a.v) + ((size_t)row * a.Hkv + hk) * D, h);
+    const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
     const int over = a.window > 0 && bl.len - j0 > kRows + a.window - 1 ? j0 + kRows + a.window - 1
                                                                          : bl.len;
     const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
 
-    auto stage = [&](int n) {
+    auto stage = [&](int n) GDR_INLINE {
         const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
         const size_t first = (size_t)bl.row0 + t * kTok;
         const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
@@ -273,15 +277,15 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
     f32x16 acc[kCols];
     typename R::P kept;                      // this wave's half of tile n, for its own sums
     // each of 32 rows from i on attends to all of the pair's tokens
-    auto whole = [&](int i) {
+    auto whole = [&](int i) GDR_INLINE {
         return i >= jw + 31 && i + 32 <= bl.len && (a.window == 0 || i + 31 < jw + a.window);
     };
-    // w and ds of this wave's half of tile n; between() is what may run under
-    // the last of this
-    auto weights = [&](int n, auto between) {
-        const int i0 = (t0 + n % tiles) * kTok + 32 * role;
-        const char *qt = lds[n % 3][0] + 32 * role * R::kRowBytes, *gt = qt + R::kTileBytes;
-        const float *lse2 = stats[n % 3][0] + 32 * role, *delta = lse2 + kTok;
+    // w and ds of this wave's half of tile n
+    auto weights = [&](int n, auto which, auto between) GDR_INLINE {
+        constexpr int ROLE = decltype(which)::value;
+        const int i0 = (t0 + n % tiles) * kTok + 32 * ROLE;
+        const char *qt = lds[n % 3][0] + 32 * ROLE * R::kRowBytes, *gt = qt + R::kTileBytes;
+        const float *lse2 = stats[n % 3][0] + 32 * ROLE, *delta = lse2 + kTok;
         f32x16 x = R::rows(qt, 0, at, kf);
         __builtin_amdgcn_sched_barrier(0);
         f32x16 dp = R::rows(gt, 0, at, vf);
@@ -303,34 +307,37 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int i = i0 + R::key(e, h);
-                const bool in = j <= i && i < bl.len && (a.window == 0 || j > i - a.window);
+                const bool in = (unsigned)(i - j) < span & i < bl.len;
                 x[e] = in ? x[e] : 0.f;
                 dp[e] = in ? dp[e] : 0.f;
             }
         }
         const typename R::P p = R::operand(x), ds = R::operand(dp);
+        kept = ROLE ? ds : p;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            given[n & 1][role][pair][u][lane] = role ? p.f[u] : ds.f[u];
-            kept.f[u] = role ? ds.f[u] : p.f[u];
-        }
+        for (int u = 0; u < 2; ++u) given[n & 1][ROLE][pair][u][lane] = ROLE ? p.f[u] : ds.f[u];
     };
     // dv (role 0) or dk (role 1) of tile n, by this wave's half of it (mine) or
     // the other's
-    auto sums = [&](int n, auto clear, const typename R::P &mine) {
-        const bool all = whole((t0 + n % tiles) * kTok + 32 * role);
+    auto sums = [&](int n, auto which, auto clear, const typename R::P &mine) GDR_INLINE {
+        constexpr int ROLE = decltype(which)::value;
+        const bool all = whole((t0 + n % tiles) * kTok + 32 * ROLE);
         R::template cols<decltype(clear)::value>(
-            acc, lds[n % 3][1 - role] + 32 * role * R::kRowBytes, 0, at, mine, all);
+            acc, lds[n % 3][1 - ROLE] + 32 * ROLE * R::kRowBytes, 0, at, mine, all);
     };
-    auto other_sums = [&](int n, auto clear) {
-        const bool all = whole((t0 + n % tiles) * kTok + 32 * (1 - role));
+    auto other_sums = [&](int n, auto which, auto clear) GDR_INLINE {
+        constexpr int ROLE = decltype(which)::value;
+        const bool all = whole((t0 + n % tiles) * kTok + 32 * (1 - ROLE));
         typename R::P p;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) p.f[u] = given[n & 1][1 - role][pair][u][lane];
+        for (int u = 0; u < 2; ++u) p.f[u] = given[n & 1][1 - ROLE][pair][u][lane];
         R::template cols<decltype(clear)::value>(
-            acc, lds[n % 3][1 - role] + 32 * (1 - role) * R::kRowBytes, 0, at, p, all);
+            acc, lds[n % 3][1 - ROLE] + 32 * (1 - ROLE) * R::kRowBytes, 0, at, p, all);
     };
-    auto walk = [&](auto clear) {
+    // Role 0 forms its weights first and then its sums, role 1 the other way
+    // round: the two waves of a SIMD are then in different parts of a tile.
+    auto walk_as = [&](auto which, auto clear) GDR_INLINE {
+        constexpr int ROLE = decltype(which)::value;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
@@ -340,21 +347,33 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
         R::settle(vf);
         tile_landed();
         if (all > 1) stage(1);
-        weights(0, []() {});
+        weights(0, which, []() {});
         for (int n = 1; n < all; ++n) {
             tile_landed();
             if (n + 1 < all) stage(n + 1);
-            const typename R::P mine = kept;
-            weights(n, [&]() { sums(n - 1, clear, mine); });
-            __builtin_amdgcn_sched_barrier(0);
-            other_sums(n - 1, clear);
+            if constexpr (ROLE == 0) {
+                const typename R::P mine = kept;
+                weights(n, which, [&]() { sums(n - 1, which, clear, mine); });
+                __builtin_amdgcn_sched_barrier(0);
+                other_sums(n - 1, which, clear);
+            } else {
+                sums(n - 1, which, clear, kept);
+                __builtin_amdgcn_sched_barrier(0);
+                other_sums(n - 1, which, clear);
+                __builtin_amdgcn_sched_barrier(0);
+                weights(n, which, []() {});
+            }
         }
         __syncthreads();
-        sums(all - 1, clear, kept);
-        other_sums(all - 1, clear);
+        sums(all - 1, which, clear, kept);
+        other_sums(all - 1, which, clear);
+    };
+    auto walk = [&](auto clear) GDR_INLINE {
+        if (role) walk_as(std::integral_constant<int, 1>{}, clear);
+        else      walk_as(std::integral_constant<int, 0>{}, clear);
     };
     walk(std::false_type{});
-    if (__syncthreads_or(R::any_odd(acc))) walk(std::true_type{});
+    if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) walk(std::true_type{});
     if (j >= bl.len) return;
     const size_t to = ((size_t)(bl.row0 + j) * a.Hkv + hk) * D;
     if (role) R::store(static_cast<T *>(a.dk) + to, acc, h, a.scale);

@@ -10,6 +10,10 @@
 #include "device_util.h"
 #include "gdr_internal.h"
 
+// on lambdas: the compiler leaves large ones, and those on rare paths, as calls,
+// with all that they capture in memory
+#define GDR_INLINE __attribute__((always_inline))
+
 namespace gdr {
 
 struct PromptArgs {
@@ -338,14 +342,15 @@ __device__ inline void fetch(char *tile, const T *head, size_t row0, int valid, 
     const unsigned long long base = reinterpret_cast<unsigned long long>(head) + row0 * pitch;
     const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)), 0xFFFFFFFFu,
                    0x00020000u};
-    const unsigned to = (unsigned)uniform((int)reinterpret_cast<size_t>((lds_void *)tile));
+    const unsigned to = (unsigned)reinterpret_cast<size_t>((lds_void *)tile);
 #pragma unroll
     for (int i = 0; i < kAll / WAVES; ++i) {
         const int n = w + WAVES * i, j = n * kPer + lane / R::kChunks;
         const int chunk = lane % R::kChunks ^ R::swz(j);
         const int row = j < valid ? j : valid - 1;
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :: "s"(to + 1024u * n), "v"(row * pitch + 16u * chunk), "s"(rs) : "memory");
+                     :: "s"(uniform((int)(to + 1024u * n))), "v"(row * pitch + 16u * chunk), "s"(rs)
+                     : "memory");
     }
 }
 // 4 bytes a lane of `from` (its element `index`), lanes 0 .. N - 1, into words
