@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const PromptArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
-    const int head = blockIdx.x % a.Hq;
+    const int head = query_head(a, blockIdx.x % a.Hq);
     const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
     if (bl.i < 0) return;
     const int i0 = bl.i * kRows, iw = i0 + 32 * w, i = iw + r;

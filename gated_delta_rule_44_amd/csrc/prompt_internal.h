@@ -87,6 +87,11 @@ __device__ inline Block find_block(const PromptArgs &a, int s) {
     return x;
 }
 
+// The query head of workgroup number u of a block's Hq: workgroups go to the
+// eight XCDs in turn, so that those which read one key-value head are a multiple
+// of Hkv apart, on one XCD's L2 (or few).
+__device__ inline int query_head(const PromptArgs &a, int u) { return u % a.Hkv * a.G + u / a.Hkv; }
+
 // Rows of 32 tokens as MFMA operands, and products with tiles of rows that lie
 // in LDS.  All three kernels are made of two products, with lane = 32 h + r:
 //   rows:  X = tile . b^T, b 32 rows in registers: the lane gets X[j][r] for
