@@ -61,11 +61,12 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     auto tile_full = [&](int t) GDR_INLINE {
         return t * kTok + kTok - 1 <= iw && (a.window == 0 || t * kTok > iw + 31 - a.window);
     };
+    const Fetch<T, D, kWaves> fetch(kpitch, w, lane);
     auto stage = [&](int t) GDR_INLINE {
         const size_t row = (size_t)bl.row0 + t * kTok;
         const int left = bl.len - t * kTok;
-        fetch<T, D, kWaves, kTok>(lds[t & 1][0], kh, row, left, kpitch, w, lane);
-        fetch<T, D, kWaves, kTok>(lds[t & 1][1], vh, row, left, kpitch, w, lane);
+        fetch(lds[t & 1][0], kh, row, left, lane);
+        fetch(lds[t & 1][1], vh, row, left, lane);
     };
     float m, mc, l;
     f32x16 acc[kCols];

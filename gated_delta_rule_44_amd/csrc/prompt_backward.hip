@@ -79,11 +79,12 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const int t0 = first / kTok, t1 = last / kTok + 1;
     const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
     auto attends = [&](int j) GDR_INLINE { return (unsigned)(i - j) < span; };
+    const Fetch<T, D, kWaves> fetch(kpitch, w, lane);
     auto stage = [&](int t) GDR_INLINE {
         const size_t row = (size_t)bl.row0 + t * kTok;
         const int left = bl.len - t * kTok;
-        fetch<T, D, kWaves, kTok>(lds[t & 1][0], kh, row, left, kpitch, w, lane);
-        fetch<T, D, kWaves, kTok>(lds[t & 1][1], vh, row, left, kpitch, w, lane);
+        fetch(lds[t & 1][0], kh, row, left, lane);
+        fetch(lds[t & 1][1], vh, row, left, lane);
     };
     f32x16 acc[kCols];
     auto walk = [&](auto clear) GDR_INLINE {
@@ -156,18 +157,22 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
                                                                          : bl.len;
     const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
 
-    // tile n: rows t0 + n % tiles of head hk G + n / tiles
-    auto stage = [&](int n) GDR_INLINE {
-        const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
-        const size_t first = (size_t)bl.row0 + t * kTok;
-        const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
-        const T *gh = static_cast<const T *>(a.d_o) + (size_t)head * D;
-        fetch<T, D, kWaves, kTok>(lds[n & 1][0], qh, first, left, qpitch, w, lane);
-        fetch<T, D, kWaves, kTok>(lds[n & 1][1], gh, first, left, qpitch, w, lane);
-        if (w < 2) {
-            const int at_row = lane < left ? lane : left - 1;
-            fetch_words<kTok>(stats[n & 1][w], (w ? k.delta : k.lse2) + (size_t)head * a.T_total + first,
-                              at_row, lane);
+    const Fetch<T, D, kWaves> fetch(qpitch, w, lane);
+    // the tiles in their order, head by head: where the next to be fetched is
+    const int t1 = t0 + tiles;
+    int next_head, next_t;
+    auto stage = [&](int buf) GDR_INLINE {
+        const int left = bl.len - next_t * kTok;
+        const size_t first = (size_t)bl.row0 + next_t * kTok;
+        fetch(lds[buf][0], static_cast<const T *>(a.q) + (size_t)next_head * D, first, left, lane);
+        fetch(lds[buf][1], static_cast<const T *>(a.d_o) + (size_t)next_head * D, first, left, lane);
+        if (w < 2)
+            fetch_words<kTok>(stats[buf][w],
+                              (w ? k.delta : k.lse2) + (size_t)next_head * a.T_total + first,
+                              lane < left ? lane : left - 1, lane);
+        if (++next_t == t1) {
+            next_t = t0;
+            ++next_head;
         }
     };
     f32x16 dk[kCols], dv[kCols];
@@ -177,13 +182,16 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) dk[c][e] = dv[c][e] = 0.f;
+        next_head = hk * a.G;
+        next_t = t0;
         stage(0);
         R::settle(kf);
         R::settle(vf);
-        for (int n = 0; n < all; ++n) {
+        for (int n = 0, t = t0; n < all; ++n) {
             tile_landed();
-            if (n + 1 < all) stage(n + 1);
-            const int i0 = (t0 + n % tiles) * kTok;
+            if (n + 1 < all) stage((n + 1) & 1);
+            const int i0 = t * kTok;
+            t = t + 1 == t1 ? t0 : t + 1;
             const char *qt = lds[n & 1][0], *gt = lds[n & 1][1];
             const float *lse2 = stats[n & 1][0], *delta = stats[n & 1][1];
             if (jw >= bl.len || i0 + kTok <= jw || (a.window > 0 && i0 >= jw + 31 + a.window)) continue;
@@ -261,17 +269,22 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
                                                                          : bl.len;
     const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
 
-    auto stage = [&](int n) GDR_INLINE {
-        const int head = hk * a.G + n / tiles, t = t0 + n % tiles, left = bl.len - t * kTok;
-        const size_t first = (size_t)bl.row0 + t * kTok;
-        const T *qh = static_cast<const T *>(a.q) + (size_t)head * D;
-        const T *gh = static_cast<const T *>(a.d_o) + (size_t)head * D;
-        fetch<T, D, 2 * kWaves, kTok>(lds[n % 3][0], qh, first, left, qpitch, w, lane);
-        fetch<T, D, 2 * kWaves, kTok>(lds[n % 3][1], gh, first, left, qpitch, w, lane);
-        if (w < 2) {
-            const int at_row = lane < left ? lane : left - 1;
-            fetch_words<kTok>(stats[n % 3][w], (w ? k.delta : k.lse2) + (size_t)head * a.T_total + first,
-                              at_row, lane);
+    const Fetch<T, D, 2 * kWaves> fetch(qpitch, w, lane);
+    // the tiles in their order, head by head: where the next to be fetched is
+    const int t1 = t0 + tiles;
+    int next_head, next_t;
+    auto stage = [&](int buf) GDR_INLINE {
+        const int left = bl.len - next_t * kTok;
+        const size_t first = (size_t)bl.row0 + next_t * kTok;
+        fetch(lds[buf][0], static_cast<const T *>(a.q) + (size_t)next_head * D, first, left, lane);
+        fetch(lds[buf][1], static_cast<const T *>(a.d_o) + (size_t)next_head * D, first, left, lane);
+        if (w < 2)
+            fetch_words<kTok>(stats[buf][w],
+                              (w ? k.delta : k.lse2) + (size_t)next_head * a.T_total + first,
+                              lane < left ? lane : left - 1, lane);
+        if (++next_t == t1) {
+            next_t = t0;
+            ++next_head;
         }
     };
     f32x16 acc[kCols];
@@ -280,12 +293,17 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
     auto whole = [&](int i) GDR_INLINE {
         return i >= jw + 31 && i + 32 <= bl.len && (a.window == 0 || i + 31 < jw + a.window);
     };
-    // w and ds of this wave's half of tile n
-    auto weights = [&](int n, auto which, auto between) GDR_INLINE {
+    // A tile: its number in the sequence, its place in LDS and in turn of two.
+    struct Tile { int t, buf, turn; };
+    auto after = [&](Tile x) GDR_INLINE {
+        return Tile{x.t + 1 == t1 ? t0 : x.t + 1, x.buf == 2 ? 0 : x.buf + 1, x.turn ^ 1};
+    };
+    // w and ds of this wave's half of a tile
+    auto weights = [&](Tile n, auto which, auto between) GDR_INLINE {
         constexpr int ROLE = decltype(which)::value;
-        const int i0 = (t0 + n % tiles) * kTok + 32 * ROLE;
-        const char *qt = lds[n % 3][0] + 32 * ROLE * R::kRowBytes, *gt = qt + R::kTileBytes;
-        const float *lse2 = stats[n % 3][0] + 32 * ROLE, *delta = lse2 + kTok;
+        const int i0 = n.t * kTok + 32 * ROLE;
+        const char *qt = lds[n.buf][0] + 32 * ROLE * R::kRowBytes, *gt = qt + R::kTileBytes;
+        const float *lse2 = stats[n.buf][0] + 32 * ROLE, *delta = lse2 + kTok;
         f32x16 x = R::rows(qt, 0, at, kf);
         __builtin_amdgcn_sched_barrier(0);
         f32x16 dp = R::rows(gt, 0, at, vf);
@@ -315,24 +333,24 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
         const typename R::P p = R::operand(x), ds = R::operand(dp);
         kept = ROLE ? ds : p;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) given[n & 1][ROLE][pair][u][lane] = ROLE ? p.f[u] : ds.f[u];
+        for (int u = 0; u < 2; ++u) given[n.turn][ROLE][pair][u][lane] = ROLE ? p.f[u] : ds.f[u];
     };
-    // dv (role 0) or dk (role 1) of tile n, by this wave's half of it (mine) or
+    // dv (role 0) or dk (role 1) of a tile, by this wave's half of it (mine) or
     // the other's
-    auto sums = [&](int n, auto which, auto clear, const typename R::P &mine) GDR_INLINE {
+    auto sums = [&](Tile n, auto which, auto clear, const typename R::P &mine) GDR_INLINE {
         constexpr int ROLE = decltype(which)::value;
-        const bool all = whole((t0 + n % tiles) * kTok + 32 * ROLE);
+        const bool all = whole(n.t * kTok + 32 * ROLE);
         R::template cols<decltype(clear)::value>(
-            acc, lds[n % 3][1 - ROLE] + 32 * ROLE * R::kRowBytes, 0, at, mine, all);
+            acc, lds[n.buf][1 - ROLE] + 32 * ROLE * R::kRowBytes, 0, at, mine, all);
     };
-    auto other_sums = [&](int n, auto which, auto clear) GDR_INLINE {
+    auto other_sums = [&](Tile n, auto which, auto clear) GDR_INLINE {
         constexpr int ROLE = decltype(which)::value;
-        const bool all = whole((t0 + n % tiles) * kTok + 32 * (1 - ROLE));
+        const bool all = whole(n.t * kTok + 32 * (1 - ROLE));
         typename R::P p;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) p.f[u] = given[n & 1][1 - ROLE][pair][u][lane];
+        for (int u = 0; u < 2; ++u) p.f[u] = given[n.turn][1 - ROLE][pair][u][lane];
         R::template cols<decltype(clear)::value>(
-            acc, lds[n % 3][1 - ROLE] + 32 * (1 - ROLE) * R::kRowBytes, 0, at, p, all);
+            acc, lds[n.buf][1 - ROLE] + 32 * (1 - ROLE) * R::kRowBytes, 0, at, p, all);
     };
     // Role 0 forms its weights first and then its sums, role 1 the other way
     // round: the two waves of a SIMD are then in different parts of a tile.
@@ -342,31 +360,36 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
+        next_head = hk * a.G;
+        next_t = t0;
         stage(0);
         R::settle(kf);
         R::settle(vf);
         tile_landed();
         if (all > 1) stage(1);
-        weights(0, which, []() {});
+        Tile now{t0, 0, 0};
+        weights(now, which, []() {});
         for (int n = 1; n < all; ++n) {
+            const Tile was = now;
+            now = after(now);
             tile_landed();
-            if (n + 1 < all) stage(n + 1);
+            if (n + 1 < all) stage(now.buf == 2 ? 0 : now.buf + 1);
             if constexpr (ROLE == 0) {
                 const typename R::P mine = kept;
-                weights(n, which, [&]() { sums(n - 1, which, clear, mine); });
+                weights(now, which, [&]() { sums(was, which, clear, mine); });
                 __builtin_amdgcn_sched_barrier(0);
-                other_sums(n - 1, which, clear);
+                other_sums(was, which, clear);
             } else {
-                sums(n - 1, which, clear, kept);
+                sums(was, which, clear, kept);
                 __builtin_amdgcn_sched_barrier(0);
-                other_sums(n - 1, which, clear);
+                other_sums(was, which, clear);
                 __builtin_amdgcn_sched_barrier(0);
-                weights(n, which, []() {});
+                weights(now, which, []() {});
             }
         }
         __syncthreads();
-        sums(all - 1, which, clear, kept);
-        other_sums(all - 1, which, clear);
+        sums(now, which, clear, kept);
+        other_sums(now, which, clear);
     };
     auto walk = [&](auto clear) GDR_INLINE {
         if (role) walk_as(std::integral_constant<int, 1>{}, clear);

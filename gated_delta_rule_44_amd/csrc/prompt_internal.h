@@ -336,28 +336,52 @@ template <int D> struct Rows<float, D> {
 // tile in LDS, by the waves of a workgroup, straight from memory: a wave's
 // instruction fills 1 KiB, 16 bytes a lane in their order, so that the lane
 // asks for the chunk that belongs there.  Rows from `valid` (>= 1) on are
-// copies of the last one, which the callers mask.  (Written out: the compiler
-// would wait for a load to LDS before the next read of any LDS.)
-template <typename T, int D, int WAVES, int ROWS>
-__device__ inline void fetch(char *tile, const T *head, size_t row0, int valid, unsigned pitch,
-                             int w, int lane) {
+// copies of the last one, which the callers mask.  What a lane adds to a tile's
+// address is the same for all whole tiles.  (Written out: the compiler would
+// wait for a load to LDS before the next read of any LDS.)
+template <typename T, int D, int WAVES>
+struct Fetch {
     using R = Rows<T, D>;
-    constexpr int kPer = 1024 / R::kRowBytes, kAll = ROWS / kPer;
-    static_assert(kAll % WAVES == 0, "the waves fetch alike");
-    const unsigned long long base = reinterpret_cast<unsigned long long>(head) + row0 * pitch;
-    const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)), 0xFFFFFFFFu,
-                   0x00020000u};
-    const unsigned to = (unsigned)reinterpret_cast<size_t>((lds_void *)tile);
+    static constexpr int kPer = 1024 / R::kRowBytes, kLoads = R::kTok / kPer / WAVES;
+    static_assert(kLoads * kPer * WAVES == R::kTok, "the waves fetch alike");
+    unsigned pitch, off[kLoads];
+    int w;
+    __device__ static inline int row(int i, int w, int lane) {
+        return (w + WAVES * i) * kPer + lane / R::kChunks;
+    }
+    __device__ static inline unsigned chunk(int row, int lane) {
+        return 16u * (lane % R::kChunks ^ R::swz(row));
+    }
+    __device__ inline Fetch(unsigned pitch, int w, int lane) : pitch(pitch), w(w) {
 #pragma unroll
-    for (int i = 0; i < kAll / WAVES; ++i) {
-        const int n = w + WAVES * i, j = n * kPer + lane / R::kChunks;
-        const int chunk = lane % R::kChunks ^ R::swz(j);
-        const int row = j < valid ? j : valid - 1;
+        for (int i = 0; i < kLoads; ++i) {
+            const int j = row(i, w, lane);
+            off[i] = j * pitch + chunk(j, lane);
+        }
+    }
+    __device__ inline void load(unsigned to, u32x4 rs, int i, unsigned off) const {
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :: "s"(uniform((int)(to + 1024u * n))), "v"(row * pitch + 16u * chunk), "s"(rs)
+                     :: "s"(uniform((int)(to + 1024u * (w + WAVES * i)))), "v"(off), "s"(rs)
                      : "memory");
     }
-}
+    __device__ inline void operator()(char *tile, const T *head, size_t row0, int valid,
+                                      int lane) const {
+        const unsigned long long base = reinterpret_cast<unsigned long long>(head) + row0 * pitch;
+        const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)),
+                       0xFFFFFFFFu, 0x00020000u};
+        const unsigned to = (unsigned)reinterpret_cast<size_t>((lds_void *)tile);
+        if (valid >= R::kTok) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load(to, rs, i, off[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int j = row(i, w, lane), from = j < valid ? j : valid - 1;
+                load(to, rs, i, from * pitch + chunk(j, lane));
+            }
+        }
+    }
+};
 // 4 bytes a lane of `from` (its element `index`), lanes 0 .. N - 1, into words
 // that lie together in LDS, likewise.
 template <int N>
