@@ -23,6 +23,7 @@
 #include "cache_internal.h"
 #include "gdr_internal.h"
 #include "device_util.h"
+#include "prompt_internal.h"
 
 namespace gdr {
 namespace {
@@ -128,6 +129,13 @@ int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long 
     return rows > 32 && seen * B * Hkv * D * 4 >= kShareBytes ? 64 : 32;
 }
 
+// Waves of a workgroup of a tree's rows, 32 each; more than 128 rows are several
+// blocks alike.
+int tree_waves(long long rows) {
+    const long long blocks = (rows + 127) / 128;
+    return (int)((rows + 32 * blocks - 1) / (32 * blocks));
+}
+
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
 // them, every slot's {sequence, its first slot, its slots, tokens of one};
 // (m, l) of every slot, unit and row; o of the same, unnormalised; with
@@ -192,9 +200,6 @@ __device__ inline N group_scan(N x, N &total, N *lds) {
     return before + incl - x;
 }
 
-// A value that is the same in all lanes, for a scalar register.
-__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 struct Slot { int b, first, count, chunk; };      // sequence, its first slot, its slots, tokens of one
 
 // Shares the sequences' slots out over a workgroup of 64 WAVES threads, thread
@@ -258,7 +263,9 @@ __global__ __launch_bounds__(1024) void slots_kernel(KArgs k) {
     for (int i = all + threadIdx.x; i < k.plan.max_slots; i += 1024) k.slots[i] = int4{-1, 0, 0, 0};
 }
 
-// The sequence that slot s belongs to (b = -1: past the last slot).
+// The sequence that slot s belongs to (b = -1: past the last slot), by a
+// workgroup of WAVES waves.
+template <int WAVES>
 __device__ inline Slot find_slot(const KArgs &k, int s) {
     // no sequence has a second slot: slot and sequence are one
     if (!k.parts) return Slot{s < k.a.B ? s : -1, s, 1, 1 << 30};
@@ -269,7 +276,7 @@ __device__ inline Slot find_slot(const KArgs &k, int s) {
     }
     __shared__ Slot found;
     if (threadIdx.x == 0) found.b = -1;
-    Sharing<kWaves> sh(k);
+    Sharing<WAVES> sh(k);
     int mine;
     sh.begin(mine);
     if (s >= sh.at && s < sh.at + mine) {
@@ -286,12 +293,6 @@ __device__ inline float swap_max16(float x) {
     asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(b));
     return fmaxf(a, b);
 }
-__device__ inline float swap_max32(float x) {
-    float a = x, b = x;
-    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
-    return fmaxf(a, b);
-}
-__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 // What logits are taken relative to: their maximum, or 0 where every one is
 // -inf (masked, then the weights 2^{-inf} are 0) or NaN (which fmaxf passes
 // over and the weights keep).
@@ -306,8 +307,6 @@ template <bool STREAM>
 __device__ inline u32x4 load16(rsrc_t r, unsigned off) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, STREAM ? 2 : 0);
 }
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // A block of 16 tokens of one head in a cache: its first byte, and how many
 // bytes of it may be read (0: none of its tokens are there).
@@ -683,7 +682,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     const int rb = wg / 8 % k.plan.row_blocks;
     const int unit = wg / 8 / k.plan.row_blocks * 8 + wg % 8;
     const int slot = unit / a.Hkv, h = unit % a.Hkv;
-    const Slot sl_ = find_slot(k, slot);
+    const Slot sl_ = find_slot<kWaves>(k, slot);
     const int b = sl_.b;
     if (b < 0) return;
     const int len = uniform(cached_len(a.seq_lens, b, a.map));
@@ -1029,6 +1028,200 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     }
 }
 
+// A tree's rows past 32, in bf16: a workgroup of W waves with 32 rows each, all
+// of them on every tile of 64 tokens, which passes through LDS, two tiles there,
+// the next on its way while one is worked on.  The products, the running maximum
+// and sum and what is done about infinities are those of the attention of whole
+// prompts (prompt.hip); a weight enters the product with V as one bf16 number,
+// 2^-8 off at most.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k) {
+    typedef bf16 T;
+    using R = Rows<T, D>;
+    constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols, kRows = 32 * W;
+    constexpr int kPer = 1024 / R::kRowBytes;         // rows of a load
+    __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
+    const AttnArgs &a = k.a;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int w = uniform(tid >> 6);
+    const int wg = blockIdx.x, rb = wg / 8 % k.plan.row_blocks;
+    const int unit = wg / 8 / k.plan.row_blocks * 8 + wg % 8;
+    const int slot = unit / a.Hkv, head = unit % a.Hkv;
+    const Slot sl = find_slot<W>(k, slot);
+    const int b = sl.b;
+    if (b < 0) return;
+    const int len = uniform(cached_len(a.seq_lens, b, a.map));
+    const Span seq = seq_span(len, a.n, a.window);
+    if (k.sched && head == 0 && rb == 0 && slot == sl.first && tid == 0)
+        k.sched[b] = int2{sl.first, sl.count};
+
+    const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + 32 * w + r;
+    const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0, ctx = len - a.n;
+    const typename R::At at = R::at(lane);
+    typename R::B q;
+    R::load(q, static_cast<const T *>(a.q) + (((size_t)b * a.n + t) * a.Hq + head * a.G + hg) * D, h);
+    if (k.negative) R::negate(q);
+    Span sp{0, 0};
+    unsigned long long drafts;
+    {
+        const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
+        const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
+        const int depth = __shfl(y.depth, t);
+        drafts = (unsigned long long)hi << 32 | lo;
+        if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
+    }
+    // the slot's tokens [k_lo, k_hi), in tiles from base on; all rows of the
+    // block attend to those of [all_lo, ctx)
+    const int c_lo = seq.lo + (slot - sl.first) * sl.chunk;
+    const int c_hi = c_lo + sl.chunk < len ? c_lo + sl.chunk : len;
+    const Span last = token_span(len, a.n, a.window,
+                                 ((row0 + kRows < rows ? row0 + kRows : rows) - 1) / a.G);
+    const int first_lo = token_span(len, a.n, a.window, 0).lo;
+    const int k_lo = first_lo > c_lo ? first_lo : c_lo, k_hi = last.hi < c_hi ? last.hi : c_hi;
+    const int base = k_lo & ~31, tiles = k_hi > k_lo ? (k_hi - base + kTok - 1) / kTok : 0;
+    const int all_lo = last.lo, all_hi = ctx < k_hi ? ctx : k_hi;
+    auto attends = [&](int j) GDR_INLINE {
+        return j >= sp.lo & j < sp.hi & j < k_hi &
+               (j < ctx | (int)(drafts >> ((j - ctx) & 63) & 1));
+    };
+
+    // pages of the blocks of 16 tokens of 16 tiles, a lane each (-1: absent, or
+    // past the tokens), and of the 16 tiles after them
+    auto load_pages = [&](int i0) GDR_INLINE {
+        const int j = base + i0 * kTok + 16 * lane;
+        return i0 < tiles && j < k_hi ? page_of(a.map, b, j) : -1;
+    };
+    int pages = -1, pages_after = load_pages(0);
+    // The tile i into LDS.  Rows that are not there come as zeros: the loads'
+    // bounds end before them.
+    const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
+    const size_t page_bytes = (size_t)R::kRowBytes << a.map.page_shift;
+    unsigned there = 0, there_next = 0;      // blocks of 16 tokens of the tile at hand, of the next
+    const int lrow = lane / R::kChunks;
+    auto stage = [&](int i) GDR_INLINE {
+        if ((i & 15) == 0) {
+            pages = pages_after;
+            pages_after = load_pages(i + 16);
+        }
+        there_next = (unsigned)(__builtin_amdgcn_ballot_w64(pages >= 0) >> (4 * (i & 15))) & 15u;
+        const unsigned to = lds_address(lds[i & 1][0]);
+#pragma unroll
+        for (int n = w; n < kTok / kPer; n += W) {
+            const int blk = n * kPer / 16, j0 = base + i * kTok + 16 * blk;
+            const int page = __builtin_amdgcn_readlane(pages, 4 * (i & 15) + blk);
+            const int valid = len - j0 < 16 ? len - j0 : 16;
+            const bool some = page >= 0 && valid > 0;
+            const size_t from = some ? ((size_t)page * a.Hkv + head) * page_bytes +
+                                           (size_t)slot_of(a.map, j0) * R::kRowBytes : 0;
+            const unsigned bytes = some ? (unsigned)(valid * R::kRowBytes) : 0u;
+            const int j = n * kPer + lrow;
+            const unsigned off = (j & 15) * R::kRowBytes + 16u * (lane % R::kChunks ^ R::swz(j));
+            load_lds(to + 1024u * n, source(kc + from, bytes), off);
+            load_lds(to + R::kTileBytes + 1024u * n, source(vc + from, bytes), off);
+        }
+    };
+    auto whole = [&](int i) GDR_INLINE {
+        return base + i * kTok >= all_lo && base + (i + 1) * kTok <= all_hi;
+    };
+    float m, mc, l;
+    f32x16 acc[kCols];
+    auto walk = [&](auto clear) GDR_INLINE {
+        constexpr bool CLEAR = decltype(clear)::value;
+        m = -INFINITY;
+        mc = l = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
+        if (CLEAR) pages_after = load_pages(0);
+        if (tiles > 0) stage(0);
+        R::settle(q);
+        for (int i = 0; i < tiles; ++i) {
+            there = there_next;
+            tile_landed();
+            if (i + 1 < tiles) stage(i + 1);
+            const char *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+            const bool full = whole(i) & there == 15u;
+            f32x16 x[kBlk];
+#pragma unroll
+            for (int c = 0; c < kBlk; ++c) x[c] = R::rows(kt, c, at, q);
+            if (!full) {
+#pragma unroll
+                for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const bool in = attends(base + i * kTok + 32 * c + R::key(e, h)) &
+                                        (int)(there >> (2 * c + (e >> 3)) & 1);
+                        x[c][e] = in ? x[c][e] : -INFINITY;
+                    }
+            }
+            float top = x[0][0];
+#pragma unroll
+            for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, x[c][e]);
+            const float mn = fmaxf(m, swap_max32(top));
+            const bool grow = (mn - m) * k.c > 8.f;
+            if (__builtin_amdgcn_ballot_w64(grow)) {
+                const float al = grow ? exp2_((m - mn) * k.c) : 1.f;
+                l *= al;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[c] *= al;
+                m = grow ? mn : m;
+                mc = grow ? mn * k.c : mc;
+            }
+#pragma unroll
+            for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    x[c][e] = exp2_(fmaf(x[c][e], k.c, -mc));
+                    l += x[c][e];
+                }
+#pragma unroll
+            for (int c = 0; c < kBlk; ++c)
+                R::template cols<CLEAR>(acc, vt, c, at, R::operand(x[c]), full);
+        }
+    };
+    walk(std::false_type{});
+    if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
+        walk(std::true_type{});
+        for (int j = k_lo; j < k_hi; ++j) {
+            if (whole((j - base) / kTok)) {          // (unless a page of it is absent)
+                bool all = true;
+                const int j0 = base + (j - base) / kTok * kTok;
+                for (int u = 0; u < 4; ++u) all &= page_of(a.map, b, j0 + 16 * u) >= 0;
+                if (all) continue;
+            }
+            const int page = page_of(a.map, b, j);
+            if (page >= 0 && attends(j))
+                R::add_odd(acc, static_cast<const T *>(a.v_cache) +
+                                    cache_row(a.map, a.Hkv, page, head, slot_of(a.map, j)) * D, h);
+        }
+    }
+    if (row >= rows) return;
+    l = swap_sum32(l);
+    if (sl.count == 1) {
+        if (l == 0.f) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
+        }
+        R::store(static_cast<T *>(a.o) + (((size_t)b * a.n + t) * a.Hq + head * a.G + hg) * D, acc, h,
+                 l == 0.f ? 0.f : 1.f / l);
+        return;
+    }
+    const size_t part = ((size_t)slot * k.plan.units + head * k.plan.row_blocks + rb) * kRows +
+                        32 * w + r;
+    if (h == 0) k.ml[part] = float2{m, l};
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<f32x4 *>(k.po + part * D + R::dim(c, e, h)) =
+                f32x4{acc[c][e], acc[c][e + 1], acc[c][e + 2], acc[c][e + 3]};
+}
+
 // (m, l) of one row over a sequence's slots, `stride` parts apart, by one
 // wave: lanes take slots in turn.
 __device__ inline float2 join_ml(const float2 *ml, size_t part, size_t stride, int count, float c) {
@@ -1205,8 +1398,12 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     }
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
-    if (k.plan.row_blocks == 1) attn_kernel<T, D, RW, RT, true, TREE><<<grid, kThreads, 0, s>>>(k);
-    else                        attn_kernel<T, D, RW, RT, false, TREE><<<grid, kThreads, 0, s>>>(k);
+    if constexpr (TREE && RW == 32 && RT >= 2)
+        tree_kernel<D, RT><<<grid, 64 * RT, 0, s>>>(k);
+    else if (k.plan.row_blocks == 1)
+        attn_kernel<T, D, RW, RT, true, TREE><<<grid, kThreads, 0, s>>>(k);
+    else
+        attn_kernel<T, D, RW, RT, false, TREE><<<grid, kThreads, 0, s>>>(k);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // about 4,096 workgroups join, and at most one per row: sequences in one
@@ -1227,10 +1424,20 @@ template <int D, bool TREE>
 hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
     if (!bf16_io) return launch<float, D, 16, 1, TREE>(a, s);
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
+    if constexpr (TREE) {
+        switch (tree_waves((long long)a.n * a.G)) {
+        case 1: break;
+        case 2: return launch<bf16, D, 32, 2, true>(a, s);
+        case 3: return launch<bf16, D, 32, 3, true>(a, s);
+        default: return launch<bf16, D, 32, 4, true>(a, s);
+        }
+    }
     switch (block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window)) {
     case 16: return launch<bf16, D, 16, 1, TREE>(a, s);
     case 32: return launch<bf16, D, 32, 1, TREE>(a, s);
-    default: return launch<bf16, D, 32, 2, TREE>(a, s);
+    default:
+        if constexpr (TREE) return hipErrorInvalidValue;      // (rows past 32: above)
+        else return launch<bf16, D, 32, 2, false>(a, s);
     }
 }
 
@@ -1244,6 +1451,10 @@ size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capac
     size_t most = 0;
     for (int rw = 16; rw <= 64 && (rw == 16 || rows > rw / 2); rw *= 2) {
         const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
+        if (x > most) most = x;
+    }
+    if (rows > 32) {                        // (a tree's blocks)
+        const size_t x = ws_map(B, n, G, Hkv, D, 32 * tree_waves(rows), capacity, with_scores).total;
         if (x > most) most = x;
     }
     return most;

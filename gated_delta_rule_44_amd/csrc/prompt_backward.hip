@@ -29,16 +29,6 @@ struct KArgs {
     float *lse2, *delta;  // [Hq, T_total]
 };
 
-template <typename T> __device__ inline float dot_part(const T *x, const T *y, int n) {
-    float s = 0.f;
-    for (int i = 0; i < n; i += 4) {
-        const f32x4 u = Elem<T>::load4(x + i), v = Elem<T>::load4(y + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = fmaf(u[e], v[e], s);
-    }
-    return s;
-}
-
 // Workgroup = (block of 128 rows, query head), 32 rows a wave.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) void query_kernel(KArgs k) {
@@ -65,10 +55,9 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
         const size_t at_row = ((size_t)row * a.Hq + head) * D;
         R::load(q, static_cast<const T *>(a.q) + at_row, h);
         R::load(g, static_cast<const T *>(a.d_o) + at_row, h);
-        const float x = a.lse[(size_t)row * a.Hq + head];
-        lse2 = x == -INFINITY ? INFINITY : x * kLog2e;
-        delta = swap_sum32(dot_part(static_cast<const T *>(a.d_o) + at_row + D / 2 * h,
-                                    static_cast<const T *>(a.o) + at_row + D / 2 * h, D / 2));
+        lse2 = base2(a.lse[(size_t)row * a.Hq + head]);
+        delta = row_delta<T, D>(static_cast<const T *>(a.d_o) + at_row,
+                                static_cast<const T *>(a.o) + at_row, h);
         if (i < bl.len && h == 0) {
             k.lse2[(size_t)head * a.T_total + row] = lse2;
             k.delta[(size_t)head * a.T_total + row] = delta;
@@ -412,9 +401,15 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     k.blocks = (int)blocks;
     k.lse2 = static_cast<float *>(a.ws);
     k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
-    query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
-    const hipError_t e = hipGetLastError();
+    hipError_t e;
+    if (few_rows<T, D>(a, blocks * a.Hq, 1)) {
+        e = launch_queries_short(sizeof(T) == 2, D, a, s);
+    } else {
+        query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess) return e;
+    if (few_rows<T, D>(a, blocks * a.Hkv, a.G)) return launch_keys_short(sizeof(T) == 2, D, a, s);
     if constexpr (sizeof(T) == 2)
         key_pairs_kernel<D><<<(unsigned)(blocks * a.Hkv), 2 * kThreads, 0, s>>>(k);
     else

@@ -32,6 +32,11 @@ hipError_t launch_attention_prefill(bool bf16_io, int D, const PromptArgs &a, hi
 hipError_t launch_attention_backward(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
 size_t attention_backward_workspace(bool bf16_io, int B, int T_total, int Hq, int Hkv, int D);
 
+// the same calls, or parts of them, in blocks of 32 rows (prompt_short.hip)
+hipError_t launch_prompt_short(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
+hipError_t launch_queries_short(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
+hipError_t launch_keys_short(bool bf16_io, int D, const PromptArgs &a, hipStream_t s);
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -85,6 +90,28 @@ __device__ inline Block find_block(const PromptArgs &a, int s) {
     x.len = hi - lo;
     if (x.i < 0 || x.len <= 0 || x.i > (x.len - 1) / RB) x.i = -1;
     return x;
+}
+
+// Whether blocks of 32 rows (prompt_short.hip) are done sooner than `wgs` of
+// 128, with what a mean row attends to `times` over in a workgroup's loop.  The
+// short form spreads a block over four workgroups and their waves, which pays
+// while the long one leaves CUs idle and its workgroups are long; it reads every
+// tile four times as often.  Measured, long against short, in us (forward; the
+// two backward kernels turn at the same places): bf16, 128 channels, 64
+// workgroups of 1,024 tokens 24 / 14, 128 of 2,048 42 / 29 and of 512 16 / 17,
+// 256 of 1,024 26 / 39 and of 4,096 80 / 84; 64 channels, 128 of 512 11 / 8, 256
+// of 512 12 / 15, of 1,024 18 / 19 and of 4,096 57 / 42, 512 of 2,048 43 / 48;
+// fp32, 64 channels, 256 of 512 43 / 42 and of 4,096 300 / 181, 512 of 1,024
+// 139 / 122, of 2,048 269 / 201 and of a window of 256 58 / 89, 1,024 of 2,048
+// 395 / 401.
+template <typename T, int D>
+inline bool few_rows(const PromptArgs &a, long long wgs, int times) {
+    long long len = a.T_total / a.B;
+    if (a.window > 0 && a.window < len) len = a.window;
+    len *= times;
+    if (sizeof(T) == 2 && D == 128) return wgs <= 128;
+    if (sizeof(T) == 4 && len >= 2048) return wgs <= 512;
+    return wgs <= (len >= 1024 ? 256 : 128);
 }
 
 // The query head of workgroup number u of a block's Hq: workgroups go to the
@@ -217,6 +244,15 @@ template <int D> struct Rows<bf16, D> {
                 acc[c][e] += fabsf(x) < INFINITY ? 0.f : x;
             }
     }
+    // a row's accumulators into D floats
+    __device__ static inline void put(float *row, const f32x16 (&acc)[kCols], int h) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<f32x4 *>(row + dim(c, e, h)) =
+                    f32x4{acc[c][e], acc[c][e + 1], acc[c][e + 2], acc[c][e + 3]};
+    }
     // acc[.][.] of one row: D / 2 channels from D / 2 h on
     __device__ static inline void store(T *row, const f32x16 (&acc)[kCols], int h, float f) {
 #pragma unroll
@@ -321,6 +357,9 @@ template <int D> struct Rows<float, D> {
                 acc[c][e] += odd(x) ? x : 0.f;
             }
     }
+    __device__ static inline void put(float *row, const f32x16 (&acc)[kCols], int h) {
+        store(row, acc, h, 1.f);
+    }
     __device__ static inline void store(T *row, const f32x16 (&acc)[kCols], int h, float f) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -332,13 +371,49 @@ template <int D> struct Rows<float, D> {
     }
 };
 
+// What the backward pass keeps of a row in its workspace: lse log2 e (+inf for a
+// row without weights) and delta = do . o, of which each half of a wave sums
+// half the channels.
+__device__ inline float base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+template <typename T, int D>
+__device__ inline float row_delta(const T *d_o, const T *o, int h) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 2; i += 8) {
+#pragma unroll
+        for (int u = 0; u < 8; u += 4) {
+            const f32x4 x = Elem<T>::load4(d_o + D / 2 * h + i + u);
+            const f32x4 y = Elem<T>::load4(o + D / 2 * h + i + u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = fmaf(x[e], y[e], s);
+        }
+    }
+    return swap_sum32(s);
+}
+
+// Loads straight from memory into LDS, 16 bytes a lane, in the lanes' order.
+// (Written out: the compiler would wait for a load to LDS before the next read
+// of any LDS.)
+__device__ inline unsigned lds_address(const char *p) {
+    return (unsigned)reinterpret_cast<size_t>((const lds_void *)p);
+}
+// memory from `from` on; what lies at `bytes` and past it comes as zeros
+__device__ inline u32x4 source(const char *from, unsigned bytes) {
+    const unsigned long long base = reinterpret_cast<unsigned long long>(from);
+    return u32x4{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)),
+                 (unsigned)uniform((int)bytes), 0x00020000u};
+}
+__device__ inline void load_lds(unsigned to, u32x4 from, unsigned off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(uniform((int)to)), "v"(off), "s"(from) : "memory");
+}
+
 // Rows row0 .. of a head ([rows, heads, D], heads * D elements apart) into a
 // tile in LDS, by the waves of a workgroup, straight from memory: a wave's
 // instruction fills 1 KiB, 16 bytes a lane in their order, so that the lane
 // asks for the chunk that belongs there.  Rows from `valid` (>= 1) on are
 // copies of the last one, which the callers mask.  What a lane adds to a tile's
-// address is the same for all whole tiles.  (Written out: the compiler would
-// wait for a load to LDS before the next read of any LDS.)
+// address is the same for all whole tiles.
 template <typename T, int D, int WAVES>
 struct Fetch {
     using R = Rows<T, D>;
@@ -359,25 +434,18 @@ struct Fetch {
             off[i] = j * pitch + chunk(j, lane);
         }
     }
-    __device__ inline void load(unsigned to, u32x4 rs, int i, unsigned off) const {
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                     :: "s"(uniform((int)(to + 1024u * (w + WAVES * i)))), "v"(off), "s"(rs)
-                     : "memory");
-    }
     __device__ inline void operator()(char *tile, const T *head, size_t row0, int valid,
                                       int lane) const {
-        const unsigned long long base = reinterpret_cast<unsigned long long>(head) + row0 * pitch;
-        const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)),
-                       0xFFFFFFFFu, 0x00020000u};
-        const unsigned to = (unsigned)reinterpret_cast<size_t>((lds_void *)tile);
+        const u32x4 from = source(reinterpret_cast<const char *>(head) + row0 * pitch, 0xFFFFFFFFu);
+        const unsigned to = lds_address(tile) + 1024u * w;
         if (valid >= R::kTok) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) load(to, rs, i, off[i]);
+            for (int i = 0; i < kLoads; ++i) load_lds(to + 1024u * WAVES * i, from, off[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int j = row(i, w, lane), from = j < valid ? j : valid - 1;
-                load(to, rs, i, from * pitch + chunk(j, lane));
+                const int j = row(i, w, lane), last = j < valid ? j : valid - 1;
+                load_lds(to + 1024u * WAVES * i, from, last * pitch + chunk(j, lane));
             }
         }
     }
@@ -386,10 +454,8 @@ struct Fetch {
 // that lie together in LDS, likewise.
 template <int N>
 __device__ inline void fetch_words(float *to, const float *from, int index, int lane) {
-    const unsigned long long base = reinterpret_cast<unsigned long long>(from);
-    const u32x4 rs{(unsigned)uniform((int)base), (unsigned)uniform((int)(base >> 32)), 0xFFFFFFFFu,
-                   0x00020000u};
-    const unsigned at = (unsigned)uniform((int)reinterpret_cast<size_t>((lds_void *)to));
+    const u32x4 rs = source(reinterpret_cast<const char *>(from), 0xFFFFFFFFu);
+    const int at = uniform((int)lds_address(reinterpret_cast<const char *>(to)));
     if (lane < N)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                      :: "s"(at), "v"(4u * index), "s"(rs) : "memory");

@@ -127,6 +127,12 @@ SHAPES = [
     (64, 2, 1, 64),
     (128, 1, 1, 129),
     (64, 3, 1, 1000),
+    # (many heads: blocks of 128 rows in place of 32)
+    (128, 9, 1, 0),
+    (64, 9, 1, 0),
+    (128, 8, 2, 50),
+    (64, 10, 1, 64),
+    (128, 9, 1, 129),
 ]
 
 
@@ -164,14 +170,17 @@ def test_many_sequences():
     lens[4321], lens[0], lens[-1] = 200, 0, 70
     data = make(lens, 2, 1, 64, torch.bfloat16, seed=6, tail=5)
     check(data, lens, 0.125, what="5,000 sequences")
+    lens = lens[:100]
+    data = make(lens, 2, 1, 64, torch.float32, seed=6, tail=5)
+    check(data, lens, 0.125, what="100 sequences")
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
-@pytest.mark.parametrize("window", [0, 40])
-def test_masked_values(dt, window):
+@pytest.mark.parametrize("window,H", [(0, 2), (40, 2), (0, 30), (40, 30)])
+def test_masked_values(dt, window, H):
     """Infinities and NaN of tokens that a row does not attend to have no part
     in its results; those that it attends to have."""
-    lens, D, H = [150, 90, 70], 64, 2
+    lens, D = [150, 90, 70], 64
     cu = offsets(lens)
     data = make(lens, H, H, D, DTYPES[dt], seed=8)
     clean = check(data, lens, D ** -0.5, window, what="clean")
@@ -242,6 +251,9 @@ def test_long():
     data = make([T], 2, 1, D, torch.bfloat16, seed=11)
     check(data, [T], D ** -0.5, what="5,000 tokens")
     check(data, [T], D ** -0.5, 700, what="a window of 700")
+    for dt in (torch.float32, torch.bfloat16):
+        data = make([2100], 8, 8, D, dt, seed=12)
+        check(data, [2100], D ** -0.5, what="8 heads")
 
 
 def test_bad_offsets_stay_inside():
