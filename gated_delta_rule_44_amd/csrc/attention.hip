@@ -700,19 +700,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         const size_t qb = (size_t)b * a.n * a.Hq * D;
         const rsrc_t rq = make_rsrc(static_cast<const T *>(a.q) + qb, 0xFFFFFFFFu);
         const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0;
-        if constexpr (TREE) {
-            // (a place's span, but its lower end from the position)
-            const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
-            const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
-            const int depth = __shfl(y.depth, t);
-            drafts = (unsigned long long)hi << 32 | lo;
-            if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
-        } else {
-            if (row < rows) sp = token_span(len, a.n, a.window, t);
-        }
+        if (!TREE && row < rows) sp = token_span(len, a.n, a.window, t);
         TL::load_q(q, rq, (unsigned)(t * a.Hq + h * a.G + hg) * (D * (unsigned)sizeof(T)), lane);
         if (k.negative) TL::negate(q);
     }
+    // a draft's span and way, found while the first tiles are on their way (a
+    // place's span, but its lower end from the position)
+    auto find_way = [&]() {
+        const int t = row < rows ? row / a.G : 0;
+        const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
+        const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
+        const int depth = __shfl(y.depth, t);
+        drafts = (unsigned long long)hi << 32 | lo;
+        if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
+    };
     auto attends = [&](int j) {
         bool in = j >= sp.lo && j < sp.hi;
         if constexpr (TREE) in = in && (j < ctx || (drafts >> ((j - ctx) & 63) & 1));
@@ -883,6 +884,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
             load_k(s1);
             load_v(s1);
         }
+        if constexpr (TREE) find_way();
         for (int i = w; i < tiles; i += kWaves) {
             work(i, s0);
             if constexpr (kTwo) {
@@ -1062,14 +1064,14 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
     R::load(q, static_cast<const T *>(a.q) + (((size_t)b * a.n + t) * a.Hq + head * a.G + hg) * D, h);
     if (k.negative) R::negate(q);
     Span sp{0, 0};
-    unsigned long long drafts;
-    {
+    unsigned long long drafts = 0;
+    auto find_way = [&]() GDR_INLINE {
         const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
         const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
         const int depth = __shfl(y.depth, t);
         drafts = (unsigned long long)hi << 32 | lo;
         if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
-    }
+    };
     // the slot's tokens [k_lo, k_hi), in tiles from base on; all rows of the
     // block attend to those of [all_lo, ctx)
     const int c_lo = seq.lo + (slot - sl.first) * sl.chunk;
@@ -1136,6 +1138,7 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
         if (CLEAR) pages_after = load_pages(0);
         if (tiles > 0) stage(0);
         R::settle(q);
+        if (!CLEAR) find_way();
         for (int i = 0; i < tiles; ++i) {
             there = there_next;
             tile_landed();

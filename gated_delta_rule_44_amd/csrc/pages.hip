@@ -124,24 +124,26 @@ hipError_t accept(const AcceptArgs &a, hipStream_t s) {
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kGroup = 16;                       // words of a group of pages
 constexpr int kWords = kMaxPages / 32, kGroups = kWords / kGroup;
-constexpr int kRowsAtOnce = 8;                   // rows whose entries a wave requests together
+constexpr int kRowsAtOnce = 16;                  // rows whose entries a wave requests together
 
-// Sums over the workgroup's threads before this one; total: over all.
-__device__ inline long long scan(long long x, long long &total, long long *lds) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    long long incl = x;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const long long y = __shfl_up(incl, m);
-        if (lane >= m) incl += y;
-    }
-    if (lane == 63) lds[w] = incl;
+// Sums over the workgroup's threads before this one; total: over all.  Within a
+// wave by DPP: shifts within rows of 16 lanes, then the rows' last lanes.
+__device__ inline int scan(int x, int &total, int *lds) {
+    const int w = threadIdx.x >> 6;
+    int incl = x;
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, true);      // row_shr:1
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);     // row_bcast:15
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);     // row_bcast:31
+    if ((threadIdx.x & 63) == 63) lds[w] = incl;
     __syncthreads();
-    long long before = 0;
+    int before = 0;
     total = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-        const long long v = lds[i];
+        const int v = lds[i];
         before += i < w ? v : 0;
         total += v;
     }
@@ -152,75 +154,82 @@ __device__ inline long long scan(long long x, long long &total, long long *lds) 
 // One workgroup does all, as each step needs the whole of the one before: the
 // pages that some row keeps, as bits in LDS; how many are free in the groups of
 // 512 before each; and, 1,024 rows at a time, which rows are served, from the
-// sums of what they ask for, and their entries.  An entry's page is the free
-// one of its number: a search over the groups' sums, then within one group.
+// sums of what they ask for, and the new entries, a thread each, whatever rows
+// they are of.  An entry's page is the free one of its number: a search over the
+// groups' sums, then within one group.  Latency bounds it (256 rows of up to 128
+// pages: 9 us, 4 rows 4.6).
 __global__ __launch_bounds__(kThreads) void resize_kernel(ResizeArgs a) {
     __shared__ __align__(16) unsigned used[kWords];
     __shared__ int free_before[kGroups];
-    __shared__ int have[kThreads], need[kThreads], first[kThreads];
-    __shared__ long long sums[kWaves];
+    __shared__ int keeps[kThreads], have[kThreads], first[kThreads];
+    __shared__ int sums[kWaves], given;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int groups = (a.num_pages + 32 * kGroup - 1) / (32 * kGroup), words = groups * kGroup;
     const long long cap = (long long)a.max_pages * a.page_size;
-    auto held = [&](const int32_t *lens, int b) {
-        const int l = lens[b];
-        return (int)(l < 0 ? 0 : (l > cap ? cap : l));
-    };
+    const int shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz(a.page_size) : -1;
     auto pages = [&](int tokens) {
-        return (int)(((long long)tokens + a.page_size - 1) / a.page_size);
+        const long long n = (long long)tokens + a.page_size - 1;
+        return (int)(shift >= 0 ? n >> shift : n / a.page_size);
+    };
+    // a row's lengths, in tokens and in pages
+    int old = 0, now = 0, x = 0, y = 0;
+    auto load = [&](int b) {
+        old = now = x = y = 0;
+        if (b < a.B) {
+            const int l = a.seq_lens[b], m = a.want[b];
+            old = (int)(l < 0 ? 0 : (l > cap ? cap : l));
+            now = (int)(m < 0 ? 0 : (m > cap ? cap : m));
+            x = pages(old);
+            y = pages(now);
+        }
     };
     for (int i = tid; i < words; i += kThreads) {
         const int left = a.num_pages - 32 * i;            // bits past the last page are taken
         used[i] = left >= 32 ? 0u : (left <= 0 ? ~0u : ~0u << left);
     }
-    // entries of the rows from row0 on, lo .. hi of each, a wave's rows together
-    auto entries = [&](int row0, const int *lo, const int *hi, auto &&f) {
+    if (tid == 0) given = 0;
+    for (int row0 = 0; row0 < a.B; row0 += kThreads) {
+        load(row0 + tid);
+        keeps[tid] = x < y ? x : y;
+        __syncthreads();
         for (int r0 = w * kRowsAtOnce; r0 < kThreads && row0 + r0 < a.B; r0 += kWaves * kRowsAtOnce) {
-            int longest = 0;
+            // (a lane's row's entries, and the longest of the 16)
+            int keep[kRowsAtOnce], longest = 0;
 #pragma unroll
             for (int u = 0; u < kRowsAtOnce; ++u) {
-                const int n = hi[r0 + u] - (lo ? lo[r0 + u] : 0);
-                longest = n > longest ? n : longest;
+                keep[u] = keeps[r0 + u];
+                longest = keep[u] > longest ? keep[u] : longest;
             }
-            for (int c = lane; c < longest + lane; c += 64) f(r0, c);
-        }
-    };
-    for (int row0 = 0; row0 < a.B; row0 += kThreads) {
-        const int b = row0 + tid;
-        int keep = 0;
-        if (b < a.B) {
-            const int x = pages(held(a.seq_lens, b)), y = pages(held(a.want, b));
-            keep = x < y ? x : y;
-        }
-        have[tid] = keep;
-        __syncthreads();
-        entries(row0, nullptr, have, [&](int r0, int c) {
-            int page[kRowsAtOnce];
+            const int32_t *rows = a.table + (size_t)(row0 + r0) * a.max_pages;
+            for (int c0 = 0; c0 < longest; c0 += 64) {
+                const int c = c0 + lane;
+                int page[kRowsAtOnce];
 #pragma unroll
-            for (int u = 0; u < kRowsAtOnce; ++u)
-                page[u] = c < have[r0 + u]
-                              ? a.table[(size_t)(row0 + r0 + u) * a.max_pages + c] : -1;
+                for (int u = 0; u < kRowsAtOnce; ++u)
+                    page[u] = c < keep[u] ? rows[(size_t)u * a.max_pages + c] : -1;
 #pragma unroll
-            for (int u = 0; u < kRowsAtOnce; ++u)
-                if ((unsigned)page[u] < (unsigned)a.num_pages)
-                    atomicOr(&used[page[u] >> 5], 1u << (page[u] & 31));
-        });
+                for (int u = 0; u < kRowsAtOnce; ++u)
+                    if ((unsigned)page[u] < (unsigned)a.num_pages)
+                        atomicOr(&used[page[u] >> 5], 1u << (page[u] & 31));
+            }
+        }
         __syncthreads();
     }
     __syncthreads();
     int free_all = 0;
     for (int g0 = 0; g0 < groups; g0 += kThreads) {
-        int n = 0;
+        int n = 0, total;
         if (g0 + tid < groups) {
+            const u32x4 *word = reinterpret_cast<const u32x4 *>(used + (g0 + tid) * kGroup);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) n += __builtin_popcount(~used[(g0 + tid) * kGroup + i]);
+            for (int i = 0; i < kGroup / 4; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) n += __builtin_popcount(~word[i][u]);
         }
-        long long total;
-        const int before = (int)scan(n, total, sums);
+        const int before = scan(n, total, sums);
         if (g0 + tid < groups) free_before[g0 + tid] = free_all + before;
-        free_all += (int)total;
+        free_all += total;
     }
-    __syncthreads();
     // the free page of number k < free_all
     auto free_page = [&](int k) {
         int lo = 0, n = groups;                           // the last group with free_before <= k
@@ -231,76 +240,81 @@ __global__ __launch_bounds__(kThreads) void resize_kernel(ResizeArgs a) {
             n = up ? n - half : half;
         }
         k -= free_before[lo];
+        const u32x4 *group = reinterpret_cast<const u32x4 *>(used + lo * kGroup);
         unsigned word = 0;
-        int at = 0, seen = 0;
+        int at = 0;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-            const unsigned x = ~used[lo * kGroup + i];
-            const int c = __builtin_popcount(x);
-            if (seen <= k && k < seen + c) {
-                word = x;
-                at = i;
-                k -= seen;
-                seen = 1 << 30;
+            const unsigned f = ~group[i / 4][i % 4];
+            const int c = __builtin_popcount(f);
+            if (k >= 0 && k < c) {
+                word = f;
+                at = i | k << 8;
             }
-            seen += c;
+            k -= c;
         }
-        int bit = 0;
+        int bit = 0, left = at >> 8;
+        at &= 255;
 #pragma unroll
         for (int half = 16; half; half >>= 1) {
             const int c = __builtin_popcount(word >> bit & ((1u << half) - 1));
-            if (k >= c) {
-                k -= c;
+            if (left >= c) {
+                left -= c;
                 bit += half;
             }
         }
         return 32 * (lo * kGroup + at) + bit;
     };
-    long long asked = 0, grown = 0;
-    int given = 0;
+    int asked = 0, grown = 0, done = 0;
     for (int row0 = 0; row0 < a.B; row0 += kThreads) {
         const int b = row0 + tid;
-        int old = 0, now = 0, x = 0, y = 0;
-        if (b < a.B) {
-            old = held(a.seq_lens, b);
-            now = held(a.want, b);
-            x = pages(old);
-            y = pages(now);
-        }
-        const int more = y > x ? y - x : 0;
-        long long all;
-        const long long before = asked + scan(more, all, sums);
-        asked += all;
+        if (a.B > kThreads) load(b);
+        // (a row that asks for more than there are is not served, nor any after
+        // it: sums of 1,024 such numbers are below 2^31)
+        int all, more = y > x ? y - x : 0;
+        more = more > a.num_pages ? a.num_pages + 1 : more;
+        const int before = asked + scan(more, all, sums);
+        asked = asked + all < 1 << 29 ? asked + all : 1 << 29;
         // what is asked for only grows, so that every row served before this one
         // got all that was asked for up to it
-        const bool served = more == 0 || before + more <= free_all;
+        const bool served = more == 0 || (before <= free_all && before + more <= free_all);
         if (!served) {
             now = old;
             y = x;
         }
         have[tid] = x;
-        need[tid] = y;
-        first[tid] = served && more ? (int)before : 0;
-        const long long up = scan(now > old ? now - old : 0, all, sums);
+        first[tid] = before;
+        if (served && more) atomicMax(&given, before + more);
+        const int up = scan(now > old ? now - old : 0, all, sums);    // (and LDS is written)
         if (b < a.B) {
             a.new_lens[b] = now;
-            if (a.cu_seqlens) a.cu_seqlens[b] = (int)(grown + up);
+            if (a.cu_seqlens) a.cu_seqlens[b] = grown + up;
         }
         grown += all;
-        scan(served ? more : 0, all, sums);               // (and have, need, first are there)
-        given += (int)all;
-        // columns past the shorter of the two lengths: new pages, or none
-        for (int r = w; r < kThreads && row0 + r < a.B; r += kWaves) {
-            const int x = have[r], y = need[r];
-            int32_t *row = a.table + (size_t)(row0 + r) * a.max_pages;
-            for (int c = x + lane; c < y; c += 64) row[c] = free_page(first[r] + c - x);
-            for (int c = y + lane; c < x; c += 64) row[c] = -1;
+        // the new entries, whose numbers are their free pages': of the last row
+        // that starts at or before a number
+        const int end = given;
+        for (int n = done + tid; n < end; n += kThreads) {
+            int r = 0;
+#pragma unroll
+            for (int half = kThreads / 2; half; half >>= 1) r = first[r + half] <= n ? r + half : r;
+            a.table[(size_t)(row0 + r) * a.max_pages + have[r] + n - first[r]] = free_page(n);
+        }
+        done = end;
+        // the dropped ones, a wave's rows in turn
+        unsigned long long drops = __builtin_amdgcn_ballot_w64(x > y);
+        while (drops) {
+            const int u = __builtin_ctzll(drops);
+            drops &= drops - 1;
+            const int from = __builtin_amdgcn_readlane(y, u), to = __builtin_amdgcn_readlane(x, u);
+            int32_t *row = a.table + (size_t)(row0 + 64 * w + u) * a.max_pages;
+            for (int c = from + lane; c < to; c += 64) row[c] = -1;
         }
         __syncthreads();
     }
     if (tid == 0) {
-        if (a.cu_seqlens) a.cu_seqlens[a.B] = (int)grown;
-        if (a.free_pages) a.free_pages[0] = free_all - given;
+        if (a.cu_seqlens) a.cu_seqlens[a.B] = grown;
+        if (a.free_pages) a.free_pages[0] = free_all - done;
     }
 }
 

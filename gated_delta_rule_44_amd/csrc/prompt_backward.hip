@@ -230,22 +230,22 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
 // wave then has 64 accumulators instead of 128, and two waves share a SIMD:
 // one's exponentials run under the other's products.  A tile's sums are formed
 // while the next one's w and ds are, so that one barrier a tile orders all.
-template <int D>
-__global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
+template <int D, int PAIRS>
+__global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
     typedef bf16 T;
     using R = Rows<T, D>;
-    constexpr int kTok = R::kTok, kCols = R::kCols;
+    constexpr int kTok = R::kTok, kCols = R::kCols, kTokens = 32 * PAIRS;
     static_assert(kTok == 64, "a half of the rows each");
     __shared__ __align__(1024) char lds[3][2][R::kTileBytes];
-    __shared__ __align__(16) bf16x8 given[2][2][kWaves][2][64];   // [n & 1][role][pair]
+    __shared__ __align__(16) bf16x8 given[2][2][PAIRS][2][64];   // [n & 1][role][pair]
     __shared__ __align__(16) float stats[3][2][kTok];
     const PromptArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
-    const int w = uniform(tid >> 6), pair = w % kWaves, role = w / kWaves;
+    const int w = uniform(tid >> 6), pair = w % PAIRS, role = w / PAIRS;
     const int hk = blockIdx.x % a.Hkv;
-    const Block bl = find_block<kRows>(a, blockIdx.x / a.Hkv);
+    const Block bl = find_block<kTokens>(a, blockIdx.x / a.Hkv);
     if (bl.i < 0) return;
-    const int j0 = bl.i * kRows, jw = j0 + 32 * pair, j = jw + r;
+    const int j0 = bl.i * kTokens, jw = j0 + 32 * pair, j = jw + r;
     const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
     const typename R::At at = R::at(lane);
 
@@ -254,11 +254,11 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
     R::load(kf, static_cast<const T *>(a.k) + ((size_t)row * a.Hkv + hk) * D, h);
     R::load(vf, static_cast<const T *>(a.v) + ((size_t)row * a.Hkv + hk) * D, h);
     const unsigned span = a.window > 0 ? a.window : 1u << 31;     // tokens a row attends to
-    const int over = a.window > 0 && bl.len - j0 > kRows + a.window - 1 ? j0 + kRows + a.window - 1
+    const int over = a.window > 0 && bl.len - j0 > kTokens + a.window - 1 ? j0 + kTokens + a.window - 1
                                                                          : bl.len;
     const int t0 = j0 / kTok, tiles = (over - 1) / kTok + 1 - t0, all = tiles * a.G;
 
-    const Fetch<T, D, 2 * kWaves> fetch(qpitch, w, lane);
+    const Fetch<T, D, 2 * PAIRS> fetch(qpitch, w, lane);
     // the tiles in their order, head by head: where the next to be fetched is
     const int t1 = t0 + tiles;
     int next_head, next_t;
@@ -392,6 +392,11 @@ __global__ __launch_bounds__(2 * kThreads, 2) void key_pairs_kernel(KArgs k) {
     else      R::store(static_cast<T *>(a.dv) + to, acc, h, 1.f);
 }
 
+// Pairs of a workgroup.  Of 128 channels four fill a CU's LDS; of 64, two
+// workgroups of two fit, each with barriers of its own (12 sequences of 300 to
+// 6,100 tokens, window 512, 16 heads: both kernels 313 us, 351 with four).
+template <int D> constexpr int kPairs = D == 128 ? 4 : 2;
+
 template <typename T, int D>
 hipError_t launch(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
@@ -411,7 +416,8 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (few_rows<T, D>(a, blocks * a.Hkv, a.G)) return launch_keys_short(sizeof(T) == 2, D, a, s);
     if constexpr (sizeof(T) == 2)
-        key_pairs_kernel<D><<<(unsigned)(blocks * a.Hkv), 2 * kThreads, 0, s>>>(k);
+        key_pairs_kernel<D, kPairs<D>><<<(unsigned)(block_bound<32 * kPairs<D>>(a) * a.Hkv),
+                                         128 * kPairs<D>, 0, s>>>(k);
     else
         key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
     return hipGetLastError();
