@@ -1030,26 +1030,37 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     }
 }
 
-// A tree's rows past 32, in bf16: a workgroup of W waves with 32 rows each, all
-// of them on every tile of 64 tokens, which passes through LDS, two tiles there,
-// the next on its way while one is worked on.  The products, the running maximum
+template <int W> constexpr int kTreeShares = W == 2 ? 2 : 1;
+
+// A tree's rows past 32, in bf16: a workgroup of W tiles of 32 rows, all of them
+// on every tile of 64 tokens, which passes through LDS, two tiles there, the next
+// on its way while one is worked on.  Two tiles of rows are two waves each, for a
+// half of the tokens, joined at the end: the card is as busy with long contexts
+// (64 rows, 32 contexts of 512 to 8,192: 96 us either way) and sooner done with
+// short ones (4 of 300 to 900: 19 us, 24 with one); three in this way are slower
+// (96 rows, 32 contexts: 121 us, 106 with one), as are 4, of too many registers.
+// The products, the running maximum
 // and sum and what is done about infinities are those of the attention of whole
 // prompts (prompt.hip); a weight enters the product with V as one bf16 number,
 // 2^-8 off at most.
 template <int D, int W>
-__global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k) {
+__global__ __launch_bounds__(64 * W * kTreeShares<W>, 2) void tree_kernel(KArgs k) {
     typedef bf16 T;
     using R = Rows<T, D>;
-    constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols, kRows = 32 * W;
+    constexpr int kShares = kTreeShares<W>, kWaves = W * kShares;
+    constexpr int kTok = R::kTok, kBlk = kTok / 32 / kShares, kCols = R::kCols, kRows = 32 * W;
+    constexpr int kPad = D + 4;
     constexpr int kPer = 1024 / R::kRowBytes;         // rows of a load
     __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
+    __shared__ float2 other[W][32];            // (m, l) of the second share
+    static_assert(kShares == 1 || W * 32 * kPad * 4 <= (int)sizeof(lds), "its o");
     const AttnArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
-    const int w = uniform(tid >> 6);
+    const int w = uniform(tid >> 6), rt = w % W, share = w / W;
     const int wg = blockIdx.x, rb = wg / 8 % k.plan.row_blocks;
     const int unit = wg / 8 / k.plan.row_blocks * 8 + wg % 8;
     const int slot = unit / a.Hkv, head = unit % a.Hkv;
-    const Slot sl = find_slot<W>(k, slot);
+    const Slot sl = find_slot<kWaves>(k, slot);
     const int b = sl.b;
     if (b < 0) return;
     const int len = uniform(cached_len(a.seq_lens, b, a.map));
@@ -1057,7 +1068,7 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
     if (k.sched && head == 0 && rb == 0 && slot == sl.first && tid == 0)
         k.sched[b] = int2{sl.first, sl.count};
 
-    const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + 32 * w + r;
+    const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + 32 * rt + r;
     const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0, ctx = len - a.n;
     const typename R::At at = R::at(lane);
     typename R::B q;
@@ -1087,39 +1098,52 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
                (j < ctx | (int)(drafts >> ((j - ctx) & 63) & 1));
     };
 
-    // pages of the blocks of 16 tokens of 16 tiles, a lane each (-1: absent, or
-    // past the tokens), and of the 16 tiles after them
-    auto load_pages = [&](int i0) GDR_INLINE {
+    // Where the blocks of 16 tokens of 16 tiles lie in the caches, a lane each,
+    // and how much of them is there (0: absent, or past the tokens); and those of
+    // the 16 tiles after them.
+    struct Blocks { unsigned lo, hi, bytes; };
+    const size_t page_bytes = (size_t)R::kRowBytes << a.map.page_shift;
+    auto find_blocks = [&](int i0) GDR_INLINE {
         const int j = base + i0 * kTok + 16 * lane;
-        return i0 < tiles && j < k_hi ? page_of(a.map, b, j) : -1;
+        Blocks x{0, 0, 0};
+        if (i0 < tiles && j < k_hi) {
+            const int page = page_of(a.map, b, j), valid = len - j < 16 ? len - j : 16;
+            if (page >= 0 && valid > 0) {
+                const size_t from = ((size_t)page * a.Hkv + head) * page_bytes +
+                                    (size_t)slot_of(a.map, j) * R::kRowBytes;
+                x = Blocks{(unsigned)from, (unsigned)(from >> 32), (unsigned)(valid * R::kRowBytes)};
+            }
+        }
+        return x;
     };
-    int pages = -1, pages_after = load_pages(0);
+    Blocks blocks{0, 0, 0}, blocks_after = find_blocks(0);
     // The tile i into LDS.  Rows that are not there come as zeros: the loads'
     // bounds end before them.
     const char *kc = static_cast<const char *>(a.k_cache), *vc = static_cast<const char *>(a.v_cache);
-    const size_t page_bytes = (size_t)R::kRowBytes << a.map.page_shift;
     unsigned there = 0, there_next = 0;      // blocks of 16 tokens of the tile at hand, of the next
-    const int lrow = lane / R::kChunks;
+    constexpr int kLoads = (kTok / kPer + kWaves - 1) / kWaves;
+    unsigned off[kLoads];                    // within a block
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+        const int j = (w + kWaves * u) * kPer + lane / R::kChunks;
+        off[u] = (j & 15) * R::kRowBytes + 16u * (lane % R::kChunks ^ R::swz(j));
+    }
     auto stage = [&](int i) GDR_INLINE {
         if ((i & 15) == 0) {
-            pages = pages_after;
-            pages_after = load_pages(i + 16);
+            blocks = blocks_after;
+            blocks_after = find_blocks(i + 16);
         }
-        there_next = (unsigned)(__builtin_amdgcn_ballot_w64(pages >= 0) >> (4 * (i & 15))) & 15u;
+        there_next = (unsigned)(__builtin_amdgcn_ballot_w64(blocks.bytes != 0) >> (4 * (i & 15))) & 15u;
         const unsigned to = lds_address(lds[i & 1][0]);
 #pragma unroll
-        for (int n = w; n < kTok / kPer; n += W) {
-            const int blk = n * kPer / 16, j0 = base + i * kTok + 16 * blk;
-            const int page = __builtin_amdgcn_readlane(pages, 4 * (i & 15) + blk);
-            const int valid = len - j0 < 16 ? len - j0 : 16;
-            const bool some = page >= 0 && valid > 0;
-            const size_t from = some ? ((size_t)page * a.Hkv + head) * page_bytes +
-                                           (size_t)slot_of(a.map, j0) * R::kRowBytes : 0;
-            const unsigned bytes = some ? (unsigned)(valid * R::kRowBytes) : 0u;
-            const int j = n * kPer + lrow;
-            const unsigned off = (j & 15) * R::kRowBytes + 16u * (lane % R::kChunks ^ R::swz(j));
-            load_lds(to + 1024u * n, source(kc + from, bytes), off);
-            load_lds(to + R::kTileBytes + 1024u * n, source(vc + from, bytes), off);
+        for (int u = 0; u < kLoads; ++u) {
+            const int n = w + kWaves * u, at_lane = 4 * (i & 15) + n * kPer / 16;
+            if (n >= kTok / kPer) break;
+            const size_t from = (size_t)(unsigned)__builtin_amdgcn_readlane(blocks.hi, at_lane) << 32 |
+                                (unsigned)__builtin_amdgcn_readlane(blocks.lo, at_lane);
+            const unsigned bytes = __builtin_amdgcn_readlane(blocks.bytes, at_lane);
+            load_lds(to + 1024u * n, source(kc + from, bytes), off[u]);
+            load_lds(to + R::kTileBytes + 1024u * n, source(vc + from, bytes), off[u]);
         }
     };
     auto whole = [&](int i) GDR_INLINE {
@@ -1135,7 +1159,7 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[c][e] = 0.f;
-        if (CLEAR) pages_after = load_pages(0);
+        if (CLEAR) blocks_after = find_blocks(0);
         if (tiles > 0) stage(0);
         R::settle(q);
         if (!CLEAR) find_way();
@@ -1143,7 +1167,11 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
             there = there_next;
             tile_landed();
             if (i + 1 < tiles) stage(i + 1);
-            const char *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+            // this share's blocks of 32 tokens
+            const int j0 = base + i * kTok + 32 * kBlk * share;
+            const char *kt = lds[i & 1][0] + 32 * kBlk * share * R::kRowBytes;
+            const char *vt = kt + R::kTileBytes;
+            const unsigned here = there >> (2 * kBlk * share);
             const bool full = whole(i) & there == 15u;
             f32x16 x[kBlk];
 #pragma unroll
@@ -1153,8 +1181,8 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
                 for (int c = 0; c < kBlk; ++c)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const bool in = attends(base + i * kTok + 32 * c + R::key(e, h)) &
-                                        (int)(there >> (2 * c + (e >> 3)) & 1);
+                        const bool in = attends(j0 + 32 * c + R::key(e, h)) &
+                                        (int)(here >> (2 * c + (e >> 3)) & 1);
                         x[c][e] = in ? x[c][e] : -INFINITY;
                     }
             }
@@ -1189,6 +1217,7 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
     if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
         walk(std::true_type{});
         for (int j = k_lo; j < k_hi; ++j) {
+            if ((j - base) % kTok / (32 * kBlk) != share) continue;
             if (whole((j - base) / kTok)) {          // (unless a page of it is absent)
                 bool all = true;
                 const int j0 = base + (j - base) / kTok * kTok;
@@ -1201,8 +1230,31 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
                                     cache_row(a.map, a.Hkv, page, head, slot_of(a.map, j)) * D, h);
         }
     }
-    if (row >= rows) return;
     l = swap_sum32(l);
+    if constexpr (kShares == 2) {
+        float *so = reinterpret_cast<float *>(lds) + (32 * rt + r) * kPad;
+        __syncthreads();
+        if (share) {
+            R::put(so, acc, h);
+            if (h == 0) other[rt][r] = float2{m, l};
+        }
+        __syncthreads();
+        if (share) return;
+        const float2 o = other[rt][r];
+        const float mn = fmaxf(m, o.x), ms = finite_top(mn);
+        const float f = exp2_((m - ms) * k.c), fo = exp2_((o.x - ms) * k.c);
+        m = mn;
+        l = l * f + o.y * fo;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const f32x4 y = *reinterpret_cast<const f32x4 *>(so + R::dim(c, e, h));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[c][e + u] = acc[c][e + u] * f + y[u] * fo;
+            }
+    }
+    if (row >= rows) return;
     if (sl.count == 1) {
         if (l == 0.f) {
 #pragma unroll
@@ -1215,7 +1267,7 @@ __global__ __launch_bounds__(64 * W, (W == 2 ? 1 : 2)) void tree_kernel(KArgs k)
         return;
     }
     const size_t part = ((size_t)slot * k.plan.units + head * k.plan.row_blocks + rb) * kRows +
-                        32 * w + r;
+                        32 * rt + r;
     if (h == 0) k.ml[part] = float2{m, l};
 #pragma unroll
     for (int c = 0; c < kCols; ++c)
@@ -1402,7 +1454,7 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     const long long pairs = ((long long)k.plan.max_slots * a.Hkv + 7) / 8 * 8;
     const unsigned grid = (unsigned)(pairs * k.plan.row_blocks);
     if constexpr (TREE && RW == 32 && RT >= 2)
-        tree_kernel<D, RT><<<grid, 64 * RT, 0, s>>>(k);
+        tree_kernel<D, RT><<<grid, 64 * RT * kTreeShares<RT>, 0, s>>>(k);
     else if (k.plan.row_blocks == 1)
         attn_kernel<T, D, RW, RT, true, TREE><<<grid, kThreads, 0, s>>>(k);
     else
