@@ -1038,7 +1038,7 @@ template <int W> constexpr int kTreeShares = W == 2 ? 2 : 1;
 // half of the tokens, joined at the end: the card is as busy with long contexts
 // (64 rows, 32 contexts of 512 to 8,192: 96 us either way) and sooner done with
 // short ones (4 of 300 to 900: 19 us, 24 with one); three in this way are slower
-// (96 rows, 32 contexts: 121 us, 106 with one), as are 4, of too many registers.
+// (96 rows, 32 contexts: 121 us, 106 with one).
 // The products, the running maximum
 // and sum and what is done about infinities are those of the attention of whole
 // prompts (prompt.hip); a weight enters the product with V as one bf16 number,

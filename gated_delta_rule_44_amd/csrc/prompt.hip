@@ -93,6 +93,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
             f32x16 x[kBlk];
 #pragma unroll
             for (int b = 0; b < kBlk; ++b) x[b] = R::rows(kt, b, at, q);
+            R::template ahead<kBlk>();
             const bool full = tile_full(t);
             if (!full) {
 #pragma unroll

@@ -401,7 +401,7 @@ template <typename T, int D>
 hipError_t launch(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
-    k.c = a.scale * kLog2e;
+    k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     const long long blocks = block_bound<kRows>(a);
     k.blocks = (int)blocks;
     k.lse2 = static_cast<float *>(a.ws);

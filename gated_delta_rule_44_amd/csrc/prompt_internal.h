@@ -186,6 +186,20 @@ template <int D> struct Rows<bf16, D> {
         }
         return s;
     }
+    // After `rows` of N blocks: six of the reads from LDS go ahead of the products
+    // that need them (16 packed prompts of 512 to 8,192 tokens, 32 heads over 8 of
+    // 128: 1,722 us, 1,765 in the compiler's order).
+    template <int N>
+    __device__ static inline void ahead() {
+        constexpr int kMfma = 0x8, kRead = 0x100, kAll = N * D / 16;
+        __builtin_amdgcn_sched_group_barrier(kRead, 6, 0);
+#pragma unroll
+        for (int i = 0; i < kAll - 6; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kMfma, 6, 0);
+    }
     struct P { bf16x8 f[2]; };
     __device__ static inline P operand(const f32x16 &x) {
         P p;
@@ -316,6 +330,7 @@ template <int D> struct Rows<float, D> {
         }
         return s + t;
     }
+    template <int N> __device__ static inline void ahead() {}
     struct P { f32x16 f; };
     __device__ static inline P operand(const f32x16 &x) { return P{x}; }
     typedef float run_t __attribute__((ext_vector_type(kCols)));

@@ -416,7 +416,7 @@ template <typename T, int D>
 hipError_t backward_q(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
-    k.c = a.scale * kLog2e;
+    k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
     k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
@@ -428,7 +428,7 @@ template <typename T, int D>
 hipError_t backward_k(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
-    k.c = a.scale * kLog2e;
+    k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
     k.delta = k.lse2 + (size_t)a.Hq * a.T_total;

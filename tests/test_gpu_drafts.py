@@ -157,13 +157,14 @@ def test_tree_bad_parents():
                parents.astype(np.int32), 0.125, what="bad parents")
 
 
-@pytest.mark.parametrize("dt", ["fp32", "bf16"])
-def test_tree_masked_values(dt):
+@pytest.mark.parametrize("dt,G", [("fp32", 2), ("bf16", 2), ("bf16", 8), ("bf16", 14), ("bf16", 20),
+                                  ("bf16", 40)])
+def test_tree_masked_values(dt, G):
     """Infinities and NaN of drafts on other ways and of tokens outside the
     window have no part in a row; on its own way they have."""
     lens, n, D, window = [100, 90], 6, 64, 30
     kc, vc, _, table = make_cache(lens, 2, D, 16, DTYPES[dt], seed=9)
-    q = queries(2, n, 4, D, DTYPES[dt], 10)
+    q = queries(2, n, 2 * G, D, DTYPES[dt], 10)
     parents = np.array([[-1, 0, 0, 1, 2, 3]] * 2)
     args = (table, lens, parents, 0.125, window)
     clean = check_tree(q, kc, vc, *args, what="clean")
