@@ -1487,13 +1487,11 @@ hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
         default: return launch<bf16, D, 32, 4, true>(a, s);
         }
     }
-    switch (block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window)) {
-    case 16: return launch<bf16, D, 16, 1, TREE>(a, s);
-    case 32: return launch<bf16, D, 32, 1, TREE>(a, s);
-    default:
-        if constexpr (TREE) return hipErrorInvalidValue;      // (rows past 32: above)
-        else return launch<bf16, D, 32, 2, false>(a, s);
-    }
+    const int block = block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window);
+    if (block == 16) return launch<bf16, D, 16, 1, TREE>(a, s);
+    if constexpr (!TREE)
+        if (block == 64) return launch<bf16, D, 32, 2, false>(a, s);
+    return launch<bf16, D, 32, 1, TREE>(a, s);
 }
 
 }  // namespace

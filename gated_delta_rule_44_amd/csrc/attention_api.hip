@@ -53,10 +53,10 @@ gdr_status check_prompts(const char *what, int dt, int B, int T, int T_total, in
                     (long long)B * T);
     if ((long long)Hq * D > (1 << 20))
         return fail(GDR_EUNSUPPORTED, "%s: %d heads of %d are too wide", what, Hq, D);
-    // a launch holds fewer than 2^32 threads: 256 for 128 rows of a head, and a
-    // sequence may leave one block unused
-    if (T_total >= (1 << 30) || B >= (1 << 24) || (long long)T_total * Hq >= (1LL << 31) ||
-        ((long long)T_total / 128 + B) * Hq >= (1LL << 24))
+    // a launch holds fewer than 2^32 threads: 256 for 64 rows of a head (the
+    // least of the long forms), and a sequence may leave one block unused; a row
+    // and a window add up to a 32-bit number
+    if (T_total >= (1 << 29) || ((long long)T_total / 64 + B) * Hq >= (1LL << 24))
         return fail(GDR_EUNSUPPORTED, "%s: %d rows in %d sequences of %d heads are too many", what,
                     T_total, B, Hq);
     if (cu_seqlens_host) {

@@ -26,7 +26,6 @@ using gdr::kMaxRows;
 using gdr::page_shift_of;
 using gdr::reaches;
 
-
 }  // namespace
 
 extern "C" {

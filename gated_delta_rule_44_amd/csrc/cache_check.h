@@ -35,7 +35,7 @@ inline int page_shift_of(int page_size) {
 
 // dtype, width, heads and the cache's geometry
 inline gdr_status check_cache(const char *what, int dt, int B, int Hkv, int D, int max_pages,
-                       int page_size, int num_pages) {
+                              int page_size, int num_pages) {
     if (dt != GDR_F32 && dt != GDR_BF16)
         return fail(GDR_EINVAL, "%s: dtype %d is not GDR_F32 or GDR_BF16", what, dt);
     if (D != 64 && D != 128)
@@ -57,8 +57,8 @@ inline gdr_status check_cache(const char *what, int dt, int B, int Hkv, int D, i
 
 // A host copy of a page table: every entry in -1..num_pages-1, and none
 // twice where `once` is not NULL (num_pages flags, kept over several tables).
-inline gdr_status check_table(const char *what, const char *name, const int32_t *t, int B, int max_pages,
-                       int num_pages, unsigned char *once) {
+inline gdr_status check_table(const char *what, const char *name, const int32_t *t, int B,
+                              int max_pages, int num_pages, unsigned char *once) {
     const long long n = (long long)B * max_pages;
     for (long long i = 0; i < n; ++i) {
         if (t[i] < -1 || t[i] >= num_pages)

@@ -52,8 +52,8 @@ extern "C" {
  *                not decrease, ends at or below T_total)
  *   lse          [T_total, Hq] fp32 or NULL (the backward pass needs it)
  *
- * Limits (GDR_EUNSUPPORTED): T_total < 2^30, T_total * Hq < 2^31, Hq * D <=
- * 2^20.
+ * Limits (GDR_EUNSUPPORTED): T_total < 2^29, (T_total / 64 + B) * Hq < 2^24
+ * (T_total * Hq < 2^30 for a few sequences), Hq * D <= 2^20.
  *
  * Numerics: fp32 accumulation, logits, softmax statistics and weights; with
  * bf16 inputs a weight enters the product with V as one bf16 number, off by

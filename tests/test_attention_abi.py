@@ -108,6 +108,22 @@ def test_backward_rejects(lib, kw, code, msg):
     assert msg in err(lib)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1, T=1 << 29, total=1 << 29, Hq=1, Hkv=1, D=64),     # a row and a window: past 2^31
+    dict(B=(1 << 22) - 128, total=64 * 128, cu=FAKE),            # keys in blocks of 64: 2^24
+    dict(B=1, T=1 << 28, total=1 << 28),
+])
+def test_prompts_past_a_launch(lib, kw):
+    for call in (prefill, backward):
+        assert call(lib, **kw) == EUNSUPPORTED
+        assert "too many" in err(lib)
+        # a smaller batch fails at the next check
+        assert call(lib, **{**kw, "B": 1, "T": 4096, "total": 4096, "cu": None, "q": None}) == EINVAL
+        assert "q is NULL" in err(lib)
+    assert lib.gdr_attention_backward_workspace_bytes(
+        1, kw["B"], kw["total"], kw.get("Hq", 4), kw.get("Hkv", 2), kw.get("D", 128)) == 0
+
+
 def test_empty_calls_are_ok_without_gpu(lib):
     for call in (prefill, backward):
         assert call(lib, B=0, T=0, total=0) == 0
