@@ -7,7 +7,10 @@
 // barrier is on the way), and their sums are joined through LDS at the end, in a
 // fixed order.  A short call is then four times as many workgroups, each a
 // quarter as long: what bounds it is the chain from a load to the product that
-// needs it, not the card's rates.
+// needs it, not the card's rates.  (One prompt of 301 tokens, 16 heads over 4 of
+// 128 in bf16: 9.0 us, 10.5 in blocks of 128; the gradients of 2 x 150 tokens, 4
+// heads over 2 of 64 in fp32: 34.5 us, 13.8 and 21.1, for 79.)  few_rows says
+// where it is taken, with both sides measured.
 #include "prompt_internal.h"
 
 namespace gdr {
