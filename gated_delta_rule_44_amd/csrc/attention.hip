@@ -49,11 +49,16 @@ __device__ inline Span seq_span(int len, int n, int window) {
 // drafts before it on its way, and attends to the context and to the drafts of
 // its way whose positions its window holds: one bit each, 64 at most.
 struct Way { unsigned long long drafts; int depth; };
-// By one wave, lane u for draft u: all lanes go up together, a step at a time
-// (trees are a few drafts deep).
-__device__ inline Way draft_way(const int32_t *parents, int n, int window) {
+// By one wave, lane u for draft u, whose parent is `up`: all lanes go up together,
+// a step at a time (trees are a few drafts deep).  The parents are loaded ahead of
+// the first tiles and the ways found behind those loads: a load is there only
+// after all that were asked for before it.
+__device__ inline int load_parent(const AttnArgs &a, int b) {
     const int u = threadIdx.x & 63;
-    int up = u < n ? parents[u] : -1;
+    return u < a.n ? a.parents[(size_t)b * a.n + u] : -1;
+}
+__device__ inline Way draft_way(int up, int window) {
+    const int u = threadIdx.x & 63;
     if (up >= u) up = -1;
     Way y{1ull << u, 0};
     int at = up < 0 ? -1 : up;
@@ -66,6 +71,16 @@ __device__ inline Way draft_way(const int32_t *parents, int n, int window) {
         }
     }
     return y;
+}
+
+// Which of the places j0 .. j0 + 31 a row attends to: those of its span that are
+// before place ctx or of a draft on its way.
+__device__ inline unsigned way_bits(Span sp, int ctx, unsigned long long drafts, int j0) {
+    const int d = j0 - ctx, lo = sp.lo - j0, hi = sp.hi - j0;
+    const unsigned in = d >= 64 ? 0u : d >= 0 ? (unsigned)(drafts >> d)
+                      : d > -32 ? (unsigned)drafts << -d | ((1u << -d) - 1) : ~0u;
+    return in & (hi >= 32 ? ~0u : hi > 0 ? (1u << hi) - 1 : 0u) &
+           (lo <= 0 ? ~0u : lo < 32 ? ~0u << lo : 0u);
 }
 
 // How the cached tokens are shared out.  Every sequence's span is cut into
@@ -695,6 +710,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     Span sp{0, 0};
     const int ctx = len - a.n;                  // TREE: the context's tokens
     unsigned long long drafts = 0;
+    const int parent = TREE ? load_parent(a, b) : -1;
     typename TL::Q q;
     {
         const size_t qb = (size_t)b * a.n * a.Hq * D;
@@ -708,16 +724,15 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
     // place's span, but its lower end from the position)
     auto find_way = [&]() {
         const int t = row < rows ? row / a.G : 0;
-        const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
+        const Way y = draft_way(parent, a.window);
         const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
         const int depth = __shfl(y.depth, t);
         drafts = (unsigned long long)hi << 32 | lo;
         if (row < rows) sp = Span{token_span(len, a.n, a.window, depth).lo, ctx + t + 1};
     };
-    auto attends = [&](int j) {
-        bool in = j >= sp.lo && j < sp.hi;
-        if constexpr (TREE) in = in && (j < ctx || (drafts >> ((j - ctx) & 63) & 1));
-        return in;
+    // token `key` of the tile from j0 on (way: TREE's way_bits of it)
+    auto attends = [&](int j0, unsigned way, int key) {
+        return TREE ? (way >> key & 1) != 0 : j0 + key >= sp.lo && j0 + key < sp.hi;
     };
     // the block's tokens: what its rows attend to, within the slot (TREE: at
     // most; a draft's position is that of its place or before)
@@ -760,11 +775,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
                                                TL::key(i, g)) = f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
         }
         if (!full) {
+            const unsigned way = TREE ? way_bits(sp, ctx, drafts, j0) : 0u;
 #pragma unroll
-            for (int i = 0; i < kVals; ++i) {
-                const int j = j0 + TL::key(i, g);
-                x[i] = here[TL::block(i)] && attends(j) ? x[i] : -INFINITY;
-            }
+            for (int i = 0; i < kVals; ++i)
+                x[i] = here[TL::block(i)] && attends(j0, way, TL::key(i, g)) ? x[i] : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < kVals; ++i) top = fmaxf(top, x[i]);
@@ -788,12 +802,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
         // NaN) their sum in that channel.
         const int j1 = j0 + kTile < len ? j0 + kTile : len;
         if ((j0 < all_lo || j1 > all_hi) && __builtin_amdgcn_ballot_w64(TL::odd(vf))) {
+            const unsigned way = TREE ? way_bits(sp, ctx, drafts, j0) : 0u;
             float in[kVals];
 #pragma unroll
-            for (int i = 0; i < kVals; ++i) {
-                const int j = j0 + TL::key(i, g);
-                in[i] = attends(j) ? 1.f : 0.f;
-            }
+            for (int i = 0; i < kVals; ++i) in[i] = attends(j0, way, TL::key(i, g)) ? 1.f : 0.f;
             const typename TL::Ones ones = TL::ones(in);
 #pragma unroll
             for (int c = 0; c < PER; ++c) {
@@ -1071,13 +1083,14 @@ __global__ __launch_bounds__(64 * W * kTreeShares<W>, 2) void tree_kernel(KArgs 
     const int rows = a.n * a.G, row0 = rb * kRows, row = row0 + 32 * rt + r;
     const int t = row < rows ? row / a.G : 0, hg = row < rows ? row % a.G : 0, ctx = len - a.n;
     const typename R::At at = R::at(lane);
+    const int parent = load_parent(a, b);
     typename R::B q;
     R::load(q, static_cast<const T *>(a.q) + (((size_t)b * a.n + t) * a.Hq + head * a.G + hg) * D, h);
     if (k.negative) R::negate(q);
     Span sp{0, 0};
     unsigned long long drafts = 0;
     auto find_way = [&]() GDR_INLINE {
-        const Way y = draft_way(a.parents + (size_t)b * a.n, a.n, a.window);
+        const Way y = draft_way(parent, a.window);
         const unsigned lo = __shfl((unsigned)y.drafts, t), hi = __shfl((unsigned)(y.drafts >> 32), t);
         const int depth = __shfl(y.depth, t);
         drafts = (unsigned long long)hi << 32 | lo;
