@@ -144,11 +144,26 @@ int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long 
     return rows > 32 && seen * B * Hkv * D * 4 >= kShareBytes ? 64 : 32;
 }
 
-// Waves of a workgroup of a tree's rows, 32 each; more than 128 rows are several
-// blocks alike.
-int tree_waves(long long rows) {
+// Rows of a tree's block.  With few tokens to read, blocks of 16 side by side, as
+// many times as they read a token: bf16, 8 heads, one context of 300, 28 rows: 7.2
+// us against 10.7 in a block of 32, 96 rows 7.7 against 17.5 in one of 96; up to
+// 160 K of (token, head, block), where 16 heads of one context of 2,000, 66 rows
+// take 20.2 us against 25.2 (64 channels: 16.0 against 19.1), and 4 of 1,000, 40
+// rows (190 K) 25.2 against 21.0.  Past that, over 32 rows, a tile of 32 a wave,
+// up to 128 rows, and blocks alike of more; at most 32 rows, for 64 channels 32
+// (one context of 16,000 17.0 us, 18.6 by blocks of 16; 8 of 2,000 17.3 and 20.5;
+// 64 of 4,000 131 and 119), for 128 still 16, as the accumulators of 32 leave few
+// registers for loads (26.4 and 23.6; 26.1 and 26.3; 302 and 204).  As above, the
+// table and the window stand for the lengths.
+constexpr long long kFewTokens = 160 << 10;
+int tree_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long long capacity,
+              int window) {
+    if (!bf16_io || rows <= 16) return 16;
+    const long long seen = window > 0 && window < capacity - n ? window + n : capacity;
+    if (seen * B * Hkv * ((rows + 15) / 16) <= kFewTokens) return 16;
+    if (rows <= 32) return D == 64 ? 32 : 16;
     const long long blocks = (rows + 127) / 128;
-    return (int)((rows + 32 * blocks - 1) / (32 * blocks));
+    return 32 * (int)((rows + 32 * blocks - 1) / (32 * blocks));
 }
 
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
@@ -1488,23 +1503,30 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int D, bool TREE>
-hipError_t launch_d(bool bf16_io, const AttnArgs &a, hipStream_t s) {
-    if (!bf16_io) return launch<float, D, 16, 1, TREE>(a, s);
+template <int D>
+hipError_t launch_decode(bool bf16_io, const AttnArgs &a, hipStream_t s) {
+    if (!bf16_io) return launch<float, D, 16, 1, false>(a, s);
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
-    if constexpr (TREE) {
-        switch (tree_waves((long long)a.n * a.G)) {
-        case 1: break;
-        case 2: return launch<bf16, D, 32, 2, true>(a, s);
-        case 3: return launch<bf16, D, 32, 3, true>(a, s);
-        default: return launch<bf16, D, 32, 4, true>(a, s);
-        }
+    switch (block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window)) {
+    case 16: return launch<bf16, D, 16, 1, false>(a, s);
+    case 32: return launch<bf16, D, 32, 1, false>(a, s);
+    default: return launch<bf16, D, 32, 2, false>(a, s);
     }
-    const int block = block_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window);
-    if (block == 16) return launch<bf16, D, 16, 1, TREE>(a, s);
-    if constexpr (!TREE)
-        if (block == 64) return launch<bf16, D, 32, 2, false>(a, s);
-    return launch<bf16, D, 32, 1, TREE>(a, s);
+}
+
+template <int D>
+hipError_t launch_tree(bool bf16_io, const AttnArgs &a, hipStream_t s) {
+    if (!bf16_io) return launch<float, D, 16, 1, true>(a, s);
+    const long long cap = (long long)a.map.max_pages << a.map.page_shift;
+    const int rows = tree_rows(true, (long long)a.n * a.G, a.B, a.n, a.Hkv, D, cap, a.window);
+    if (rows == 16) return launch<bf16, D, 16, 1, true>(a, s);
+    if constexpr (D == 64)
+        if (rows == 32) return launch<bf16, D, 32, 1, true>(a, s);
+    switch (rows) {
+    case 64: return launch<bf16, D, 32, 2, true>(a, s);
+    case 96: return launch<bf16, D, 32, 3, true>(a, s);
+    default: return launch<bf16, D, 32, 4, true>(a, s);
+    }
 }
 
 }  // namespace
@@ -1519,19 +1541,20 @@ size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capac
         const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
         if (x > most) most = x;
     }
-    if (rows > 32) {                        // (a tree's blocks)
-        const size_t x = ws_map(B, n, G, Hkv, D, 32 * tree_waves(rows), capacity, with_scores).total;
+    // (a tree's blocks of over 64)
+    for (int rw = 96; rw <= 128 && rows > 64; rw += 32) {
+        const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
         if (x > most) most = x;
     }
     return most;
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
-    return D == 128 ? launch_d<128, false>(bf16_io, a, s) : launch_d<64, false>(bf16_io, a, s);
+    return D == 128 ? launch_decode<128>(bf16_io, a, s) : launch_decode<64>(bf16_io, a, s);
 }
 
 hipError_t launch_attention_tree(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {
-    return D == 128 ? launch_d<128, true>(bf16_io, a, s) : launch_d<64, true>(bf16_io, a, s);
+    return D == 128 ? launch_tree<128>(bf16_io, a, s) : launch_tree<64>(bf16_io, a, s);
 }
 
 }  // namespace gdr
