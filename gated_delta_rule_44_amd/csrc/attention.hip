@@ -1059,13 +1059,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_kernel(KArgs k) {
 
 template <int W> constexpr int kTreeShares = W == 2 ? 2 : 1;
 
-// A tree's rows past 32, in bf16: a workgroup of W tiles of 32 rows, all of them
-// on every tile of 64 tokens, which passes through LDS, two tiles there, the next
-// on its way while one is worked on.  Two tiles of rows are two waves each, for a
-// half of the tokens, joined at the end: the card is as busy with long contexts
-// (64 rows, 32 contexts of 512 to 8,192: 96 us either way) and sooner done with
-// short ones (4 of 300 to 900: 19 us, 24 with one); three in this way are slower
-// (96 rows, 32 contexts: 121 us, 106 with one).
+// A tree's rows past 32, in bf16, with much to read: a workgroup of W tiles of 32
+// rows, all of them on every tile of 64 tokens, which passes through LDS, two tiles
+// there, the next on its way while one is worked on.  Two tiles of rows are two
+// waves each, for a half of the tokens, joined at the end (64 rows, 8 heads of 128:
+// 4 contexts of 4,000 25.5 us, 30.1 with one wave each, 64 of 4,000 237 and 242; of
+// 64 channels 19.7 and 21.8, 133 and 130); three in this way are slower (96 rows,
+// 32 contexts of 512 to 8,192: 121 us, 106 with one).
 // The products, the running maximum and sum and what is done about infinities are
 // those of the attention of whole prompts (prompt.hip); a weight is two bf16
 // numbers as above (119 us for the 96 rows, o's error 1.66e-3 against 64 bits;

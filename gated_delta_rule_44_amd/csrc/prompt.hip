@@ -18,7 +18,7 @@
 // products.
 //
 // Products bound it.  16 packed prompts of 512 to 8,192 tokens, 32 heads over 8 of
-// 128 in bf16: 1,722 to 1,810 us, 1.00 to 1.05 PFLOP/s (a library's product of
+// 128 in bf16: 1,722 to 1,906 us by the card, 0.94 to 1.05 PFLOP/s (a library's product of
 // 8192^3: 1.21), the matrix units busy for 55 % of the CUs' cycles at about 1.8
 // GHz, no bank conflicts in LDS.  Copies of the kernel without a part of it: without
 // barriers 1,755 (of 1,780 to 1,805), without fetches 1,564, without exponentials
