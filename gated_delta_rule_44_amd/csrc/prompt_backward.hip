@@ -29,13 +29,14 @@ constexpr int kWaves = 4;                  // waves of a workgroup, 32 rows or t
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
 
-// Workspace: lse log2 e (+inf for a row without weights) and delta of every
-// row, head by head.
+// Workspace: lse log2 e (+inf for a row without weights) and -delta of every
+// row, head by head.  The sums do.v start from -delta, so that none is taken off
+// after them (4 x 4,096 tokens 1,904 -> 1,874 us, of 64 channels 1,053 -> 1,027).
 struct KArgs {
     PromptArgs a;
     float c;              // scale log2 e
     int blocks;           // block_bound
-    float *lse2, *delta;  // [Hq, T_total]
+    float *lse2, *start;  // [Hq, T_total]
 };
 
 // Workgroup = (block of 128 rows, query head), 32 rows a wave.
@@ -58,18 +59,18 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const typename R::At at = R::at(lane);
 
     typename R::B q, g;
-    float lse2, delta;
+    float lse2, start;
     {
         const int row = bl.row0 + (i < bl.len ? i : bl.len - 1);
         const size_t at_row = ((size_t)row * a.Hq + head) * D;
         R::load(q, static_cast<const T *>(a.q) + at_row, h);
         R::load(g, static_cast<const T *>(a.d_o) + at_row, h);
         lse2 = base2(a.lse[(size_t)row * a.Hq + head]);
-        delta = row_delta<T, D>(static_cast<const T *>(a.d_o) + at_row,
+        start = minus_delta<T, D>(static_cast<const T *>(a.d_o) + at_row,
                                 static_cast<const T *>(a.o) + at_row, h);
         if (i < bl.len && h == 0) {
             k.lse2[(size_t)head * a.T_total + row] = lse2;
-            k.delta[(size_t)head * a.T_total + row] = delta;
+            k.start[(size_t)head * a.T_total + row] = start;
         }
     }
     const int last = i0 + kRows < bl.len ? i0 + kRows - 1 : bl.len - 1;
@@ -94,7 +95,11 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
         stage(t0);
         R::settle(q);
         R::settle(g);
-        asm volatile("" : "+v"(lse2), "+v"(delta));
+        asm volatile("" : "+v"(lse2));
+        f32x16 from;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) from[e] = start;
+        asm volatile("" : "+v"(from));
         for (int t = t0; t < t1; ++t) {
             tile_landed();
             if (t + 1 < t1) stage(t + 1);
@@ -106,10 +111,9 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
 #pragma unroll
             for (int b = 0; b < kBlk; ++b) {
                 f32x16 x = R::rows(kt, b, at, q);
-                const f32x16 dp = R::rows(vt, b, at, g);
+                const f32x16 dp = R::rows(vt, b, at, g, from);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[e] = exp2_(fmaf(x[e], k.c, -lse2)) * (dp[e] - delta);
+                for (int e = 0; e < 16; ++e) x[e] = exp2_(fmaf(x[e], k.c, -lse2)) * dp[e];
                 if (!full) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     using R = Rows<T, D>;
     constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols;
     __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
-    __shared__ __align__(16) float stats[2][2][kTok];      // lse2 and delta of a tile's rows
+    __shared__ __align__(16) float stats[2][2][kTok];      // lse2 and -delta of a tile's rows
     const PromptArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
         fetch(lds[buf][1], static_cast<const T *>(a.d_o) + (size_t)next_head * D, first, left, lane);
         if (w < 2)
             fetch_words<kTok>(stats[buf][w],
-                              (w ? k.delta : k.lse2) + (size_t)next_head * a.T_total + first,
+                              (w ? k.start : k.lse2) + (size_t)next_head * a.T_total + first,
                               lane < left ? lane : left - 1, lane);
         if (++next_t == t1) {
             next_t = t0;
@@ -191,22 +195,21 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
             const int i0 = t * kTok;
             t = t + 1 == t1 ? t0 : t + 1;
             const char *qt = lds[n & 1][0], *gt = lds[n & 1][1];
-            const float *lse2 = stats[n & 1][0], *delta = stats[n & 1][1];
+            const float *lse2 = stats[n & 1][0], *start = stats[n & 1][1];
             if (jw >= bl.len || i0 + kTok <= jw || (a.window > 0 && i0 >= jw + 31 + a.window)) continue;
             const bool full = i0 >= jw + 31 && i0 + kTok <= bl.len &&
                               (a.window == 0 || i0 + kTok - 1 < jw + a.window);
 #pragma unroll
             for (int b = 0; b < kBlk; ++b) {
                 f32x16 x = R::rows(qt, b, at, kf);
-                f32x16 dp = R::rows(gt, b, at, vf);
+                f32x16 dp = R::rows(gt, b, at, vf, R::per_row(start + 32 * b, h));
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse2 + 32 * b + R::key(e, h));
-                    const f32x4 de = *reinterpret_cast<const f32x4 *>(delta + 32 * b + R::key(e, h));
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         x[e + u] = exp2_(fmaf(x[e + u], k.c, -ls[u]));
-                        dp[e + u] = x[e + u] * (dp[e + u] - de[u]);
+                        dp[e + u] *= x[e + u];
                     }
                 }
                 if (!full) {
@@ -280,7 +283,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
         fetch(lds[buf][1], static_cast<const T *>(a.d_o) + (size_t)next_head * D, first, left, lane);
         if (w < 2)
             fetch_words<kTok>(stats[buf][w],
-                              (w ? k.delta : k.lse2) + (size_t)next_head * a.T_total + first,
+                              (w ? k.start : k.lse2) + (size_t)next_head * a.T_total + first,
                               lane < left ? lane : left - 1, lane);
         if (++next_t == t1) {
             next_t = t0;
@@ -303,10 +306,10 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
         constexpr int ROLE = decltype(which)::value;
         const int i0 = n.t * kTok + 32 * ROLE;
         const char *qt = lds[n.buf][0] + 32 * ROLE * R::kRowBytes, *gt = qt + R::kTileBytes;
-        const float *lse2 = stats[n.buf][0] + 32 * ROLE, *delta = lse2 + kTok;
+        const float *lse2 = stats[n.buf][0] + 32 * ROLE, *start = lse2 + kTok;
         f32x16 x = R::rows(qt, 0, at, kf);
         __builtin_amdgcn_sched_barrier(0);
-        f32x16 dp = R::rows(gt, 0, at, vf);
+        f32x16 dp = R::rows(gt, 0, at, vf, R::per_row(start, h));
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
             const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse2 + R::key(e, h));
@@ -315,12 +318,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
         }
         __builtin_amdgcn_sched_barrier(0);
         between();
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const f32x4 de = *reinterpret_cast<const f32x4 *>(delta + R::key(e, h));
-#pragma unroll
-            for (int u = 0; u < 4; ++u) dp[e + u] = x[e + u] * (dp[e + u] - de[u]);
-        }
+        dp *= x;
         if (!whole(i0)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -416,7 +414,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     const long long blocks = block_bound<kRows>(a);
     k.blocks = (int)blocks;
     k.lse2 = static_cast<float *>(a.ws);
-    k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
+    k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     hipError_t e;
     if (few_rows<T, D>(a, blocks * a.Hq, 1)) {
         e = launch_queries_short(sizeof(T) == 2, D, a, s);

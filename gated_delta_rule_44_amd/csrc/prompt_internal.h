@@ -145,6 +145,17 @@ template <int D> struct Rows<bf16, D> {
         if constexpr (D == 128) return ((j & 3) << 1) | ((j >> 2) & 1) | (((j >> 3) & 1) << 3);
         else return (((j >> 1) & 1) << 1) | ((j >> 2) & 1) | (((j >> 3) & 1) << 2);
     }
+    // a number for each of a block's 32 rows, where `rows` has that row's
+    __device__ static inline f32x16 per_row(const float *x, int h) {
+        f32x16 y;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(x + key(e, h));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[e + u] = v[u];
+        }
+        return y;
+    }
     // row: the lane's row of b
     __device__ static inline void load(B &b, const T *row, int h) {
 #pragma unroll
@@ -173,11 +184,9 @@ template <int D> struct Rows<bf16, D> {
         a.col = row * kRowBytes + ((chunk ^ swz(row)) << 4) + 8 * (q & 1);
         return a;
     }
-    // rows 32 blk .. of the tile
-    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b) {
-        f32x16 s;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = 0.f;
+    // rows 32 blk .. of the tile, the sums from s on
+    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b,
+                                         f32x16 s = f32x16{}) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const bf16x8 x = *reinterpret_cast<const bf16x8 *>(
@@ -331,6 +340,17 @@ template <int D> struct Rows<float, D> {
     __device__ static inline int key(int e, int h) { return 8 * (e >> 2) + 4 * h + (e & 3); }
     __device__ static inline int dim(int c, int e, int h) { return kCols * key(e, h) + c; }
     __device__ static inline int swz(int j) { return j & 15; }
+    // a number for each of a block's 32 rows, where `rows` has that row's
+    __device__ static inline f32x16 per_row(const float *x, int h) {
+        f32x16 y;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(x + key(e, h));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[e + u] = v[u];
+        }
+        return y;
+    }
     __device__ static inline void load(B &b, const T *row, int h) {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) b.f[i] = *reinterpret_cast<const f32x4 *>(row + 8 * i + 4 * h);
@@ -356,10 +376,9 @@ template <int D> struct Rows<float, D> {
         return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
     }
     // two sums of D / 2 products, then theirs
-    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b) {
-        f32x16 s, t;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = t[e] = 0.f;
+    __device__ static inline f32x16 rows(const char *tile, int blk, const At &a, const B &b,
+                                         f32x16 s = f32x16{}) {
+        f32x16 t{};
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
             const f32x4 x = *reinterpret_cast<const f32x4 *>(
@@ -428,11 +447,11 @@ template <int D> struct Rows<float, D> {
 };
 
 // What the backward pass keeps of a row in its workspace: lse log2 e (+inf for a
-// row without weights) and delta = do . o, of which each half of a wave sums
-// half the channels.
+// row without weights) and -delta = -do . o, from which the sums do . v start, of
+// which each half of a wave sums half the channels.
 __device__ inline float base2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 template <typename T, int D>
-__device__ inline float row_delta(const T *d_o, const T *o, int h) {
+__device__ inline float minus_delta(const T *d_o, const T *o, int h) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 2; i += 8) {
@@ -441,7 +460,7 @@ __device__ inline float row_delta(const T *d_o, const T *o, int h) {
             const f32x4 x = Elem<T>::load4(d_o + D / 2 * h + i + u);
             const f32x4 y = Elem<T>::load4(o + D / 2 * h + i + u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s = fmaf(x[e], y[e], s);
+            for (int e = 0; e < 4; ++e) s = fmaf(-x[e], y[e], s);
         }
     }
     return swap_sum32(s);

@@ -24,7 +24,7 @@ struct KArgs {
     float ascale;         // |scale|
     bool negative;        // forward: scale < 0
     int blocks;           // block_bound<32>
-    float *lse2, *delta;  // [Hq, T_total]: backward (prompt_internal.h)
+    float *lse2, *start;  // [Hq, T_total]: backward (prompt_internal.h)
 };
 
 // A wave's own tiles of 32 rows of two arrays: two on their way, or one where
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kThreads, 1) void query_kernel(KArgs k) {
         own.fetch(buf, 1, vh, row, left, kpitch);
     };
     typename R::B q, g;
-    float lse2, delta;
+    float lse2, start;
     f32x16 acc[kCols];
     auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
@@ -260,24 +260,28 @@ __global__ __launch_bounds__(kThreads, 1) void query_kernel(KArgs k) {
             R::load(q, static_cast<const T *>(a.q) + at_row, h);
             R::load(g, static_cast<const T *>(a.d_o) + at_row, h);
             lse2 = base2(a.lse[(size_t)row * a.Hq + head]);
-            delta = row_delta<T, D>(static_cast<const T *>(a.d_o) + at_row,
+            start = minus_delta<T, D>(static_cast<const T *>(a.d_o) + at_row,
                                     static_cast<const T *>(a.o) + at_row, h);
             if (i < bl.len && h == 0 && w == 0) {
                 k.lse2[(size_t)head * a.T_total + row] = lse2;
-                k.delta[(size_t)head * a.T_total + row] = delta;
+                k.start[(size_t)head * a.T_total + row] = start;
             }
         }
         R::settle(q);
         R::settle(g);
-        asm volatile("" : "+v"(lse2), "+v"(delta));
+        asm volatile("" : "+v"(lse2));
+        f32x16 from;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) from[e] = start;
+        asm volatile("" : "+v"(from));
         int buf = 0;
         for (int t = t0; t < t1; t += kWaves) {
             O::template landed<2 * O::kLoads>(kBufs > 1 && t + kWaves < t1);
             const bool full = t * 32 + 31 <= i0 && (a.window == 0 || t * 32 > i0 + 31 - a.window);
             f32x16 x = R::rows(own.tile(buf, 0), 0, at, q);
-            const f32x16 dp = R::rows(own.tile(buf, 1), 0, at, g);
+            const f32x16 dp = R::rows(own.tile(buf, 1), 0, at, g, from);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = exp2_(fmaf(x[e], k.c, -lse2)) * (dp[e] - delta);
+            for (int e = 0; e < 16; ++e) x[e] = exp2_(fmaf(x[e], k.c, -lse2)) * dp[e];
             if (!full) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = attends(t * 32 + R::key(e, h)) ? x[e] : 0.f;
@@ -309,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     constexpr int kCols = R::kCols, kBufs = O::kBufs;
     constexpr int kLds = O::kWave > 2 * O::kSums ? O::kWave : 2 * O::kSums;
     __shared__ __align__(1024) char lds[kWaves * kLds];
-    __shared__ __align__(16) float stats[kWaves][kBufs][2][32];    // lse2 and delta of a tile's rows
+    __shared__ __align__(16) float stats[kWaves][kBufs][2][32];    // lse2 and -delta of a tile's rows
     const PromptArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
@@ -332,7 +336,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
         const int at_row = r < left ? r : left - 1;
         const size_t from = (size_t)head * a.T_total + first;
         fetch_words<32>(stats[w][buf][0], k.lse2 + from, at_row, lane);
-        fetch_words<32>(stats[w][buf][1], k.delta + from, at_row, lane);
+        fetch_words<32>(stats[w][buf][1], k.start + from, at_row, lane);
     };
     typename R::B kf, vf;
     f32x16 dk[kCols], dv[kCols];
@@ -357,17 +361,16 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
             const int i0 = (t0 + n % tiles) * 32;
             const bool full = i0 >= j0 + 31 && i0 + 32 <= bl.len &&
                               (a.window == 0 || i0 + 31 < j0 + a.window);
-            const float *lse2 = stats[w][buf][0], *delta = stats[w][buf][1];
+            const float *lse2 = stats[w][buf][0], *start = stats[w][buf][1];
             f32x16 x = R::rows(own.tile(buf, 0), 0, at, kf);
-            f32x16 dp = R::rows(own.tile(buf, 1), 0, at, vf);
+            f32x16 dp = R::rows(own.tile(buf, 1), 0, at, vf, R::per_row(start, h));
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const f32x4 ls = *reinterpret_cast<const f32x4 *>(lse2 + R::key(e, h));
-                const f32x4 de = *reinterpret_cast<const f32x4 *>(delta + R::key(e, h));
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     x[e + u] = exp2_(fmaf(x[e + u], k.c, -ls[u]));
-                    dp[e + u] = x[e + u] * (dp[e + u] - de[u]);
+                    dp[e + u] *= x[e + u];
                 }
             }
             if (!full) {
@@ -422,7 +425,7 @@ hipError_t backward_q(const PromptArgs &a, hipStream_t s) {
     k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
-    k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
+    k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     query_kernel<T, D><<<(unsigned)k.blocks * a.Hq, kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
@@ -434,7 +437,7 @@ hipError_t backward_k(const PromptArgs &a, hipStream_t s) {
     k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
-    k.delta = k.lse2 + (size_t)a.Hq * a.T_total;
+    k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     key_kernel<T, D><<<(unsigned)k.blocks * a.Hkv, kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
