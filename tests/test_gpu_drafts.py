@@ -190,6 +190,48 @@ def test_tree_many_sequences():
                0.125, what="700 sequences")
 
 
+@pytest.mark.parametrize("n,G", [(2, 1), (33, 2)])
+def test_tree_65536_sequences(n, G):
+    """So many that each is one slot, one more than a table of slots holds."""
+    lens = [40, 0, 70, 33, 5]
+    kc, vc, _, table = make_cache(lens, 1, 64, 16, torch.bfloat16, seed=11)
+    check_tree(queries(5, n, G, 64, torch.bfloat16, 12), kc, vc, table, lens, trees(5, n, 13), 0.125,
+               what="65,537 sequences", empty=65532)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+def test_tree_without_pages(dt):
+    """No columns, or no pages: every token is absent, o is 0, and the workspace
+    that the call asks for is not exceeded."""
+    for P, M in ((0, 4), (3, 0), (0, 0)):
+        kc = torch.full((P, 2, 16, 64), NAN, dtype=DTYPES[dt], device=DEV)
+        table = torch.zeros(3, M, dtype=torch.int32, device=DEV)
+        q = torch.ones(3, 24, 8, 64, dtype=DTYPES[dt], device=DEV)
+        need = gdr.attention_workspace_bytes(3, 24, 8, 2, 64, M, 16)
+        ws = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+        o = gdr.attention_tree(q, kc, kc, table, i32([24, 50, 1]), i32(trees(3, 24, 1)),
+                               o=torch.full_like(q, NAN), workspace=ws[:need])
+        sync()
+        assert not o.any() and (ws[need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_tree_workspace_is_enough(D):
+    """Nothing is written past the bytes that the library asks for, in any of the
+    blocks."""
+    lens, Hkv, page = [900, 0, 33, 700], 2, 32
+    kc, vc, _, table = make_cache(lens, Hkv, D, page, torch.bfloat16, seed=D)
+    for n, G in ((8, 4), (24, 2), (24, 4), (64, 2), (40, 4)):
+        q = queries(4, n, Hkv * G, D, torch.bfloat16, n)
+        for extra in (0, 100 + (160 << 10) // (4 * Hkv * page)):
+            wide = np.pad(table, ((0, 0), (0, extra)), constant_values=-1)
+            need = gdr.attention_workspace_bytes(4, n, Hkv * G, Hkv, D, wide.shape[1], page)
+            ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+            check_tree(q, kc, vc, wide, lens, trees(4, n, n), D ** -0.5, what="%d x %d" % (n, G),
+                       workspace=ws[:need])
+            assert (ws[need:] == 0x5A).all(), (n, G, extra)
+
+
 def test_tree_bad_parents():
     """Values that are no earlier draft mean the context."""
     lens = [40, 40, 40]
