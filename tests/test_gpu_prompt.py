@@ -265,6 +265,25 @@ def test_bad_offsets_stay_inside():
         run_backward(data, o, lse, cu, 0.125, 0)
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("H", [1, 70])
+def test_backward_workspace_is_enough(dt, H):
+    """Nothing is written past the bytes that the library asks for, by either
+    form (blocks of 32 rows and of 128)."""
+    lens, D = [200, 1, 77], 64
+    data, cu = make(lens, H, H, D, DTYPES[dt], seed=31), offsets(lens)
+    o, lse = run_forward(data, cu, 0.125, 0)
+    want = run_backward(data, o, lse, cu, 0.125, 0)
+    need = gdr.attention_backward_workspace_bytes(DTYPES[dt], 3, 278, H, H, D)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = run_backward(data, o, lse, cu, 0.125, 0, workspace=ws[:need])
+    assert (ws[need:] == 0x5A).all()
+    for x, y in zip(got, want):
+        assert same(x, y)
+    with pytest.raises(gdr.GdrError, match="workspace"):
+        run_backward(data, o, lse, cu, 0.125, 0, workspace=ws[:need - 16])
+
+
 @pytest.mark.parametrize("packed", [False, True])
 def test_streams_and_graphs(packed):
     """On another stream, two at once, and captured: every replay on new
