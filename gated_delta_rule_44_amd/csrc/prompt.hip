@@ -42,7 +42,7 @@ struct KArgs {
     float c;              // |scale| log2 e, above 0
     float ascale;         // |scale|
     bool negative;        // scale < 0
-    int blocks;           // block_bound
+    int mixed;            // mixed_seqs
 };
 
 template <typename T, int D>
@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int head = query_head(a, blockIdx.x % a.Hq);
-    const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
+    const Block bl = find_block<kRows, false>(a, blockIdx.x / a.Hq, k.mixed);
     if (bl.i < 0) return;
     const int i0 = bl.i * kRows, iw = i0 + 32 * w, i = iw + r;
     const int hk = head / a.G;
@@ -172,6 +172,10 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
         a.lse[row] = l == 0.f ? -INFINITY : m * k.ascale + kLn2F * __builtin_amdgcn_logf(l);
 }
 
+// workgroups at a time, by the registers of a wave
+template <typename T, int D>
+constexpr int kResident = 256 * (sizeof(T) == 2 ? (D == 128 ? 2 : 4) : (D == 128 ? 1 : 3));
+
 template <typename T, int D>
 hipError_t launch(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
@@ -182,7 +186,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     k.negative = a.scale < 0.f;
     const long long blocks = block_bound<kRows>(a);
     if (few_rows<T, D>(a, blocks * a.Hq, 1)) return launch_prompt_short(sizeof(T) == 2, D, a, s);
-    k.blocks = (int)blocks;
+    k.mixed = mixed_seqs<kRows>(a, a.Hq, kResident<T, D>);
     prompt_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
     return hipGetLastError();
 }

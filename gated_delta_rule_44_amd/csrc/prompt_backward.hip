@@ -35,7 +35,7 @@ constexpr int kRows = 32 * kWaves;
 struct KArgs {
     PromptArgs a;
     float c;              // scale log2 e
-    int blocks;           // block_bound
+    int mixed;            // mixed_seqs
     float *lse2, *start;  // [Hq, T_total]
 };
 
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int head = query_head(a, blockIdx.x % a.Hq);
-    const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
+    const Block bl = find_block<kRows, false>(a, blockIdx.x / a.Hq, k.mixed);
     if (bl.i < 0) return;
     const int i0 = bl.i * kRows, iw = i0 + 32 * w, i = iw + r;
     const int hk = head / a.G;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int hk = blockIdx.x % a.Hkv;
-    const Block bl = find_block<kRows>(a, blockIdx.x / a.Hkv);
+    const Block bl = find_block<kRows, true>(a, blockIdx.x / a.Hkv, k.mixed);
     if (bl.i < 0) return;
     const int j0 = bl.i * kRows, jw = j0 + 32 * w, j = jw + r;
     const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6), pair = w % PAIRS, role = w / PAIRS;
     const int hk = blockIdx.x % a.Hkv;
-    const Block bl = find_block<kTokens>(a, blockIdx.x / a.Hkv);
+    const Block bl = find_block<kTokens, true>(a, blockIdx.x / a.Hkv, k.mixed);
     if (bl.i < 0) return;
     const int j0 = bl.i * kTokens, jw = j0 + 32 * pair, j = jw + r;
     const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
@@ -406,29 +406,38 @@ __global__ __launch_bounds__(128 * PAIRS, 2) void key_pairs_kernel(KArgs k) {
 // 6,100 tokens, window 512, 16 heads: both kernels 313 us, 351 with four).
 template <int D> constexpr int kPairs = D == 128 ? 4 : 2;
 
+// workgroups at a time, by the registers of a wave (queries; keys, of 128 channels
+// by the LDS)
+template <typename T, int D>
+constexpr int kQueries = 256 * (sizeof(T) == 2 ? (D == 128 ? 2 : 3) : (D == 128 ? 1 : 2));
+template <typename T, int D> constexpr int kKeys = 256 * (sizeof(T) == 2 && D == 64 ? 2 : 1);
+
 template <typename T, int D>
 hipError_t launch(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
     k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
     const long long blocks = block_bound<kRows>(a);
-    k.blocks = (int)blocks;
     k.lse2 = static_cast<float *>(a.ws);
     k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     hipError_t e;
     if (few_rows<T, D>(a, blocks * a.Hq, 1)) {
         e = launch_queries_short(sizeof(T) == 2, D, a, s);
     } else {
+        k.mixed = mixed_seqs<kRows>(a, a.Hq, kQueries<T, D>);
         query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
         e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
     if (few_rows<T, D>(a, blocks * a.Hkv, a.G)) return launch_keys_short(sizeof(T) == 2, D, a, s);
-    if constexpr (sizeof(T) == 2)
-        key_pairs_kernel<D, kPairs<D>><<<(unsigned)(block_bound<32 * kPairs<D>>(a) * a.Hkv),
-                                         128 * kPairs<D>, 0, s>>>(k);
-    else
+    if constexpr (sizeof(T) == 2) {
+        constexpr int kTokens = 32 * kPairs<D>;
+        k.mixed = mixed_seqs<kTokens>(a, a.Hkv, kKeys<T, D>);
+        key_pairs_kernel<D, kPairs<D>><<<(unsigned)(block_bound<kTokens>(a) * a.Hkv), 4 * kTokens, 0, s>>>(k);
+    } else {
+        k.mixed = mixed_seqs<kRows>(a, a.Hkv, kKeys<T, D>);
         key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
+    }
     return hipGetLastError();
 }
 

@@ -23,7 +23,6 @@ struct KArgs {
     float c;              // forward: |scale| log2 e, above 0; else scale log2 e
     float ascale;         // |scale|
     bool negative;        // forward: scale < 0
-    int blocks;           // block_bound<32>
     float *lse2, *start;  // [Hq, T_total]: backward (prompt_internal.h)
 };
 
@@ -98,7 +97,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int head = query_head(a, blockIdx.x % a.Hq);
-    const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
+    const Block bl = find_block<kRows, false>(a, blockIdx.x / a.Hq, 0);
     if (bl.i < 0) return;
     const int i0 = bl.i * kRows, i = i0 + r, hk = head / a.G;
     const unsigned kpitch = a.Hkv * D * (unsigned)sizeof(T);
@@ -224,7 +223,7 @@ __global__ __launch_bounds__(kThreads, 1) void query_kernel(KArgs k) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int head = query_head(a, blockIdx.x % a.Hq);
-    const Block bl = find_block<kRows>(a, k.blocks - 1 - blockIdx.x / a.Hq);
+    const Block bl = find_block<kRows, false>(a, blockIdx.x / a.Hq, 0);
     if (bl.i < 0) return;
     const int i0 = bl.i * kRows, i = i0 + r, hk = head / a.G;
     const unsigned kpitch = a.Hkv * D * (unsigned)sizeof(T);
@@ -318,7 +317,7 @@ __global__ __launch_bounds__(kThreads, 1) void key_kernel(KArgs k) {
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
     const int hk = blockIdx.x % a.Hkv;
-    const Block bl = find_block<kRows>(a, blockIdx.x / a.Hkv);
+    const Block bl = find_block<kRows, true>(a, blockIdx.x / a.Hkv, 0);
     if (bl.i < 0) return;
     const int j0 = bl.i * kRows, j = j0 + r;
     const unsigned qpitch = a.Hq * D * (unsigned)sizeof(T);
@@ -413,8 +412,7 @@ hipError_t forward(const PromptArgs &a, hipStream_t s) {
     k.ascale = fabsf(a.scale);
     k.c = fminf(fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f), 3.4e38f);
     k.negative = a.scale < 0.f;
-    k.blocks = (int)block_bound<kRows>(a);
-    prompt_kernel<T, D><<<(unsigned)k.blocks * a.Hq, kThreads, 0, s>>>(k);
+    prompt_kernel<T, D><<<(unsigned)(block_bound<kRows>(a) * a.Hq), kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
 
@@ -423,10 +421,9 @@ hipError_t backward_q(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
     k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
-    k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
     k.start = k.lse2 + (size_t)a.Hq * a.T_total;
-    query_kernel<T, D><<<(unsigned)k.blocks * a.Hq, kThreads, 0, s>>>(k);
+    query_kernel<T, D><<<(unsigned)(block_bound<kRows>(a) * a.Hq), kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
 
@@ -435,10 +432,9 @@ hipError_t backward_k(const PromptArgs &a, hipStream_t s) {
     KArgs k{};
     k.a = a;
     k.c = fminf(fmaxf(a.scale * kLog2e, -3.4e38f), 3.4e38f);
-    k.blocks = (int)block_bound<kRows>(a);
     k.lse2 = static_cast<float *>(a.ws);
     k.start = k.lse2 + (size_t)a.Hq * a.T_total;
-    key_kernel<T, D><<<(unsigned)k.blocks * a.Hkv, kThreads, 0, s>>>(k);
+    key_kernel<T, D><<<(unsigned)(block_bound<kRows>(a) * a.Hkv), kThreads, 0, s>>>(k);
     return hipGetLastError();
 }
 
