@@ -18,16 +18,16 @@
 // products.
 //
 // Products bound it.  16 packed prompts of 512 to 8,192 tokens, 32 heads over 8 of
-// 128 in bf16: 1,722 to 1,906 us by the card, 0.94 to 1.05 PFLOP/s (a library's product of
+// 128 in bf16: 1,722 to 1,915 us by the card, 0.94 to 1.05 PFLOP/s (a library's product of
 // 8192^3: 1.21), the matrix units busy for 55 % of the CUs' cycles at about 1.8
 // GHz, no bank conflicts in LDS.  Copies of the kernel without a part of it: without
 // barriers 1,755 (of 1,780 to 1,805), without fetches 1,564, without exponentials
 // 1,653, with products only 1,320.  8 prompts of 700 to 2,900 tokens in fp32,
-// window 1,024, 16 heads of 64: 481 us, the matrix units busy for 76 %.  Measured
+// window 1,024, 16 heads of 64: 427 us, the matrix units busy for 76 %.  Measured
 // and not kept: 256 rows a workgroup (1,806 us for 1,802), the next tile's logits
 // under this one's weights (1,880 for 1,865), a wave's priority raised around its
 // products (1,870 for 1,805), products and weights interleaved by force (1,884 for
-// 1,867), the longest sequences first (no change).
+// 1,867).
 #include "prompt_internal.h"
 
 namespace gdr {

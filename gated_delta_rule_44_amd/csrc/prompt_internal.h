@@ -48,6 +48,18 @@ __device__ inline float swap_max32(float x) {
     return fmaxf(a, b);
 }
 
+// The sum over a wave's lanes, which all take part: DPP shifts within rows of 16, the
+// rows' last lanes after.
+__device__ inline int wave_sum(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);      // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);     // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);     // row_bcast:31
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // A block of RB tokens of one sequence: its number in the sequence (-1: there
 // is none), the sequence's first row and its tokens.
 struct Block { int i, row0, len; };
@@ -60,12 +72,15 @@ template <int RB>
 inline long long block_bound(const PromptArgs &a) {
     return a.cu ? (long long)a.T_total / RB + a.B : (long long)a.B * ((a.T + RB - 1) / RB);
 }
-// A fixed-length batch goes sequence by sequence, each one's longest blocks first
-// (of rows the last, of tokens (KEYS) the first), which keeps what a sequence's
-// blocks read in the XCDs' caches, but for the last `mixed` sequences: of those the
-// longest of all go first, so that no long block is left for the end.  Rows go from
-// the last sequence to the first and tokens, after them, from the first on, of which
-// most is still in the caches (12 of 6,100, window 512: 2 % of the gradients' time).
+// A batch goes sequence by sequence, each one's longest blocks first (of rows the
+// last, of tokens (KEYS) the first), which keeps what a sequence's blocks read in
+// the XCDs' caches, but for the last `mixed` sequences, of a packed batch all or
+// none: of those the longest blocks of all go first, so that no long one is left for
+// the end.  Packed, these are found by sums over the sequences, one a lane: of the
+// blocks that are longer than t, for a t that halves the range each time.
+//   Rows go from the last sequence to the first and tokens, after them, from the
+// first on, of which most is still in the caches (12 of 6,100, window 512: 2 % of the
+// gradients' time).
 template <int RB, bool KEYS>
 __device__ inline Block find_block(const PromptArgs &a, int s, int mixed) {
     Block x;
@@ -80,12 +95,37 @@ __device__ inline Block find_block(const PromptArgs &a, int s, int mixed) {
         x.len = a.T;
         return x;
     }
-    if (!KEYS) s = (int)((long long)a.T_total / RB + a.B) - 1 - s;
     auto at = [&](int b) {
         const int c = a.cu[b];
         return c < 0 ? 0 : (c > a.T_total ? a.T_total : c);
     };
     const int lane = threadIdx.x & 63;
+    if (mixed) {                             // (64 sequences at most, one a lane)
+        const int row0 = lane < a.B ? at(lane) : 0, len = lane < a.B ? at(lane + 1) - row0 : 0;
+        const int n = len > 0 ? (len - 1) / RB + 1 : 0;
+        // blocks with at least t of their sequence on their shorter side
+        auto longer = [&](int t) { return wave_sum(n > t ? n - t : 0); };
+        int lo = 0, hi = a.T_total / RB + 1;          // longer(lo) > s, longer(hi) <= s
+        x.i = -1;
+        if (longer(0) <= s) return x;
+        while (hi - lo > 1) {
+            const int t = (lo + hi) / 2;
+            if (longer(t) > s) lo = t;
+            else               hi = t;
+        }
+        // (the sum by all lanes, ahead of what only some of them do)
+        const int rank = s - longer(hi);
+        const unsigned long long have = __builtin_amdgcn_ballot_w64(n > lo);
+        const unsigned long long mine = __builtin_amdgcn_ballot_w64(
+            (n > lo) & (__builtin_popcountll(have & ((1ull << lane) - 1)) == rank));
+        if (!mine) return x;
+        const int b = __builtin_ctzll(mine);
+        x.i = KEYS ? __builtin_amdgcn_readlane(n, b) - 1 - lo : lo;
+        x.row0 = __builtin_amdgcn_readlane(row0, b);
+        x.len = __builtin_amdgcn_readlane(len, b);
+        return x;
+    }
+    if (!KEYS) s = (int)((long long)a.T_total / RB + a.B) - 1 - s;
     int base = 0, count = a.B;               // the sequence is in [base, base + count)
     while (count > 1) {
         const int step = (count + 63) / 64, b = base + lane * step;
@@ -104,16 +144,17 @@ __device__ inline Block find_block(const PromptArgs &a, int s, int mixed) {
 }
 
 // How many: as many as keep the card's places for workgroups (`resident`) as long
-// as the longest block takes; h heads.  (4 sequences of 4,096 tokens, 8 heads of 64
-// in fp32, all mixed, forward: 586 us, 786 with each by itself; 12 of 1,024, 16
-// heads of 64, 8 or so mixed, backward: 142 us, 155; all of 64 sequences of 1,024, 32
-// heads of 128, 821 us, 762 with the last 4, 749 with none.)  With a window most blocks
-// are as long, and there is nothing to gain.
+// as the longest block takes; h heads.  fp32, 8 heads of 64, forward: 4 sequences of
+// 4,096 tokens 582 us, 785 (packed: 762) with each by itself, 8 packed of 1,000 to
+// 4,096 552 and 685; bf16, gradients of 12 x 1,024, 16 heads of 64: 138 us, 149;
+// all of 64 sequences of 1,024, 32 heads of 128: 821 us, 762 with the last 4, 749 with
+// none.  With a window most blocks are as long, and there is nothing to gain.
 template <int RB>
 inline int mixed_seqs(const PromptArgs &a, int h, int resident) {
-    const long long n = (a.T + RB - 1) / RB, m = a.window > 0 ? a.window / RB + 1 : n;
+    const long long n = (a.cu ? a.T_total / a.B : a.T) / RB + 1, m = a.window > 0 ? a.window / RB + 1 : n;
     if (2 * m < n) return 0;
     const long long g = (2LL * resident + h * (n + 1) - 1) / (h * (n + 1));
+    if (a.cu) return a.B > 64 || 2 * g < a.B ? 0 : a.B;
     return (int)(g < a.B ? g : a.B);
 }
 

@@ -266,6 +266,25 @@ def test_bad_offsets_stay_inside():
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,window", [(63, 0), (64, 0), (64, 90), (65, 0), (2, 0)])
+def test_longest_blocks_first(dt, B, window):
+    """Batches of few rounds of workgroups, whose longest blocks go first where they
+    have up to 64 sequences; empty ones, and of equal lengths, among them."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.choice([0, 1, 127, 128, 129, 300], B)]
+    lens[0], lens[-1] = 500, 260
+    H = 560 // (sum(lens) // 128 + B) + 2
+    data = make(lens, H, H, 64, DTYPES[dt], seed=B, tail=2)
+    check(data, lens, 0.125, window, what="%d sequences of %d heads" % (B, H))
+
+
+@pytest.mark.parametrize("B,T,H", [(3, 300, 70), (7, 129, 40), (5, 513, 25)])
+def test_longest_blocks_first_fixed(B, T, H):
+    data = make([T] * B, H, H, 64, torch.bfloat16, seed=T)
+    check(data, [T] * B, 0.125, fixed=B, what="%d x %d" % (B, T))
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("H", [1, 70])
 def test_backward_workspace_is_enough(dt, H):
     """Nothing is written past the bytes that the library asks for, by either
