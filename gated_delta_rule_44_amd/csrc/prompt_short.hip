@@ -73,9 +73,8 @@ __device__ inline f32x4 join4(const char *lds, int stride, int row, int d, const
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         const f32x4 s = *reinterpret_cast<const f32x4 *>(lds + w * stride + (row * (D + 4) + d) * 4);
-        // (a factor of zero leaves a sum of infinities out)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += f[w] == 0.f ? 0.f : f[w] * s[e];
+        for (int e = 0; e < 4; ++e) y[e] += f[w] * s[e];
     }
     return y;
 }
@@ -193,11 +192,14 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     float top = -INFINITY, f[kWaves], sum = 0.f;
 #pragma unroll
     for (int u = 0; u < kWaves; ++u) top = fmaxf(top, sm[u][row]);
+    // A wave whose tokens the row does not attend to has m = -inf, f = 0 and sums of
+    // zero.  So has, but for its sums, one whose logits are all NaN, which the maximum
+    // passes over: 0 times these are NaN.
     const float ms = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int u = 0; u < kWaves; ++u) {
         f[u] = exp2_((sm[u][row] - ms) * k.c);
-        sum += f[u] == 0.f ? 0.f : sl[u][row] * f[u];
+        sum += sl[u][row] * f[u];
     }
     const size_t to = (size_t)(bl.row0 + i0 + row) * a.Hq + head;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -1,0 +1,62 @@
+"""GPU tests of attention over whole prompts at the edges of its values, in both
+forms (blocks of 32 rows and of 128): NaN and infinities that a row attends to."""
+import pytest
+import torch
+
+from tests.conftest import gpu_available
+from tests.test_gpu_prompt import DTYPES, INF, NAN, make, offsets, run_forward, same
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+FORMS = [2, 70]          # heads: blocks of 32 rows, of 128
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", FORMS)
+def test_nan_that_a_row_attends_to(dt, D, H):
+    """o and lse of a row are NaN where its query or a key that it attends to is,
+    also where all of its keys, or all of a tile of them, are; other rows keep
+    their bits."""
+    lens = [150, 40, 128]
+    cu = offsets(lens)
+    data = make(lens, H, H, D, DTYPES[dt], seed=D)
+    for what, n, bad, window, rows in [
+        ("a query", 0, [70], 0, [70]),
+        ("a query of one token", 0, [150], 0, [150]),
+        ("a sequence's first key", 1, [150], 0, range(150, 190)),
+        ("the only key of a row", 1, [60], 1, [60]),
+        ("both keys of a row", 1, [60, 61], 2, [60, 61, 62]),
+        ("a tile of keys", 1, range(32, 64), 0, range(32, 150)),
+        ("a tile of keys in a window", 1, range(32, 64), 40, range(32, 103)),
+        ("two tiles of keys", 1, range(64, 128), 0, range(64, 150)),
+        ("a sequence's keys", 1, range(190, 318), 0, range(190, 318)),
+    ]:
+        clean = run_forward(data, cu, D ** -0.5, window)
+        mine = [x.clone() for x in data]
+        mine[n][list(bad), :, 3] = NAN
+        o, lse = run_forward(mine, cu, D ** -0.5, window)
+        hit = torch.zeros(cu[-1], dtype=torch.bool)
+        hit[list(rows)] = True
+        assert bool(torch.isnan(o[hit]).all()) and bool(torch.isnan(lse[hit]).all()), what
+        assert same(o[~hit], clean[0][~hit]) and same(lse[~hit], clean[1][~hit]), what
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("H", FORMS)
+@pytest.mark.parametrize("low", [[40], range(32, 64), range(0, 64)])
+def test_infinite_values_of_small_weights(dt, H, low):
+    """An infinity of V that a row attends to reaches it whatever its weight is (of
+    one token, or of a tile or two whose weights all vanish beside the others'): the
+    result is not finite, in no other channel."""
+    lens, D = [150], 64
+    data = make(lens, H, H, D, DTYPES[dt], seed=5, amp=1.0)
+    data[0][:, :, 0] = 20.0
+    data[1][:, :, 0] = 0.0
+    data[1][list(low), :, 0] = -80.0             # logits lower by 200
+    clean = run_forward(data, [0, 150], D ** -0.5, 0)
+    data[2][40, :, 5] = INF
+    o, lse = run_forward(data, [0, 150], D ** -0.5, 0)
+    assert not torch.isfinite(o[40:, :, 5]).any()
+    o[40:, :, 5] = clean[0][40:, :, 5]
+    assert same(o, clean[0]) and same(lse, clean[1])
