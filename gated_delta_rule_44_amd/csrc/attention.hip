@@ -156,14 +156,17 @@ int block_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long 
 // registers for loads (26.4 and 23.6; 26.1 and 26.3; 302 and 204).  As above, the
 // table and the window stand for the lengths.
 constexpr long long kFewTokens = 160 << 10;
+int many_rows(long long rows) {
+    const long long blocks = (rows + 127) / 128;
+    return 32 * (int)((rows + 32 * blocks - 1) / (32 * blocks));
+}
 int tree_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long long capacity,
               int window) {
     if (!bf16_io || rows <= 16) return 16;
     const long long seen = window > 0 && window < capacity - n ? window + n : capacity;
     if (seen * B * Hkv * ((rows + 15) / 16) <= kFewTokens) return 16;
     if (rows <= 32) return D == 64 ? 32 : 16;
-    const long long blocks = (rows + 127) / 128;
-    return 32 * (int)((rows + 32 * blocks - 1) / (32 * blocks));
+    return many_rows(rows);
 }
 
 // Workspace: {first slot, slots} of every sequence; with more than kScan of
@@ -174,11 +177,11 @@ int tree_rows(bool bf16_io, long long rows, int B, int n, int Hkv, int D, long l
 struct WsMap {
     size_t sched, slots, ml, o, logits, total;
 };
-WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bool with_scores) {
+WsMap ws_map(const Plan &p, int B, int n, int G, int Hkv, int D, int rw, long long capacity,
+             bool with_scores) {
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
     WsMap w{};
     if (capacity == 0) return w;
-    const Plan p = make_plan(B, n, G, Hkv, rw, capacity);
     const size_t rows = (size_t)p.max_slots * p.units * rw;
     const bool parts = p.max_slots > B;
     w.sched = 0;
@@ -189,6 +192,42 @@ WsMap ws_map(int B, int n, int G, int Hkv, int D, int rw, long long capacity, bo
     w.total = w.logits + (with_scores ? (size_t)B * Hkv * n * G * ((capacity + 31) / 32 * 32) *
                                             sizeof(float) : 0);
     return w;
+}
+
+// A decode's bytes for every dtype and window: the largest over its blocks.
+size_t decode_workspace(int B, int n, int G, int Hkv, int D, long long capacity, bool with_scores) {
+    const long long rows = (long long)n * G;
+    size_t most = 0;
+    for (int rw = 16; rw <= 64 && (rw == 16 || rows > rw / 2); rw *= 2) {
+        const Plan p = make_plan(B, n, G, Hkv, rw, capacity);
+        const size_t x = ws_map(p, B, n, G, Hkv, D, rw, capacity, with_scores).total;
+        if (x > most) most = x;
+    }
+    return most;
+}
+
+// The plan of a tree's blocks of 96 and 128 rows.  Their units are half as many and
+// twice as large, so that the sharing above would ask for up to 2.6 times a decode's
+// bytes.  Past one round of workgroups they have as many slots as a decode's workspace
+// holds, of longer chunks: 32 contexts of 4,000 tokens, 512 rows of 64 channels 125 us
+// against 143 with all of them; 16 of 512 to 8,192, 264 rows of 128 129 and 144; 128
+// of up to 4,096, 96 rows 140 and 156.  One round has all (2 of 16,000, 512 rows 116 us,
+// 142 with half a round), at most 34 MB.
+Plan tree_plan(int B, int n, int G, int Hkv, int D, int rw, long long capacity) {
+    Plan p = make_plan(B, n, G, Hkv, rw, capacity);
+    if (rw <= 64 || 4LL * B * p.units <= kResident) return p;
+    const size_t have = decode_workspace(B, n, G, Hkv, D, capacity, false);
+    if (ws_map(p, B, n, G, Hkv, D, rw, capacity, false).total <= have) return p;
+    const size_t slot = (size_t)p.units * rw * (2 + D) * sizeof(float) + sizeof(int4);
+    const size_t rest = (size_t)B * 2 * sizeof(int) + 4 * 256;         // (and what is rounded up)
+    const size_t slots = have > rest ? (have - rest) / slot : 0;
+    if (slots > (size_t)B) {
+        p.want_slots = (int)slots - B;
+        p.max_slots = (int)slots;
+    } else {
+        p.max_slots = B;                       // a sequence is one slot
+    }
+    return p;
 }
 
 struct KArgs {
@@ -1458,11 +1497,12 @@ template <typename T, int D, int RW, int RT, bool TREE>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
     constexpr int kRows = RW * RT;
     const long long cap = (long long)a.map.max_pages << a.map.page_shift;
-    const WsMap w = ws_map(a.B, a.n, a.G, a.Hkv, D, kRows, cap, a.scores != nullptr);
-    char *ws = static_cast<char *>(a.ws);
     KArgs k{};
     k.a = a;
-    k.plan = make_plan(a.B, a.n, a.G, a.Hkv, kRows, cap);
+    if constexpr (kRows > 64) k.plan = tree_plan(a.B, a.n, a.G, a.Hkv, D, kRows, cap);
+    else                      k.plan = make_plan(a.B, a.n, a.G, a.Hkv, kRows, cap);
+    const WsMap w = ws_map(k.plan, a.B, a.n, a.G, a.Hkv, D, kRows, cap, a.scores != nullptr);
+    char *ws = static_cast<char *>(a.ws);
     k.sched = cap > 0 ? reinterpret_cast<int2 *>(ws + w.sched) : nullptr;
     k.ml = reinterpret_cast<float2 *>(ws + w.ml);
     k.po = reinterpret_cast<float *>(ws + w.o);
@@ -1532,21 +1572,13 @@ hipError_t launch_tree(bool bf16_io, const AttnArgs &a, hipStream_t s) {
 }  // namespace
 
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
-                           bool with_scores) {
-    const int G = Hq / Hkv;
-    // one size for every dtype and window: the largest over the blocks there can be
-    const long long rows = (long long)n * G;
-    size_t most = 0;
-    for (int rw = 16; rw <= 64 && (rw == 16 || rows > rw / 2); rw *= 2) {
-        const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
-        if (x > most) most = x;
-    }
-    // (a tree's blocks of over 64)
-    for (int rw = 96; rw <= 128 && rows > 64; rw += 32) {
-        const size_t x = ws_map(B, n, G, Hkv, D, rw, capacity, with_scores).total;
-        if (x > most) most = x;
-    }
-    return most;
+                           bool with_scores, bool tree) {
+    const int G = Hq / Hkv, rw = many_rows((long long)n * G);
+    const size_t x = decode_workspace(B, n, G, Hkv, D, capacity, with_scores);
+    if (!tree || rw <= 64) return x;
+    const size_t y = ws_map(tree_plan(B, n, G, Hkv, D, rw, capacity), B, n, G, Hkv, D, rw, capacity,
+                            false).total;
+    return x > y ? x : y;
 }
 
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s) {

@@ -19,13 +19,11 @@ using gdr::check_table;
 using gdr::check_workspace;
 using gdr::fail;
 using gdr::finish;
+using gdr::kMaxDrafts;
 using gdr::kMaxPairs;
 using gdr::kMaxQueryRows;
 using gdr::page_shift_of;
 using gdr::reaches;
-
-// a tree's drafts are bits of a word
-constexpr int kMaxDrafts = 64;
 
 gdr_status check_heads(const char *what, int dt, int Hq, int Hkv, int D, float scale, int window) {
     if (dt != GDR_F32 && dt != GDR_BF16)

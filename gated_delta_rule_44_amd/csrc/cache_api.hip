@@ -20,11 +20,22 @@ using gdr::check_table;
 using gdr::check_workspace;
 using gdr::fail;
 using gdr::finish;
+using gdr::kMaxDrafts;
 using gdr::kMaxPairs;
 using gdr::kMaxQueryRows;
 using gdr::kMaxRows;
 using gdr::page_shift_of;
 using gdr::reaches;
+
+size_t attention_bytes(int B, int n_tok, int Hq, int Hkv, int D, int max_pages, int page_size,
+                       bool with_scores, bool tree) {
+    if (B <= 0 || n_tok <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_pages < 0 ||
+        page_shift_of(page_size) < 0 || (long long)max_pages * page_size >= (1LL << 30) ||
+        reaches(B, n_tok, Hq, kMaxQueryRows))
+        return 0;
+    return gdr::attention_workspace(B, n_tok, Hq, Hkv, D, (long long)max_pages * page_size,
+                                    with_scores, tree);
+}
 
 }  // namespace
 
@@ -80,12 +91,9 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
 
 size_t gdr_attention_workspace_bytes(int B, int n_tok, int Hq, int Hkv, int D, int max_pages,
                                      int page_size, int with_scores) {
-    if (B <= 0 || n_tok <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_pages < 0 ||
-        page_shift_of(page_size) < 0 || (long long)max_pages * page_size >= (1LL << 30) ||
-        reaches(B, n_tok, Hq, kMaxQueryRows))
-        return 0;
-    return gdr::attention_workspace(B, n_tok, Hq, Hkv, D, (long long)max_pages * page_size,
-                                    with_scores != 0);
+    // (what a tree can be of: not over kMaxDrafts tokens, no scores)
+    return attention_bytes(B, n_tok, Hq, Hkv, D, max_pages, page_size, with_scores != 0,
+                           n_tok <= kMaxDrafts && !with_scores);
 }
 
 gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int Hkv, int D,
@@ -127,8 +135,8 @@ gdr_status gdr_attention_decode(enum gdr_dtype dt, int B, int n_tok, int Hq, int
     }
     REQUIRE_ALIGNED_OR_NULL(scores, "scores");
     st = check_workspace(what, workspace, ws_bytes,
-                         gdr_attention_workspace_bytes(B, n_tok, Hq, Hkv, D, max_pages, page_size,
-                                                       scores != nullptr));
+                         attention_bytes(B, n_tok, Hq, Hkv, D, max_pages, page_size,
+                                         scores != nullptr, false));
     if (st != GDR_OK) return st;
     gdr::AttnArgs a{};
     a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;

@@ -12,6 +12,9 @@ namespace gdr {
 // threads each), query rows (256 threads), trimmed pairs (1,024 threads)
 constexpr long long kMaxRows = 1LL << 26, kMaxQueryRows = 1LL << 23, kMaxPairs = 1LL << 21;
 
+// a tree's drafts are bits of a word
+constexpr int kMaxDrafts = 64;
+
 inline bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
 #define REQUIRE_I32(p, name)                                                       \

@@ -62,8 +62,9 @@ struct AttnArgs {
     int window;                  // 0: none
     const int32_t *parents;      // [B, n]: a tree of drafts; nullptr: a chain
 };
+// of a decode, or of a tree as well
 size_t attention_workspace(int B, int n, int Hq, int Hkv, int D, long long capacity,
-                           bool with_scores);
+                           bool with_scores, bool tree);
 hipError_t launch_attention_decode(bool bf16_io, int D, const AttnArgs &a, hipStream_t s);
 // drafts of a tree (a.parents), 64 of a sequence at most; no scores
 hipError_t launch_attention_tree(bool bf16_io, int D, const AttnArgs &a, hipStream_t s);

@@ -108,7 +108,9 @@ gdr_status gdr_cache_append(enum gdr_dtype dt, int B, int n_tok, int T_total, in
  *                every row and place of the table, 4 * B * n_tok * Hq *
  *                max_pages * page_size bytes whatever the lengths and the
  *                window are (64 sequences, one token, 32 heads, a table of
- *                131,072 tokens: 1 GiB)
+ *                131,072 tokens: 1 GiB).  Without, and of up to 64 tokens,
+ *                the function counts gdr_attention_tree as well, which can
+ *                take up to 20 MB more than this call needs
  *
  * The lengths are on the device: sizes, launches and the choice of a kernel
  * follow the table's width.  A table no wider than the longest sequence of

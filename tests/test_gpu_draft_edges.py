@@ -1,0 +1,74 @@
+"""GPU tests of trees of drafts and of the decode beside them at the edges of their
+plans and values."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_44_amd as gdr
+from tests import draft_ref as ref
+from tests.conftest import gpu_available
+from tests.gpu_util import announce
+from tests.test_gpu_drafts import DEV, i32, make_cache, queries, sync, trees
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+
+def check_some(o, q, kc, vc, table, lens, parents, scale, some, what):
+    """The sequences `some` of a call against the reference."""
+    want, bound = ref.attend(q[some], kc, vc, table[some], [lens[b] for b in some], parents[some],
+                             scale)
+    err = np.abs(o[some].double().cpu().numpy() - want)
+    announce("  %s: worst error / bound %.3f" % (what, (err / np.maximum(bound, 1e-300)).max()))
+    assert (err <= bound).all(), what
+
+
+# (a decode's bytes at these sizes: what the call took before there were trees)
+@pytest.mark.parametrize("B,n,Hkv,G,D,M,page,need", [
+    (16, 33, 8, 8, 128, 50, 64, 54579456), (80, 64, 4, 2, 64, 80, 64, 28115712)])
+def test_plans_of_many_rows(B, n, Hkv, G, D, M, page, need):
+    """Past one round of workgroups a tree of over 64 rows a head has the slots that a
+    decode's workspace holds, and a decode takes a buffer of that size: neither writes
+    past it, long sequences lie over several slots, and a chain gives what a decode
+    does."""
+    announce("B=%d n=%d Hkv=%d G=%d D=%d" % (B, n, Hkv, G, D))
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(0, 300, B)]
+    long = [1, B // 2, B - 1]
+    for b, x in zip(long, (M * page, 2500, 1300)):
+        lens[b] = x
+    kc, vc, _, table = make_cache(lens, Hkv, D, page, torch.bfloat16, seed=B, extra=0)
+    table = np.pad(table, ((0, 0), (0, M - table.shape[1])), constant_values=-1)
+    q = queries(B, n, Hkv * G, D, torch.bfloat16, seed=n)
+    args = (q.to(DEV), kc.to(DEV), vc.to(DEV), i32(table), i32(lens))
+    assert gdr.attention_workspace_bytes(B, n, Hkv * G, Hkv, D, M, page) == need
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    chain = np.tile(np.arange(n) - 1, (B, 1)).astype(np.int32)
+    for what, parents in (("tree", trees(B, n, seed=3)), ("chain", chain)):
+        o = gdr.attention_tree(*args, i32(parents), scale=D ** -0.5, workspace=ws[:need])
+        sync()
+        assert (ws[need:] == 0x5A).all(), what
+        check_some(o, q, kc, vc, table, lens, parents, D ** -0.5, long[1:], what)
+    d = gdr.attention_decode(*args, scale=D ** -0.5, workspace=ws[:need])
+    sync()
+    assert (ws[need:] == 0x5A).all()
+    check_some(d, q, kc, vc, table, lens, chain, D ** -0.5, long[1:], "decode")
+    # two results within a rounding of o and 2^-15 of the weights each
+    assert torch.allclose(o.float(), d.float(), rtol=2 ** -7, atol=2 ** -13 * 4)
+    with pytest.raises(gdr.GdrError, match="workspace"):
+        gdr.attention_decode(*args, workspace=ws[:need - 16])
+
+
+def test_decode_takes_its_own_bytes():
+    """Where a tree of as many rows takes more, and past the 64 tokens of a tree."""
+    for B, n, Hkv, G, M, page, need in ((2, 64, 8, 8, 250, 64, 17039616), (4, 300, 8, 4, 50, 64, 50585856)):
+        lens = [M * page - 5] + [400] * (B - 1)
+        kc, vc, _, table = make_cache(lens, Hkv, 128, page, torch.bfloat16, seed=n, extra=0)
+        args = (queries(B, n, Hkv * G, 128, torch.bfloat16, n).to(DEV), kc.to(DEV), vc.to(DEV),
+                i32(table), i32(lens))
+        assert table.shape[1] == M
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        o = gdr.attention_decode(*args, workspace=ws[:need])
+        sync()
+        assert (ws[need:] == 0x5A).all()
+        assert torch.equal(o, gdr.attention_decode(*args))
