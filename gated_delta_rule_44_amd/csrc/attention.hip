@@ -1216,7 +1216,7 @@ __global__ __launch_bounds__(64 * W * kTreeShares<W>, 2) void tree_kernel(KArgs 
     auto whole = [&](int i) GDR_INLINE {
         return base + i * kTok >= all_lo && base + (i + 1) * kTok <= all_hi;
     };
-    float m, mc, l;
+    float m, mc, l, behind = 8.f;            // how far a maximum is left behind
     f32x16 acc[kCols];
     auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
@@ -1259,7 +1259,7 @@ __global__ __launch_bounds__(64 * W * kTreeShares<W>, 2) void tree_kernel(KArgs 
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, x[c][e]);
             const float mn = fmaxf(m, swap_max32(top));
-            const bool grow = (mn - m) * k.c > 8.f;
+            const bool grow = (mn - m) * k.c > (CLEAR ? behind : 8.f);
             if (__builtin_amdgcn_ballot_w64(grow)) {
                 const float al = grow ? exp2_((m - mn) * k.c) : 1.f;
                 l *= al;
@@ -1282,7 +1282,17 @@ __global__ __launch_bounds__(64 * W * kTreeShares<W>, 2) void tree_kernel(KArgs 
     };
     walk(std::false_type{});
     if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
-        walk(std::true_type{});
+        // Rows whose sums are infinite or NaN without those values as well are summed
+        // once more with the maximum itself: sums that are joined over slots keep their
+        // scale, so that, as above, finite values have to be below 2^128 / tokens.
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            walk(std::true_type{});
+            if (pass) break;
+            const bool odd = R::any_odd(acc);
+            if (!__syncthreads_or(odd)) break;
+            behind = rows_of(odd) >> r & 1 ? 0.f : 8.f;
+        }
         for (int j = k_lo; j < k_hi; ++j) {
             if ((j - base) % kTok / (32 * kBlk) != share) continue;
             if (whole((j - base) / kTok)) {          // (unless a page of it is absent)

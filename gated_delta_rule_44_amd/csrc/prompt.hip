@@ -45,8 +45,12 @@ struct KArgs {
     int mixed;            // mixed_seqs
 };
 
+// waves a SIMD that a wave's registers leave room for
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) void prompt_kernel(KArgs k) {
+constexpr int kShare = Rows<T, D>::kRowBytes > 256 ? 1 : Rows<T, D>::kRowBytes > 128 ? 2 : 4;
+
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, (kShare<T, D>)) void prompt_kernel(KArgs k) {
     using R = Rows<T, D>;
     constexpr int kTok = R::kTok, kBlk = kTok / 32, kCols = R::kCols;
     __shared__ __align__(1024) char lds[2][2][R::kTileBytes];
@@ -88,11 +92,13 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
         fetch(lds[t & 1][1], vh, row, left, lane);
     };
     float m, mc, l;
+    unsigned small = 0;                      // rows whose weights are kDown times theirs
     f32x16 acc[kCols];
     // All tiles.  CLEAR: infinities and NaN are taken out of V where some row
-    // does not attend to a token.
+    // does not attend to a token, and the weights of `small` rows are made smaller.
     auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
+        const float down = CLEAR && (small >> r & 1) ? kDown : 1.f;
         m = -INFINITY;
         mc = l = 0.f;
 #pragma unroll
@@ -141,6 +147,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     x[b][e] = exp2_(fmaf(x[b][e], k.c, -mc));
+                    if (CLEAR) x[b][e] *= down;
                     l += x[b][e];
                 }
 #pragma unroll
@@ -151,9 +158,16 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     walk(std::false_type{});
     // A weight of zero must not meet an infinity or NaN of V.  Where one has, a
     // result is NaN: then all is done again without such values, and the rows
-    // that do attend to them get them after.
+    // that do attend to them get them after.  Rows whose sums are infinite or NaN
+    // even so are summed once more, smaller (the others to the same bits).
     if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
-        walk(std::true_type{});
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            walk(std::true_type{});
+            if (pass) break;
+            small = rows_of(R::any_odd(acc));
+            if (!__syncthreads_or(small)) break;
+        }
         for (int j = first; j <= last; ++j)
             if (!tile_full(j / kTok) && attends(j))
                 R::add_odd(acc, vh + (size_t)(bl.row0 + j) * a.Hkv * D, h);
@@ -169,7 +183,7 @@ __global__ __launch_bounds__(kThreads, (Rows<T, D>::kRowBytes > 256 ? 1 : 2)) vo
     }
     R::store(static_cast<T *>(a.o) + row * D, acc, h, l == 0.f ? 0.f : 1.f / l);
     if (a.lse && h == 0)
-        a.lse[row] = l == 0.f ? -INFINITY : m * k.ascale + kLn2F * __builtin_amdgcn_logf(l);
+        a.lse[row] = l == 0.f ? -INFINITY : m * k.ascale + kLn2F * __builtin_amdgcn_logf(small >> r & 1 ? l * kUp : l);
 }
 
 // workgroups at a time, by the registers of a wave

@@ -512,6 +512,17 @@ template <int D> struct Rows<float, D> {
     }
 };
 
+// Sums of weights times values are divided by the weights' sum only at the end, so that
+// finite values of V may sum to infinities.  Rows where they did are summed again with
+// weights times kDown: those are then at most 2^-30 (2^8 where a maximum is left
+// behind), and the sums of fewer than 2^29 tokens below the largest value.
+constexpr float kDown = 0x1p-38f, kUp = 0x1p38f;
+// One bit for each of the wave's 32 rows: whether `odd` is set in either half.
+__device__ inline unsigned rows_of(bool odd) {
+    const unsigned long long m = __builtin_amdgcn_ballot_w64(odd);
+    return (unsigned)m | (unsigned)(m >> 32);
+}
+
 // What the backward pass keeps of a row in its workspace: lse log2 e (+inf for a
 // row without weights) and -delta = -do . o, from which the sums do . v start, of
 // which each half of a wave sums half the channels.

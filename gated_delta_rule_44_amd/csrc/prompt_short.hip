@@ -92,6 +92,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     constexpr int kCols = R::kCols, kBufs = O::kBufs, kLds = O::kWave > O::kSums ? O::kWave : O::kSums;
     __shared__ __align__(1024) char lds[kWaves * kLds];
     __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
+    __shared__ unsigned odd_rows[kWaves];
     const PromptArgs &a = k.a;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
     const int w = uniform(tid >> 6);
@@ -120,7 +121,8 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
         own.fetch(buf, 1, vh, row, left, kpitch);
     };
     typename R::B q;
-    float m, mc, l;
+    float m, mc, l, down = 1.f;
+    unsigned small = 0;                      // rows whose weights are kDown times theirs
     f32x16 acc[kCols];
     auto walk = [&](auto clear) GDR_INLINE {
         constexpr bool CLEAR = decltype(clear)::value;
@@ -163,6 +165,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 x[e] = exp2_(fmaf(x[e], k.c, -mc));
+                if (CLEAR) x[e] *= down;
                 l += x[e];
             }
             R::template cols<CLEAR>(acc, own.tile(buf, 1), 0, at, R::operand(x), full);
@@ -173,7 +176,19 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     };
     walk(std::false_type{});
     if (__builtin_expect(__syncthreads_or(R::any_odd(acc)), 0)) {
-        walk(std::true_type{});
+        // (as in prompt.hip, the rows to be smaller those of any wave)
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            walk(std::true_type{});
+            if (pass) break;
+            const unsigned odd = rows_of(R::any_odd(acc));
+            if (lane == 0) odd_rows[w] = odd;
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kWaves; ++u) small |= odd_rows[u];
+            if (!small) break;
+            down = small >> r & 1 ? kDown : 1.f;
+        }
         for (int t = t0; t < t1; t += kWaves)
             for (int j = t * 32; j < t * 32 + 32 && j <= last; ++j)
                 if (!tile_full(t) && attends(j))
@@ -207,10 +222,22 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     for (int d = 4 * x; d < D; d += 32) {
         f32x4 y = join4<D>(lds, kLds, row, d, f) * inv;
         if (sum == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
+        // (finite sums of the waves may add up to an infinity)
+        if (!(fabsf(y[0]) < INFINITY & fabsf(y[1]) < INFINITY & fabsf(y[2]) < INFINITY &
+              fabsf(y[3]) < INFINITY)) {
+            float g[kWaves];
+#pragma unroll
+            for (int u = 0; u < kWaves; ++u) g[u] = f[u] * inv;
+            const f32x4 z = join4<D>(lds, kLds, row, d, g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fabsf(y[e]) < INFINITY ? y[e] : z[e];
+        }
         store4(static_cast<T *>(a.o) + to * D + d, y);
     }
     if (a.lse && x == 0)
-        a.lse[to] = sum == 0.f ? -INFINITY : ms * k.ascale + kLn2F * __builtin_amdgcn_logf(sum);
+        a.lse[to] = sum == 0.f ? -INFINITY
+                               : ms * k.ascale + kLn2F * __builtin_amdgcn_logf(
+                                                             small >> row & 1 ? sum * kUp : sum);
 }
 
 // ------------------------------------------------------------------ backward

@@ -57,7 +57,9 @@ extern "C" {
  *
  * Numerics: fp32 accumulation, logits, softmax statistics and weights; with
  * bf16 inputs a weight enters the product with V as one bf16 number, off by
- * at most 2^-8 of it, and o is rounded once.
+ * at most 2^-8 of it, and o is rounded once.  Values of V up to 2^127 in
+ * magnitude give finite results (those past 2^120 / tokens at up to three
+ * times the cost).
  */
 gdr_status gdr_attention_prefill(enum gdr_dtype dt, int B, int T, int T_total, int Hq, int Hkv,
                                  int D, float scale, int window, const void *q, const void *k,
@@ -116,8 +118,10 @@ gdr_status gdr_attention_backward(enum gdr_dtype dt, int B, int T, int T_total, 
  *     positions are above p - window if window > 0,
  * as far as they are at 0 or above and on a present page.  (A chain, parents
  * t - 1, is gdr_attention_decode.)  Everything else is as there: the softmax,
- * rows without tokens, absent pages, the numerics, the workspace
- * (gdr_attention_workspace_bytes, without scores).
+ * rows without tokens, absent pages, the numerics (sums of weights times
+ * values are divided last: values below 2^128 / tokens in magnitude give
+ * finite results), the workspace (gdr_attention_workspace_bytes, without
+ * scores).
  *
  *   n_tok        drafts per sequence, 0..64 (a smaller tree is padded with
  *                drafts that follow the context)

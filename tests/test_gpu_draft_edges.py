@@ -72,3 +72,30 @@ def test_decode_takes_its_own_bytes():
         sync()
         assert (ws[need:] == 0x5A).all()
         assert torch.equal(o, gdr.attention_decode(*args))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G,wide", [(8, 2, 0), (24, 1, 1), (40, 1, 1), (24, 4, 1), (64, 2, 1)])
+def test_tree_large_values(D, n, G, wide):
+    """Values below 2^128 / tokens give finite results, as in the decode, also where
+    logits grow by a little under 8 ln 2 after the first tile and a maximum is left
+    behind; in blocks of 16 to 128 rows."""
+    L, page, Hkv = 500, 16, 2
+    rng = np.random.default_rng(n)
+    kc, vc, _, table = make_cache([L], Hkv, D, page, torch.bfloat16, seed=D,
+                                  extra=wide * ((160 << 10) // (Hkv * page) + 100))
+    v = torch.from_numpy(rng.choice([-1.0, 1.0], tuple(vc.shape))).bfloat16() * 2.0 ** 118
+    v[..., 3] = 2.0 ** 118
+    vc = torch.where(torch.isnan(vc), vc, v)
+    k = torch.zeros_like(kc)
+    for j in range(L):
+        k[table[0, j // page], :, j % page, 0] = 0.0 if j < 64 else 5.5
+    kc = torch.where(torch.isnan(kc), kc, k)
+    q = torch.zeros((1, n, Hkv * G, D), dtype=torch.bfloat16)
+    q[..., 0] = 8.0
+    parents = trees(1, n, seed=1)
+    o = gdr.attention_tree(q.to(DEV), kc.to(DEV), vc.to(DEV), i32(table), i32([L]), i32(parents),
+                           scale=0.125)
+    sync()
+    assert bool(torch.isfinite(o).all())
+    check_some(o, q, kc, vc, table, [L], parents, 0.125, [0], "n=%d G=%d" % (n, G))

@@ -1,10 +1,12 @@
 """GPU tests of attention over whole prompts at the edges of its values, in both
-forms (blocks of 32 rows and of 128): NaN and infinities that a row attends to."""
+forms (blocks of 32 rows and of 128): NaN and infinities that a row attends to,
+values of V whose sums overflow."""
 import pytest
 import torch
 
+from tests import prompt_ref as ref
 from tests.conftest import gpu_available
-from tests.test_gpu_prompt import DTYPES, INF, NAN, make, offsets, run_forward, same
+from tests.test_gpu_prompt import DTYPES, INF, NAN, make, offsets, run_forward, same, within
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -60,3 +62,62 @@ def test_infinite_values_of_small_weights(dt, H, low):
     assert not torch.isfinite(o[40:, :, 5]).any()
     o[40:, :, 5] = clean[0][40:, :, 5]
     assert same(o, clean[0]) and same(lse, clean[1])
+
+
+# Where sums overflow, weights are taken relative to a number 2^38 times larger: the
+# terms in |s| and |m| of a weight's error (8 u each, twice) gain 38 ln 2 < 27, those of
+# lse (4 u) likewise.
+LIFT = 27 * 2.0 ** -24
+
+
+def check_large(data, lens, scale, window, what):
+    cu = offsets(lens)
+    o, lse = run_forward(data, cu, scale, window)
+    want = ref.forward(*data[:3], cu, scale, window)
+    size = ref.forward(data[0], data[1], data[2].abs(), cu, scale, window)[0]   # sum w |v|
+    within(what + " o", o, want[0], want[2] + 16 * LIFT * size)
+    within(what + " lse", lse, want[1], want[3] + 20 * LIFT)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", FORMS)
+def test_large_values(dt, D, H):
+    """Values up to 2^127: their sums overflow, o does not; in a single channel and
+    row as in all, and beside infinities that other rows attend to."""
+    lens, scale = [300, 40], D ** -0.5
+    for window in (0, 70):
+        data = make(lens, H, H, D, DTYPES[dt], seed=D + 1)
+        v = data[2]
+        v.copy_((v.sign() * (0.5 + v.abs().clamp(max=1) / 2)).double() * 2.0 ** 127)
+        check_large(data, lens, scale, window, "all")
+        v[:, :, ::2] = v[:, :, ::2].sign()
+        v[:100] = v[:100].sign()
+        check_large(data, lens, scale, window, "some")
+        v.copy_(v.abs())
+        check_large(data, lens, scale, window, "of one sign")
+    # rows before an infinity keep what they have without it
+    clean = run_forward(data, offsets(lens), scale, 0)
+    data[2][200, :, 1] = -INF
+    o, lse = run_forward(data, offsets(lens), scale, 0)
+    hit = torch.zeros(340, dtype=torch.bool)
+    hit[200:300] = True
+    assert (o[hit][:, :, 1] == -INF).all() and same(lse, clean[1])
+    o[200:300, :, 1] = clean[0][200:300, :, 1]
+    assert same(o, clean[0])
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("H", FORMS)
+def test_large_values_behind_a_maximum(dt, H):
+    """Logits that grow by a little under 8 ln 2 after the first tile: the weights of
+    all later tokens are near 2^8 beside a maximum that is left behind."""
+    lens, D = [400], 64
+    data = make(lens, H, H, D, DTYPES[dt], seed=4, amp=0.0)
+    data[0][:, :, 0] = 8.0
+    data[1][:, :, 0] = 0.0
+    data[1][64:, :, 0] = 5.5                     # logits of 5.5 after 64 of 0
+    for big in (2.0 ** 105, 2.0 ** 112, 2.0 ** 118, 2.0 ** 127):
+        data[2].copy_(data[2].sign() * big)
+        data[2][:, :, 5] = big
+        check_large(data, lens, D ** -0.5, 0, "values of %g" % big)
