@@ -1,12 +1,14 @@
 """GPU tests of attention over whole prompts at the edges of its values, in both
 forms (blocks of 32 rows and of 128): NaN and infinities that a row attends to,
-values of V whose sums overflow."""
+values of V whose sums overflow, and what it writes under bad offsets."""
 import pytest
 import torch
 
+import gated_delta_rule_44_amd as gdr
 from tests import prompt_ref as ref
 from tests.conftest import gpu_available
-from tests.test_gpu_prompt import DTYPES, INF, NAN, make, offsets, run_forward, same, within
+from tests.test_gpu_prompt import (DEV, DTYPES, INF, NAN, make, offsets, run_forward, same,
+                                   within)
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -121,3 +123,74 @@ def test_large_values_behind_a_maximum(dt, H):
         data[2].copy_(data[2].sign() * big)
         data[2][:, :, 5] = big
         check_large(data, lens, D ** -0.5, 0, "values of %g" % big)
+
+
+def guarded(like, pad=1 << 20):
+    """A tensor like that one between `pad` bytes that are to keep their value."""
+    n = like.numel() * like.element_size()
+    raw = torch.full((pad + n + pad,), 0x5A, dtype=torch.uint8, device=DEV)
+    return raw, raw[pad:pad + n].view(like.dtype).view(like.shape), pad
+
+
+def untouched(raw, pad):
+    return bool((raw[:pad] == 0x5A).all()) and bool((raw[-pad:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("H,D", [(2, 64), (70, 64), (70, 128)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_bad_offsets_write_inside(dt, H, D, window):
+    """Offsets that decrease, overlap or leave the rows (the host copy is not given):
+    what the call computes is unspecified, but it writes within its outputs and its
+    workspace only; of up to 64 sequences (whose longest blocks may go first) and of
+    more."""
+    T, far = 300, (1 << 31) - 1
+    data = [x.to(DEV) for x in make([T], H, H, D, DTYPES[dt], seed=12)]
+    q, k, v, do = data
+    for cu in ([0, 250, 90], [-5, 70, 400], [0, 400, 160], [T, 0, T], [-far - 1, 3, far],
+               [0, T] * 32 + [0], [T, 0] * 33, list(range(T, T - 130, -2)), [0] * 30 + [T] * 35 + [-1] * 9):
+        cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        ro, o, pad = guarded(q)
+        rl, lse, _ = guarded(torch.empty((T, H), device=DEV))
+        o.zero_()
+        lse.zero_()
+        gdr.attention_prefill(q, k, v, cu_seqlens=cu, scale=0.125, window=window, lse=lse, o=o)
+        outs = [guarded(x) for x in (q, k, v)]
+        need = gdr.attention_backward_workspace_bytes(DTYPES[dt], cu.numel() - 1, T, H, H, D)
+        rw, ws, _ = guarded(torch.zeros(need, dtype=torch.uint8, device=DEV))
+        ws.zero_()
+        gdr.attention_backward(q, k, v, o, lse, do, cu_seqlens=cu, scale=0.125, window=window,
+                               dq=outs[0][1], dk=outs[1][1], dv=outs[2][1], workspace=ws)
+        torch.cuda.synchronize(DEV)
+        for raw in [ro, rl, rw] + [x[0] for x in outs]:
+            assert untouched(raw, pad), cu[:4].tolist()
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("H", FORMS)
+def test_padded_batches_write_inside(dt, H):
+    """Outputs and workspace between guards, sequences that end inside a block and rows
+    behind the last one."""
+    lens, D = [1, 129, 0, 70], 128
+    data = make(lens, H, H, D, DTYPES[dt], seed=13, tail=37)
+    q, k, v, do = (x.to(DEV) for x in data)
+    cu = torch.tensor(offsets(lens), dtype=torch.int32, device=DEV)
+    want = run_forward(data, offsets(lens), D ** -0.5, 0)
+    ro, o, pad = guarded(q)
+    rl, lse, _ = guarded(torch.empty(q.shape[:2], device=DEV))
+    o.fill_(7.0)
+    lse.fill_(7.0)
+    gdr.attention_prefill(q, k, v, cu_seqlens=cu, lse=lse, o=o)
+    assert same(o, want[0]) and same(lse, want[1])
+    outs = [guarded(x) for x in (q, k, v)]
+    for _, x, _ in outs:
+        x.fill_(7.0)
+    need = gdr.attention_backward_workspace_bytes(DTYPES[dt], len(lens), q.shape[0], H, H, D)
+    rw, ws, _ = guarded(torch.zeros(need, dtype=torch.uint8, device=DEV))
+    gdr.attention_backward(q, k, v, o, lse, do, cu_seqlens=cu, dq=outs[0][1], dk=outs[1][1],
+                           dv=outs[2][1], workspace=ws)
+    torch.cuda.synchronize(DEV)
+    for raw in [ro, rl, rw] + [x[0] for x in outs]:
+        assert untouched(raw, pad)
+    for _, x, _ in outs:
+        assert bool((x[sum(lens):] == 7).all())
