@@ -353,7 +353,9 @@ def cache_resize(page_table, seq_lens, want, page_size: int, num_pages: int, new
     for or (then the row keeps its length) none.
 
     page_table int32 [B,max_pages] with a row for every sequence that holds
-    pages of the num_pages there are; seq_lens, want int32 [B], all on the GPU.
+    pages of the num_pages there are, and -1 past the columns of seq_lens
+    (after cache_evict, which leaves the table as it is: a call with the old
+    lengths and the new ones); seq_lens, want int32 [B], all on the GPU.
     cu_seqlens int32 [B+1], when given, receives the offsets of the tokens
     that the rows grow by, for cache_append.  Returns (new_lens int32 [B],
     free int32 [1]: the free pages left); new_lens may be seq_lens or want.  A

@@ -171,10 +171,17 @@ gdr_status gdr_cache_accept(enum gdr_dtype dt, int B, int n_tok, int Hkv, int D,
  *   * A row that shrinks drops its entries past the new length (-1), and
  *     their pages are free if no other row keeps them.
  *   * Rows that grow are served in their order, their new columns in theirs,
- *     with the free pages from the lowest number up.  A row is served in full
- *     or not at all: it is if the pages asked for by the rows up to it
- *     (itself included, served or not) are at most the free ones.
+ *     with the free pages from the lowest number up.  A row that asks for
+ *     pages is served in full or not at all: it is if the pages asked for by
+ *     the rows up to it (itself included, served or not) are at most the free
+ *     ones.  A row that grows within its last page asks for none.
  *   * new_lens[b] = want[b], or seq_lens[b] for a row that is not served.
+ *   * Columns past a row's old and new pages are neither read nor written.  They
+ *     are to hold -1 (a call that shortens lengths in another way, as
+ *     gdr_cache_evict, is followed by one with the old lengths and the new ones):
+ *     then tokens appended to a row that was not served fall on absent pages.
+ *     Such a row has no drafts: gdr_attention_tree and gdr_cache_accept would
+ *     take its newest tokens for them (leaf -1 moves nothing).
  * A table of one column whose rows hold 0 or 1 tokens is a slot map of a
  * state pool (gdr_decode_tokens, gdr_prefill_varlen_pool).
  *

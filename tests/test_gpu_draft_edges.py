@@ -5,10 +5,10 @@ import pytest
 import torch
 
 import gated_delta_rule_44_amd as gdr
-from tests import draft_ref as ref
+from tests import cache_ref, draft_ref as ref
 from tests.conftest import gpu_available
 from tests.gpu_util import announce
-from tests.test_gpu_drafts import DEV, i32, make_cache, queries, sync, trees
+from tests.test_gpu_drafts import DEV, i32, make_cache, queries, same, sync, trees
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -99,3 +99,53 @@ def test_tree_large_values(D, n, G, wide):
     sync()
     assert bool(torch.isfinite(o).all())
     check_some(o, q, kc, vc, table, [L], parents, 0.125, [0], "n=%d G=%d" % (n, G))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_round_with_too_few_pages(dt):
+    """A round of drafts in which some sequences get no pages: those that need none are
+    served after them all the same, what is appended to the others falls on absent
+    pages or past their lengths, and every sequence keeps its tokens."""
+    B, Hkv, D, page, P, M, n = 5, 2, 64, 16, 12, 6, 4
+    lens = [40, 32, 47, 20, 28]                  # 3 + 2 + 3 + 2 + 2 pages, all of them
+    k0, v0, _, t0 = make_cache(lens, Hkv, D, page, dt, seed=3)
+    kc, vc = (torch.full((P, Hkv, page, D), float("nan"), dtype=dt) for _ in range(2))
+    full, at = np.full((B, M), -1, np.int32), np.random.default_rng(0).permutation(P).tolist()
+    for b, l in enumerate(lens):
+        for c in range(-(-l // page)):
+            p = full[b, c] = at.pop()
+            kc[p], vc[p] = k0[t0[b, c]], v0[t0[b, c]]
+    dk, dv, tb, start = kc.to(DEV), vc.to(DEV), i32(full), i32(lens)
+    held, free = gdr.cache_resize(tb, start, start + n, page, P)
+    sync()
+    served = [True, False, False, True, True]     # (the others lack a page each)
+    assert held.tolist() == [l + n if s else l for l, s in zip(lens, served)] and free.item() == 0
+    assert tb.cpu().numpy().tolist() == full.tolist()
+    rng = np.random.default_rng(1)
+    k, v = (torch.from_numpy(rng.standard_normal((B, n, Hkv, D))).to(dt) for _ in range(2))
+    gdr.cache_append(k.to(DEV), v.to(DEV), start, tb, dk, dv)
+    parents = trees(B, n, seed=2)
+    q = queries(B, n, 2 * Hkv, D, dt, seed=5)
+    o = gdr.attention_tree(q.to(DEV), dk, dv, tb, held, i32(parents), scale=0.125)
+    ok = held == start + n
+    ends, path = gdr.cache_accept(dk, dv, tb, held, i32(parents), torch.where(ok, n - 1, -1).int())
+    ends = torch.where(ok, ends, start)
+    last, free = gdr.cache_resize(tb, held, ends, page, P)
+    sync()
+    assert last.tolist() == ends.tolist() and free.item() == 0
+    mine = tb.cpu().numpy()
+    assert mine.tolist() == full.tolist()
+    both = kc.clone(), vc.clone()
+    for b in range(B):
+        way = ref.way(parents[b], n - 1) if served[b] else []
+        assert path[b].tolist() == way + [-1] * (n - len(way)) and ends[b] == lens[b] + len(way)
+        for j in range(lens[b] + len(way)):
+            p, s = cache_ref.place(mine, P, page, b, j)
+            for x, y, z in ((dk, kc, k), (dv, vc, v)):
+                assert same(x[p, :, s], y[p, :, s] if j < lens[b] else z[b, way[j - lens[b]]]), (b, j)
+        if served[b]:
+            for t in range(n):
+                p, s = cache_ref.place(full, P, page, b, lens[b] + t)
+                both[0][p, :, s], both[1][p, :, s] = k[b, t], v[b, t]
+    some = [b for b in range(B) if served[b]]
+    check_some(o, q, *both, full, [l + n for l in lens], parents, 0.125, some, "served")
