@@ -45,6 +45,7 @@ def _prompts(q, k, v, cu_seqlens, cu_seqlens_host, window):
     _int("the number of tokens", total, 0)
     _int("the number of sequences", B, 0)
     _int("Hq", Hq, 1)
+    _int("D", D, 1)
     _int("window", window, 0)
     return dev, dtype, dt, (B, T, total, Hq, Hkv, D), host
 
@@ -79,6 +80,7 @@ def attention_backward_workspace_bytes(dtype, n_seqs: int, tokens: int, heads: i
                                        dim: int) -> int:
     """Bytes of device workspace attention_backward needs over n_seqs sequences
     of `tokens` tokens in all (include/gdr_attention.h)."""
+    _need(dtype in _DTYPES, "dtype must be bfloat16 or float32, got %s" % dtype)
     return int(_load().gdr_attention_backward_workspace_bytes(
         _DTYPES[dtype], int(n_seqs), int(tokens), int(heads), int(kv_heads), int(dim)))
 

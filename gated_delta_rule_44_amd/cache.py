@@ -47,7 +47,7 @@ def _cache(k_cache, v_cache, scores):
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise GdrError("the cache must be bfloat16 or float32, got %s" % dtype)
-    if len(shape) != 4 or shape[1] < 1:
+    if len(shape) != 4 or shape[1] < 1 or shape[3] < 1:
         raise GdrError("k_cache must be [P,Hkv,page,D], got %s" % list(shape))
     _gpu("v_cache", v_cache, dtype, dev, shape)
     if scores is not None:

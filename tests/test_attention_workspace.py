@@ -43,3 +43,10 @@ def test_decode_bytes(lib, size, need):
         del kw["sc"]
         assert tree_abi.tree(lib, ws_bytes=got - 1, **kw) == cache_abi.EINVAL
         assert "workspace of %d bytes needed" % got in cache_abi.err(lib)
+
+
+def test_backward_bytes_refuse_other_types(lib):
+    torch = pytest.importorskip("torch")
+    assert gdr.attention_backward_workspace_bytes(torch.bfloat16, 2, 600, 4, 2, 128) > 0
+    with pytest.raises(gdr.GdrError, match="bfloat16 or float32"):
+        gdr.attention_backward_workspace_bytes(torch.float16, 2, 600, 4, 2, 128)

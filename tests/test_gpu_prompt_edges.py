@@ -194,3 +194,17 @@ def test_padded_batches_write_inside(dt, H):
         assert untouched(raw, pad)
     for _, x, _ in outs:
         assert bool((x[sum(lens):] == 7).all())
+
+
+def test_refuses_heads_without_channels():
+    q = torch.zeros(2, 3, 4, 0, device=DEV)
+    with pytest.raises(gdr.GdrError, match="D = 0"):
+        gdr.attention_prefill(q, q, q)
+    with pytest.raises(gdr.GdrError, match="D = 0"):
+        gdr.attention_backward(q, q, q, q, q[..., 0:0].sum(-1), q)
+    table = torch.zeros(2, 1, device=DEV, dtype=torch.int32)
+    cache, lens = torch.zeros(4, 4, 16, 0, device=DEV), torch.ones(2, device=DEV, dtype=torch.int32)
+    with pytest.raises(gdr.GdrError, match="k_cache must be"):
+        gdr.attention_decode(q, cache, cache, table, lens)
+    with pytest.raises(gdr.GdrError, match="k_cache must be"):
+        gdr.attention_tree(q, cache, cache, table, lens, table.expand(2, 3).contiguous())
