@@ -421,21 +421,21 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     k.lse2 = static_cast<float *>(a.ws);
     k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     hipError_t e;
-    if (few_rows<T, D>(a, blocks * a.Hq, 1)) {
+    if (few_rows<T, D, Pass::kQueries>(a, a.Hq)) {
         e = launch_queries_short(sizeof(T) == 2, D, a, s);
     } else {
-        k.mixed = mixed_seqs<kRows>(a, a.Hq, kQueries<T, D>);
+        k.mixed = mixed_seqs<T, kRows>(a, a.Hq, kQueries<T, D>);
         query_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
         e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
-    if (few_rows<T, D>(a, blocks * a.Hkv, a.G)) return launch_keys_short(sizeof(T) == 2, D, a, s);
+    if (few_rows<T, D, Pass::kKeys>(a, a.Hkv)) return launch_keys_short(sizeof(T) == 2, D, a, s);
     if constexpr (sizeof(T) == 2) {
         constexpr int kTokens = 32 * kPairs<D>;
-        k.mixed = mixed_seqs<kTokens>(a, a.Hkv, kKeys<T, D>);
+        k.mixed = mixed_seqs<T, kTokens>(a, a.Hkv, kKeys<T, D>);
         key_pairs_kernel<D, kPairs<D>><<<(unsigned)(block_bound<kTokens>(a) * a.Hkv), 4 * kTokens, 0, s>>>(k);
     } else {
-        k.mixed = mixed_seqs<kRows>(a, a.Hkv, kKeys<T, D>);
+        k.mixed = mixed_seqs<T, kRows>(a, a.Hkv, kKeys<T, D>);
         key_kernel<T, D><<<(unsigned)(blocks * a.Hkv), kThreads, 0, s>>>(k);
     }
     return hipGetLastError();

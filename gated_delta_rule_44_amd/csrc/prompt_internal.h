@@ -143,41 +143,75 @@ __device__ inline Block find_block(const PromptArgs &a, int s, int mixed) {
     return x;
 }
 
-// How many: as many as keep the card's places for workgroups (`resident`) as long
-// as the longest block takes; h heads.  fp32, 8 heads of 64, forward: 4 sequences of
-// 4,096 tokens 582 us, 785 (packed: 762) with each by itself, 8 packed of 1,000 to
-// 4,096 552 and 685; bf16, gradients of 12 x 1,024, 16 heads of 64: 138 us, 149;
-// all of 64 sequences of 1,024, 32 heads of 128: 821 us, 762 with the last 4, 749 with
-// none.  With a window most blocks are as long, and there is nothing to gain.
-template <int RB>
+// How many (of packed sequences only where they are 64 at most): in fp32 all, in bf16,
+// whose products wait for what comes from beyond the caches, as many as keep the card's
+// places for workgroups (`resident`) as long as the longest block takes, over h heads.
+// Where a window is less than half of a sequence most blocks are as long, and bf16 calls
+// go sequence by sequence.  In turn on warmed calls, us so, and sequence by sequence:
+//   fp32, forward: 4 sequences of 4,096 tokens, 8 heads of 64, 577, 778 (packed: 579,
+//     757), 8 of 1,000 to 4,096 548, 678, 8 of 700 to 2,900, 16 heads, window 1,024 424,
+//     492, window 700 348, 384; gradients, 8 of 4,407, window 1,022, 2,187, 2,401; the
+//     worst of 50 sizes 4 % slower (5 of 100 to 605, 64 heads of 128);
+//   bf16, gradients of 12 x 1,024, 16 heads of 64 138, 145; forward, 9 of 400 to 2,356, 8
+//     heads of 128 18 % sooner; all of 64 sequences of 1,024, 32 heads of 128 804, with
+//     the last 4 737, with none 740; 17 of 1,517, window 446, 8 heads of 64 37 with all,
+//     41 as it is, 38 of 649, window 207, 8 heads of 128 10 % slower with all.
+template <typename T, int RB>
 inline int mixed_seqs(const PromptArgs &a, int h, int resident) {
+    if (a.cu && a.B > 64) return 0;
+    if (sizeof(T) == 4) return a.B;
     const long long n = (a.cu ? a.T_total / a.B : a.T) / RB + 1, m = a.window > 0 ? a.window / RB + 1 : n;
     if (2 * m < n) return 0;
     const long long g = (2LL * resident + h * (n + 1) - 1) / (h * (n + 1));
-    if (a.cu) return a.B > 64 || 2 * g < a.B ? 0 : a.B;
+    if (a.cu) return 2 * g < a.B ? 0 : a.B;
     return (int)(g < a.B ? g : a.B);
 }
 
-// Whether blocks of 32 rows (prompt_short.hip) are done sooner than `wgs` of
-// 128, with what a mean row attends to `times` over in a workgroup's loop.  The
-// short form spreads a block over four workgroups and their waves, which pays
-// while the long one leaves CUs idle and its workgroups are long; it reads every
-// tile four times as often.  Measured, long against short, in us (forward; the
-// two backward kernels turn at the same places): bf16, 128 channels, 64
-// workgroups of 1,024 tokens 24 / 14, 128 of 2,048 42 / 29 and of 512 16 / 17,
-// 256 of 1,024 26 / 39 and of 4,096 80 / 84; 64 channels, 128 of 512 11 / 8, 256
-// of 512 12 / 15, of 1,024 18 / 19 and of 4,096 57 / 42, 512 of 2,048 43 / 48;
-// fp32, 64 channels, 256 of 512 43 / 42 and of 4,096 300 / 181, 512 of 1,024
-// 139 / 122, of 2,048 269 / 201 and of a window of 256 58 / 89, 1,024 of 2,048
-// 395 / 401.
-template <typename T, int D>
-inline bool few_rows(const PromptArgs &a, long long wgs, int times) {
-    long long len = a.T_total / a.B;
-    if (a.window > 0 && a.window < len) len = a.window;
-    len *= times;
-    if (sizeof(T) == 2 && D == 128) return wgs <= 128;
-    if (sizeof(T) == 4 && len >= 2048) return wgs <= 512;
-    return wgs <= (len >= 1024 ? 256 : 128);
+// Whether blocks of 32 rows (prompt_short.hip) are done sooner than blocks of 128, over
+// h heads: query heads, for the keys' kernel key-value heads.  The long form's time is
+// that of its longest workgroups while it has few of them, the short form's, which
+// spreads a block over four workgroups and reads every tile four times as often, that of
+// all.  So what counts is the blocks of 32 times what a mean one attends to, as a share
+// of the longest of 128, against a limit that grows with the longest: in units of 4
+// blocks of 128 half full, so that without a window it is the long form's workgroups.
+//   Measured, long against short, in us (the kernels alone; the gradients with the other
+// kernel in the long form), at limits of steps of the longest:
+//   bf16, 128 channels: forward, 64 workgroups of 256 tokens 10.7 / 8.0, 128 10.6 / 13.1,
+//     128 of 1,024 22.7 / 20.1, 192 22.9 / 29.4, of 4,096 73 / 68, 256 73 / 81;
+//     queries, 192 of 2,048 127 / 115, 256 128 / 130; keys, 128 of 1,024 73 / 66, 192
+//     74 / 84;
+//   64 channels: forward, 128 of 256 7.3 / 7.2, 192 7.4 / 11.3, 256 of 2,048 28.2 / 24.7,
+//     384 29.5 / 33.5; keys, 192 of 2,048 67.6 / 65.2, 256 69.2 / 72.5;
+//   fp32, 64 channels: forward, 256 of 512 42.6 / 40.8, 384 55.7 / 65.1, 384 of 1,024
+//     98.8 / 94.1, 512 106 / 122, of 2,048 204 / 201, 768 265 / 305; with a window of
+//     1,024, 192 of 4,096 89.8 / 83.7, 256 89.2 / 102; keys, 384 of 2,048 574 / 565, 512
+//     617 / 672;
+//   128 channels: forward, 256 of 512 78.1 / 72.9, 384 85.9 / 112, of 4,096 561 / 515,
+//     512 605 / 672; keys, 256 of 1,024 499 / 424, 384 505 / 533.
+// Over 923 sizes of 60 to 4,800 tokens, windows and packed batches among them, the form
+// taken is 0.2 % slower than the faster one in the mean, and past 10 % in 13 of 2,769
+// (up to 43 %, of 6 us: 8 of 174 tokens, window 31).
+enum class Pass { kForward, kQueries, kKeys };
+// of longest blocks that attend to fewer than 384, 1,024, 2,048, 4,096 tokens, and to more
+struct Few { int blocks[5]; };
+template <typename T, int D, Pass PASS>
+constexpr Few kFew = sizeof(T) == 4 ? (D == 64 && PASS != Pass::kKeys ? Few{208, 288, 392, 576, 576}
+                                                                : Few{208, 288, 352, 448, 448})
+                     : D == 64      ? (PASS != Pass::kKeys ? Few{128, 176, 256, 360, 360}
+                                                     : Few{80, 128, 176, 224, 256})
+                                    : (PASS == Pass::kForward   ? Few{66, 96, 128, 160, 224}
+                                       : PASS == Pass::kQueries ? Few{66, 144, 208, 240, 320}
+                                                          : Few{80, 128, 128, 160, 184});
+template <typename T, int D, Pass PASS>
+inline bool few_rows(const PromptArgs &a, int h) {
+    const long long len = a.T_total > a.B ? a.T_total / a.B : 1, w = a.window;
+    const bool windowed = w > 0 && w < len;
+    const long long blocks = (a.cu ? (a.T_total + 31LL) / 32 + a.B / 2 : a.B * ((len + 31) / 32)) * h;
+    const long long top = windowed && w + 128 < len ? w + 128 : len;
+    const long long mean = windowed ? 2 * w - w * w / len + 32 : len;      // (twice)
+    // (mean / top is over 1 / 4, so that a call taken is far from filling a launch)
+    const int step = (top >= 384) + (top >= 1024) + (top >= 2048) + (top >= 4096);
+    return blocks * mean <= 4 * top * kFew<T, D, PASS>.blocks[step];
 }
 
 // The query head of workgroup number u of a block's Hq: workgroups go to the

@@ -12,7 +12,7 @@ from tests.test_gpu_prompt import (DEV, DTYPES, INF, NAN, make, offsets, run_for
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
-FORMS = [2, 70]          # heads: blocks of 32 rows, of 128
+FORMS = [2, 260]         # heads: blocks of 32 rows, of 128
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
@@ -137,7 +137,7 @@ def untouched(raw, pad):
 
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
-@pytest.mark.parametrize("H,D", [(2, 64), (70, 64), (70, 128)])
+@pytest.mark.parametrize("H,D", [(2, 64), (260, 64), (260, 128)])
 @pytest.mark.parametrize("window", [0, 50])
 def test_bad_offsets_write_inside(dt, H, D, window):
     """Offsets that decrease, overlap or leave the rows (the host copy is not given):
