@@ -2,11 +2,10 @@
 // kept of a tree of drafts, and page tables that follow the sequences' lengths.
 #include "cache_internal.h"
 #include "device_util.h"
+#include "wave.h"
 
 namespace gdr {
 namespace {
-
-__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // ------------------------------------------------------------------ accept
 
@@ -129,17 +128,9 @@ constexpr int kGroup = 16;                       // words of a group of pages
 constexpr int kWords = kMaxPages / 32, kGroups = kWords / kGroup;
 constexpr int kRowsAtOnce = 16;                  // rows whose entries a wave requests together
 
-// Sums over the workgroup's threads before this one; total: over all.  Within a
-// wave by DPP: shifts within rows of 16 lanes, then the rows' last lanes.
+// Sums over the workgroup's threads before this one; total: over all.
 __device__ inline int scan(int x, int &total, int *lds) {
-    const int w = threadIdx.x >> 6;
-    int incl = x;
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, true);      // row_shr:1
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);     // row_bcast:15
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);     // row_bcast:31
+    const int w = threadIdx.x >> 6, incl = wave_scan(x);
     if ((threadIdx.x & 63) == 63) lds[w] = incl;
     __syncthreads();
     int before = 0;

@@ -9,6 +9,7 @@
 
 #include "device_util.h"
 #include "gdr_internal.h"
+#include "wave.h"
 
 // on lambdas: the compiler leaves large ones, and those on rare paths, as calls,
 // with all that they capture in memory
@@ -40,25 +41,7 @@ hipError_t launch_keys_short(bool bf16_io, int D, const PromptArgs &a, hipStream
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ inline float swap_max32(float x) {
-    float a = x, b = x;
-    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
-    return fmaxf(a, b);
-}
-
-// The sum over a wave's lanes, which all take part: DPP shifts within rows of 16, the
-// rows' last lanes after.
-__device__ inline int wave_sum(int x) {
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);      // row_shr:1
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);     // row_bcast:15
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);     // row_bcast:31
-    return __builtin_amdgcn_readlane(x, 63);
-}
 
 // A block of RB tokens of one sequence: its number in the sequence (-1: there
 // is none), the sequence's first row and its tokens.
