@@ -199,7 +199,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     k.c = fminf(fmaxf(fabsf(a.scale * kLog2e), 1.4e-45f), 3.4e38f);
     k.negative = a.scale < 0.f;
     const long long blocks = block_bound<kRows>(a);
-    if (few_rows<T, D, Pass::kForward>(a, a.Hq)) return launch_prompt_short(sizeof(T) == 2, D, a, s);
+    if (few_rows<T, D, Pass::kForward>(a)) return launch_prompt_short(sizeof(T) == 2, D, a, s);
     k.mixed = mixed_seqs<T, kRows>(a, a.Hq, kResident<T, D>);
     prompt_kernel<T, D><<<(unsigned)(blocks * a.Hq), kThreads, 0, s>>>(k);
     return hipGetLastError();

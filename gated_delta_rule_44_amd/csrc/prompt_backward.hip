@@ -421,7 +421,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
     k.lse2 = static_cast<float *>(a.ws);
     k.start = k.lse2 + (size_t)a.Hq * a.T_total;
     hipError_t e;
-    if (few_rows<T, D, Pass::kQueries>(a, a.Hq)) {
+    if (few_rows<T, D, Pass::kQueries>(a)) {
         e = launch_queries_short(sizeof(T) == 2, D, a, s);
     } else {
         k.mixed = mixed_seqs<T, kRows>(a, a.Hq, kQueries<T, D>);
@@ -429,7 +429,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
         e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
-    if (few_rows<T, D, Pass::kKeys>(a, a.Hkv)) return launch_keys_short(sizeof(T) == 2, D, a, s);
+    if (few_rows<T, D, Pass::kKeys>(a)) return launch_keys_short(sizeof(T) == 2, D, a, s);
     if constexpr (sizeof(T) == 2) {
         constexpr int kTokens = 32 * kPairs<D>;
         k.mixed = mixed_seqs<T, kTokens>(a, a.Hkv, kKeys<T, D>);

@@ -150,51 +150,60 @@ inline int mixed_seqs(const PromptArgs &a, int h, int resident) {
     return (int)(g < a.B ? g : a.B);
 }
 
-// Whether blocks of 32 rows (prompt_short.hip) are done sooner than blocks of 128, over
-// h heads: query heads, for the keys' kernel key-value heads.  The long form's time is
-// that of its longest workgroups while it has few of them, the short form's, which
-// spreads a block over four workgroups and reads every tile four times as often, that of
-// all.  So what counts is the blocks of 32 times what a mean one attends to, as a share
-// of the longest of 128, against a limit that grows with the longest: in units of 4
-// blocks of 128 half full, so that without a window it is the long form's workgroups.
-//   Measured, long against short, in us (the kernels alone; the gradients with the other
-// kernel in the long form), at limits of steps of the longest:
+// Whether blocks of 32 rows (prompt_short.hip) are done sooner than blocks of 128.  The
+// long form's time is that of its longest workgroups while it has few of them, the short
+// form's, which spreads a block over four workgroups and reads every tile four times as
+// often, that of all.  So what counts is the blocks of 32 times what a mean one attends
+// to, as a share of the longest of 128, against a limit that grows with the longest loop
+// (of the keys' kernel: times the heads of a group).  Its unit is 4 blocks of 128 half
+// full, so that without a window it is the long form's workgroups; packed sequences,
+// whose lengths differ, count for 7 / 8.
+//   Measured, long against short, in us (the kernels alone; of the gradients both, the
+// other one in the long form):
 //   bf16, 128 channels: forward, 64 workgroups of 256 tokens 10.7 / 8.0, 128 10.6 / 13.1,
 //     128 of 1,024 22.7 / 20.1, 192 22.9 / 29.4, of 4,096 73 / 68, 256 73 / 81;
 //     queries, 192 of 2,048 127 / 115, 256 128 / 130; keys, 128 of 1,024 73 / 66, 192
 //     74 / 84;
-//   64 channels: forward, 128 of 256 7.3 / 7.2, 192 7.4 / 11.3, 256 of 2,048 28.2 / 24.7,
-//     384 29.5 / 33.5; keys, 192 of 2,048 67.6 / 65.2, 256 69.2 / 72.5;
+//   64 channels: forward, 128 of 512 10.2 / 7.7, 192 10.2 / 11.5, 256 of 2,048 28.2 /
+//     24.7, 384 29.5 / 33.5; keys, 192 of 2,048 67.6 / 65.2, 256 69.2 / 72.5;
 //   fp32, 64 channels: forward, 256 of 512 42.6 / 40.8, 384 55.7 / 65.1, 384 of 1,024
 //     98.8 / 94.1, 512 106 / 122, of 2,048 204 / 201, 768 265 / 305; with a window of
 //     1,024, 192 of 4,096 89.8 / 83.7, 256 89.2 / 102; keys, 384 of 2,048 574 / 565, 512
-//     617 / 672;
+//     617 / 672, of 4 heads a group, 384 1,797 / 1,636, 512 2,085 / 2,159;
 //   128 channels: forward, 256 of 512 78.1 / 72.9, 384 85.9 / 112, of 4,096 561 / 515,
-//     512 605 / 672; keys, 256 of 1,024 499 / 424, 384 505 / 533.
-// Over 923 sizes of 60 to 4,800 tokens, windows and packed batches among them, the form
-// taken is 0.2 % slower than the faster one in the mean, and past 10 % in 13 of 2,769
-// (up to 43 %, of 6 us: 8 of 174 tokens, window 31).
+//     512 605 / 672; keys, 256 of 1,024 499 / 424, 384 505 / 533, packed, of 512 to 2,048
+//     tokens, 4 heads a group, 400 3,341 / 2,773, 650 4,473 / 4,546.
+// Over 1,667 sizes of 50 to 4,800 tokens, windows and packed batches among them, the form
+// taken is 0.2 % slower than the faster one in the mean, and past 10 % in 14 of 5,001 (up
+// to 42 %, of 6 us: 8 of 174 tokens, window 31).
 enum class Pass { kForward, kQueries, kKeys };
-// of longest blocks that attend to fewer than 384, 1,024, 2,048, 4,096 tokens, and to more
+// of longest loops of fewer than 384, 1,024, 2,048, 4,096 tokens, and of more
 struct Few { int blocks[5]; };
 template <typename T, int D, Pass PASS>
-constexpr Few kFew = sizeof(T) == 4 ? (D == 64 && PASS != Pass::kKeys ? Few{208, 288, 392, 576, 576}
-                                                                : Few{208, 288, 352, 448, 448})
-                     : D == 64      ? (PASS != Pass::kKeys ? Few{128, 176, 256, 360, 360}
-                                                     : Few{80, 128, 176, 224, 256})
-                                    : (PASS == Pass::kForward   ? Few{66, 96, 128, 160, 224}
-                                       : PASS == Pass::kQueries ? Few{66, 144, 208, 240, 320}
-                                                          : Few{80, 128, 128, 160, 184});
+constexpr Few few_blocks() {
+    constexpr bool kWide = D == 128;
+    if (sizeof(T) == 4) {
+        if (PASS == Pass::kForward) return kWide ? Few{196, 316, 336, 416, 448} : Few{196, 300, 392, 576, 640};
+        if (PASS == Pass::kQueries) return kWide ? Few{140, 316, 336, 388, 448} : Few{160, 238, 392, 576, 576};
+        return kWide ? Few{164, 344, 376, 424, 448} : Few{208, 304, 400, 424, 544};
+    }
+    if (PASS == Pass::kForward) return kWide ? Few{65, 100, 136, 182, 224} : Few{100, 166, 250, 360, 360};
+    if (PASS == Pass::kQueries) return kWide ? Few{65, 120, 208, 248, 288} : Few{72, 172, 312, 376, 440};
+    return kWide ? Few{66, 120, 150, 176, 194} : Few{48, 110, 176, 240, 264};
+}
 template <typename T, int D, Pass PASS>
-inline bool few_rows(const PromptArgs &a, int h) {
+inline bool few_rows(const PromptArgs &a) {
+    constexpr Few kFew = few_blocks<T, D, PASS>();
+    const int h = PASS == Pass::kKeys ? a.Hkv : a.Hq;
     const long long len = a.T_total > a.B ? a.T_total / a.B : 1, w = a.window;
     const bool windowed = w > 0 && w < len;
     const long long blocks = (a.cu ? (a.T_total + 31LL) / 32 + a.B / 2 : a.B * ((len + 31) / 32)) * h;
     const long long top = windowed && w + 128 < len ? w + 128 : len;
     const long long mean = windowed ? 2 * w - w * w / len + 32 : len;      // (twice)
+    const long long loop = PASS == Pass::kKeys ? top * a.G : top;
+    const int step = (loop >= 384) + (loop >= 1024) + (loop >= 2048) + (loop >= 4096);
     // (mean / top is over 1 / 4, so that a call taken is far from filling a launch)
-    const int step = (top >= 384) + (top >= 1024) + (top >= 2048) + (top >= 4096);
-    return blocks * mean <= 4 * top * kFew<T, D, PASS>.blocks[step];
+    return blocks * mean * (a.cu ? 7 : 8) <= 32 * top * kFew.blocks[step];
 }
 
 // The query head of workgroup number u of a block's Hq: workgroups go to the

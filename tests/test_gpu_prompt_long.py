@@ -62,7 +62,7 @@ def test_packed(dt, D, Hkv, G, window):
 
 @pytest.mark.parametrize("dt", ["fp32", "bf16"])
 @pytest.mark.parametrize("B,T,D,Hkv,G,window", [
-    (40, 40, 128, 16, 1, 0), (3, 130, 64, 70, 3, 0), (2, 257, 128, 70, 1, 0), (1, 700, 64, 70, 2, 0),
+    (40, 40, 128, 16, 1, 0), (3, 130, 64, 100, 3, 0), (2, 257, 128, 70, 1, 0), (1, 700, 64, 100, 2, 0),
     (1, 650, 128, 70, 1, 300), (2, 300, 64, 100, 1, 31), (1, 2100, 128, 36, 1, 0),
     (2, 1100, 64, 40, 1, 0), (1, 2100, 64, 48, 1, 700), (1, 4200, 128, 20, 1, 3000)])
 def test_fixed(dt, B, T, D, Hkv, G, window):
@@ -145,3 +145,28 @@ def test_graph(packed):
             base.sync()
             for x, y in zip([o, lse] + grads, eager[i]):
                 assert same(x.view(y.shape), y)
+
+
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_past_2_32_bytes(dt, packed):
+    """Tensors of 2.2e9 elements: the first sequence and the last ones."""
+    B, T, H, D, dtype = 2100, 130, 64, 128, DTYPES[dt]
+    g = torch.Generator(DEV).manual_seed(1)
+    shape = (B * T, H, D) if packed else (B, T, H, D)
+    q, k, v, do = (torch.randn(shape, generator=g, device=DEV, dtype=dtype) for _ in range(4))
+    offs = base.i32(range(0, B * T + 1, T)) if packed else None
+    o, lse = gdr.attention_prefill(q, k, v, cu_seqlens=offs, lse=True)
+    grads = gdr.attention_backward(q, k, v, o, lse, do, cu_seqlens=offs)
+    base.sync()
+    for b in (0, B - 2, B - 1):
+        rows, heads = slice(b * T, (b + 1) * T), [0, H - 1]
+        cut = lambda x: x.view(B * T, *x.shape[-2:])[rows][:, heads].cpu()  # noqa: E731
+        qs, ks, vs, os, ds = (cut(x) for x in (q, k, v, o, do))
+        ls = lse.view(B * T, H)[rows][:, heads].cpu()
+        want = ref.forward(qs, ks, vs, [0, T], D ** -0.5)
+        within("o", os, want[0], want[2])
+        within("lse", ls, want[1], want[3])
+        want, bound = ref.backward(qs, ks, vs, os, ls, ds, [0, T], D ** -0.5)
+        for name, x, y, z in zip(("dq", "dk", "dv"), grads, want, bound):
+            within(name, cut(x), y, z)
