@@ -66,9 +66,11 @@ struct Own {
     __device__ static inline void read() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 };
 
-// One output row's channels 4 x .. of the waves' sums, joined: y = sum f_w s_w.
+// One output row's channels 4 x .. of the waves' sums, joined: y = sum f_w s_w, each
+// product rounded.
 template <int D>
 __device__ inline f32x4 join4(const char *lds, int stride, int row, int d, const float *f) {
+#pragma clang fp contract(off)
     f32x4 y{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -213,6 +215,7 @@ __global__ __launch_bounds__(kThreads, 1) void prompt_kernel(KArgs k) {
     const float ms = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int u = 0; u < kWaves; ++u) {
+#pragma clang fp contract(off)
         f[u] = exp2_((sm[u][row] - ms) * k.c);
         sum += sl[u][row] * f[u];
     }
