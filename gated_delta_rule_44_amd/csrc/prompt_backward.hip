@@ -20,6 +20,8 @@
 // 28 %: of 64 channels the exponentials and what is done to ds take as long as the
 // products, and a sixth of what a wave's tiles hold is masked.  fp32 has a kernel for
 // the keys that is one wave a SIMD (its accumulators fill the registers).
+//   key_pairs_kernel<128, 4> spills 36 registers (100 bytes a lane): some 38 MB of the
+// 105 MB that the first case is seen to write; one tile loop loads five of them again.
 #include "prompt_internal.h"
 
 namespace gdr {

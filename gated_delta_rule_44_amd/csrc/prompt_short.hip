@@ -10,7 +10,8 @@
 // needs it, not the card's rates.  (One prompt of 301 tokens, 16 heads over 4 of
 // 128 in bf16: 9.0 us, 10.5 in blocks of 128; the gradients of 2 x 150 tokens, 4
 // heads over 2 of 64 in fp32: 34.5 us, 13.8 and 21.1, for 79.)  few_rows says
-// where it is taken, with both sides measured.
+// where it is taken, with both sides measured.  key_kernel<float, 128> spills 38 of its
+// 512 registers.
 #include "prompt_internal.h"
 
 namespace gdr {
