@@ -149,3 +149,39 @@ def test_round_with_too_few_pages(dt):
                 both[0][p, :, s], both[1][p, :, s] = k[b, t], v[b, t]
     some = [b for b in range(B) if served[b]]
     check_some(o, q, *both, full, [l + n for l in lens], parents, 0.125, some, "served")
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G,wide", [(1, 1, 0), (8, 2, 0), (24, 1, 1), (20, 2, 1), (24, 4, 1), (64, 2, 1)])
+def test_nan_that_a_row_attends_to(dt, D, n, G, wide):
+    """NaN queries give NaN, in their rows only, and so do NaN keys, though they be all
+    that a wave or a slot of a sequence sees; in trees and in the decode."""
+    lens, page, Hkv = [2600, 300], 16, 2
+    kc, vc, _, table = make_cache(lens, Hkv, D, page, dt, seed=D + n,
+                                  extra=wide * ((160 << 10) // (Hkv * page) + 100))
+    q = queries(2, n, Hkv * G, D, dt, seed=n)
+    parents = trees(2, n, seed=2)
+    chain = np.tile(np.arange(n) - 1, (2, 1)).astype(np.int32)
+
+    def both(q, kc):
+        args = (q.to(DEV), kc.to(DEV), vc.to(DEV), i32(table), i32(lens))
+        out = [gdr.attention_tree(*args, i32(parents)), gdr.attention_tree(*args, i32(chain)),
+               gdr.attention_decode(*args)]
+        sync()
+        return out
+
+    clean = both(q, kc)
+    mine = q.clone()
+    mine[0, n - 1, 1, 3] = float("nan")
+    for o, c in zip(both(mine, kc), clean):
+        assert bool(torch.isnan(o[0, n - 1, 1]).all())
+        o[0, n - 1, 1] = c[0, n - 1, 1]
+        assert same(o, c)
+    for places in (range(640, 1920), range(512, 1152), range(0, 128), range(2400, 2432)):
+        mine = kc.clone()
+        for j in places:
+            mine[table[0, j // page], 0, j % page, 5] = float("nan")
+        for o, c in zip(both(q, mine), clean):
+            assert bool(torch.isnan(o[0, :, :G]).all()), places
+            assert same(o[0, :, G:], c[0, :, G:]) and same(o[1], c[1]), places
